@@ -14,57 +14,14 @@
 #include <mutex>
 #include <new>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "kernels.h"
+#include "plan.h"
 
 using namespace gemmlib;
 
-struct gemm_plan {
-  int device = 0;
-  gemm_dtype_t ab = GEMM_F16;
-  gemm_dtype_t c = GEMM_F32;
-  int sm_count = 0;
-  int32_t* d_err = nullptr;          // device error word
-  void* ws = nullptr;                // int8 staging: fp16 copies of A and B
-  size_t ws_bytes = 0;
-  void* stage = nullptr;             // gemm_run_host device buffers
-  size_t stage_bytes = 0;
-  gemm_kernel_t forced = GEMM_KERNEL_AUTO;
-  int pair_clusters = 0;             // co-resident CTA-pair clusters (0: pair kernel unavailable)
-  void* sk_ws = nullptr;             // stream-K partial accumulators and flags (per cluster and CTA)
-  size_t sk_ws_bytes = 0;
-  int32_t sk_epoch = 0;
-  // Stream-K of the single-CTA kernel: two fp32 partial slots per CTA, then one
-  // arrival counter per tile (zero between launches; each tile's last arriver
-  // resets its counter).
-  void* sk1_ws = nullptr;
-  size_t sk1_ws_bytes = 0;
-  gemm_config_t last{};
-  uint64_t timeout_ns = 4000000000ull;
-  // gemm_run_host's row-panel pipeline: copy-in and copy-out streams and the
-  // events that order them with the caller's stream (created on first use).
-  cudaStream_t host_in = nullptr, host_out = nullptr;
-  cudaEvent_t host_ev[36] = {};
-  bool host_pipe = false;
-};
-
-namespace {
-
-constexpr int64_t kMaxDim = 0x7fffffffLL;   // tile indices and TMA coordinates are 32-bit
-constexpr int kHostMaxPanels = 16;           // gemm_run_host: most row panels of its copy pipeline
-
-// NVTX range around a public entry point (a profiler's timeline shows each call;
-// without a tool attached a push or pop costs a predictable branch).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
+namespace gemmlib {
 
 // GEMM_LOG=1: every launch prints the configuration it runs to stderr.
-bool log_enabled() {
+static bool log_enabled() {
   static const bool on = [] {
     const char* v = std::getenv("GEMM_LOG");
     return v != nullptr && std::atoi(v) != 0;
@@ -72,7 +29,7 @@ bool log_enabled() {
   return on;
 }
 
-const char* kernel_label(int k) {
+static const char* kernel_label(int k) {
   switch (k) {
     case GEMM_KERNEL_NONE: return "none";
     case GEMM_KERNEL_TC: return "tc";
@@ -95,8 +52,57 @@ void log_config(const char* entry, int64_t M, int64_t N, int64_t K, int64_t batc
                c.xf_staged);
 }
 
-bool is_f16ish(int t) { return t == GEMM_F16 || t == GEMM_BF16; }
-bool is_float_out(int t) { return t == GEMM_F32 || t == GEMM_F16 || t == GEMM_BF16; }
+gemm_status_t ensure_ws(gemm_plan* plan, size_t bytes, cudaStream_t stream) {
+  if (plan->ws_bytes >= bytes) return GEMM_OK;
+  if (plan->ws) {
+    cudaFreeAsync(plan->ws, stream);
+    plan->ws = nullptr;
+    plan->ws_bytes = 0;
+  }
+  void* p = nullptr;
+  if (cudaMallocAsync(&p, bytes, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  plan->ws = p;
+  plan->ws_bytes = bytes;
+  return GEMM_OK;
+}
+
+static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+static std::once_flag g_encode_once;
+
+static bool encode_fn() {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_encode != nullptr;
+}
+
+bool encode_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
+               uint64_t ld, uint64_t nbatch, uint64_t bstride, uint32_t box_inner, uint32_t box_outer) {
+  if (!encode_fn()) return false;
+  if (nbatch <= 1) {
+    nbatch = 1;
+    bstride = (ld * outer + 7) / 8 * 8;   // unused; any 16-byte multiple past the problem
+  }
+  cuuint64_t dims[3] = {inner, outer, nbatch};
+  cuuint64_t strides[2] = {ld * 2, bstride * 2};
+  cuuint32_t box[3] = {box_inner, box_outer, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(tm, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+}  // namespace gemmlib
+
+namespace {
+
+constexpr int kHostMaxPanels = 16;           // gemm_run_host: most row panels of its copy pipeline
 
 gemm_status_t check_types(gemm_dtype_t ab, gemm_dtype_t c) {
   switch (ab) {
@@ -106,13 +112,6 @@ gemm_status_t check_types(gemm_dtype_t ab, gemm_dtype_t c) {
     case GEMM_F32: return c == GEMM_F32 ? GEMM_OK : GEMM_ERR_INVALID_ARG;
     default: return GEMM_ERR_INVALID_ARG;
   }
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Can TMA describe this operand (16-byte aligned base, 16-byte multiple row pitch)?
-bool tma_ok(const void* p, int64_t ld, int esize) {
-  return aligned16(p) && ((ld * esize) % 16) == 0 && ld * esize < (int64_t(1) << 40);
 }
 
 // Storage extent (elements) of a rows x cols logical matrix in a layout.
@@ -457,68 +456,10 @@ gemm_status_t select_config(gemm_dtype_t ab, gemm_dtype_t c, gemm_layout_t la, g
 
 // --------------------------- TMA tensor maps -------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-bool encode_fn() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode != nullptr;
-}
-
-// A row-pitched tensor of 16-bit elements (inner elements contiguous, `ld`
-// elements between rows of the outer dimension) with a third, outermost
-// dimension: `nbatch` problems `bstride` elements apart (one problem when
-// nbatch == 1).  128-byte swizzle; out-of-bounds elements read as zero.
-bool encode_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
-               uint64_t ld, uint64_t nbatch, uint64_t bstride, uint32_t box_inner, uint32_t box_outer) {
-  if (!encode_fn()) return false;
-  if (nbatch <= 1) {
-    nbatch = 1;
-    bstride = (ld * outer + 7) / 8 * 8;   // unused; any 16-byte multiple past the problem
-  }
-  cuuint64_t dims[3] = {inner, outer, nbatch};
-  cuuint64_t strides[2] = {ld * 2, bstride * 2};
-  cuuint32_t box[3] = {box_inner, box_outer, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = g_encode(tm, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 // A strided batch of independent problems (count 1: one problem).
 struct Batch {
   int64_t count = 1;
   int64_t sa = 0, sb = 0, sc = 0, sd = 0, sbias = 0;   // element strides (0: shared by all)
-};
-
-// tcgen05 instruction descriptor, kind::f16 with fp32 accumulation:
-//   bits 4-5 D format (1 = f32), 7-9 A format, 10-12 B format (0 = f16, 1 = bf16),
-//   15 / 16 A / B MN-major, 17-22 N >> 3, 24-28 M >> 4.
-uint32_t make_idesc(bool bf16, int bn, bool a_mn_major, bool b_mn_major, int bm = TC_BM) {
-  const uint32_t f = bf16 ? 1u : 0u;
-  return (1u << 4) | (f << 7) | (f << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
-         ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(bm >> 4) << 24);
-}
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
 };
 
 EpiParams make_epi(const gemm_plan* plan, double alpha, double beta, const void* C, int64_t ldc, void* D,
@@ -588,22 +529,6 @@ bool xf_any(const gemm_epilogue_t* epi) {
   const LoadXf x = make_xf(GEMM_F16, epi);
   return x.a_on || x.b_on;
 }
-
-gemm_status_t ensure_ws(gemm_plan* plan, size_t bytes, cudaStream_t stream) {
-  if (plan->ws_bytes >= bytes) return GEMM_OK;
-  if (plan->ws) {
-    cudaFreeAsync(plan->ws, stream);
-    plan->ws = nullptr;
-    plan->ws_bytes = 0;
-  }
-  void* p = nullptr;
-  if (cudaMallocAsync(&p, bytes, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-  plan->ws = p;
-  plan->ws_bytes = bytes;
-  return GEMM_OK;
-}
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 gemm_status_t launch_tc_problem(gemm_plan* plan, const gemm_config_t& cfg, gemm_layout_t la, gemm_layout_t lb,
                                 int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
@@ -1459,6 +1384,27 @@ gemm_status_t gemm_run_host(gemm_plan_t plan, gemm_layout_t la, gemm_layout_t lb
 }
 
 }  // extern "C"
+
+gemm_status_t gemmlib::run_product(gemm_plan* plan, gemm_dtype_t ab, gemm_dtype_t c, gemm_dtype_t out, gemm_layout_t la,
+                                   gemm_layout_t lb, int64_t M, int64_t N, int64_t K, double alpha, const void* A,
+                                   int64_t lda, int64_t stride_a, const void* B, int64_t ldb, int64_t stride_b,
+                                   double beta, const void* C, int64_t ldc, int64_t stride_c, void* D, int64_t ldd,
+                                   int64_t stride_d, int64_t batch, gemm_stream_t stream) {
+  const gemm_dtype_t plan_ab = plan->ab, plan_c = plan->c;
+  const gemm_kernel_t forced = plan->forced;
+  plan->ab = ab;
+  plan->c = c;
+  plan->forced = GEMM_KERNEL_AUTO;
+  gemm_epilogue_t epi{};
+  epi.out_dtype = out;
+  const gemm_status_t s =
+      gemm_run_strided_batched(plan, la, lb, M, N, K, alpha, A, lda, stride_a, B, ldb, stride_b, beta, C, ldc, stride_c,
+                               D, ldd, stride_d, batch, &epi, 0, stream);
+  plan->ab = plan_ab;
+  plan->c = plan_c;
+  plan->forced = forced;
+  return s;
+}
 
 // ===========================================================================
 // gemm_run_s8_noalloc: the int8 path with its fp16 staging in a fixed device

@@ -1,0 +1,108 @@
+// plan.h -- the plan's state and the host helpers that the entry points share (internal).
+#pragma once
+
+#include <cstdint>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "kernels.h"
+
+struct gemm_plan {
+  int device = 0;
+  gemm_dtype_t ab = GEMM_F16;
+  gemm_dtype_t c = GEMM_F32;
+  int sm_count = 0;
+  int32_t* d_err = nullptr;          // device error word
+  void* ws = nullptr;                // int8 staging: fp16 copies of A and B
+  size_t ws_bytes = 0;
+  void* stage = nullptr;             // gemm_run_host device buffers
+  size_t stage_bytes = 0;
+  gemm_kernel_t forced = GEMM_KERNEL_AUTO;
+  int pair_clusters = 0;             // co-resident CTA-pair clusters (0: pair kernel unavailable)
+  void* sk_ws = nullptr;             // stream-K partial accumulators and flags (per cluster and CTA)
+  size_t sk_ws_bytes = 0;
+  int32_t sk_epoch = 0;
+  // Stream-K of the single-CTA kernel: two fp32 partial slots per CTA, then one
+  // arrival counter per tile (zero between launches; each tile's last arriver
+  // resets its counter).
+  void* sk1_ws = nullptr;
+  size_t sk1_ws_bytes = 0;
+  gemm_config_t last{};
+  uint64_t timeout_ns = 4000000000ull;
+  // gemm_run_host's row-panel pipeline: copy-in and copy-out streams and the
+  // events that order them with the caller's stream (created on first use).
+  cudaStream_t host_in = nullptr, host_out = nullptr;
+  cudaEvent_t host_ev[36] = {};
+  bool host_pipe = false;
+};
+
+namespace gemmlib {
+
+constexpr int64_t kMaxDim = 0x7fffffffLL;   // tile indices and TMA coordinates are 32-bit
+
+// NVTX range around a public entry point (a profiler's timeline shows each call;
+// without a tool attached a push or pop costs a predictable branch).
+struct NvtxRange {
+  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+  ~NvtxRange() { nvtxRangePop(); }
+  NvtxRange(const NvtxRange&) = delete;
+  NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+inline bool is_f16ish(int t) { return t == GEMM_F16 || t == GEMM_BF16; }
+inline bool is_float_out(int t) { return t == GEMM_F32 || t == GEMM_F16 || t == GEMM_BF16; }
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Can TMA describe this operand (16-byte aligned base, 16-byte multiple row pitch)?
+inline bool tma_ok(const void* p, int64_t ld, int esize) {
+  return aligned16(p) && ((ld * esize) % 16) == 0 && ld * esize < (int64_t(1) << 40);
+}
+
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// tcgen05 instruction descriptor, kind::f16 with fp32 accumulation:
+//   bits 4-5 D format (1 = f32), 7-9 A format, 10-12 B format (0 = f16, 1 = bf16),
+//   15 / 16 A / B MN-major, 17-22 N >> 3, 24-28 M >> 4.
+inline uint32_t make_idesc(bool bf16, int bn, bool a_mn_major, bool b_mn_major, int bm = TC_BM) {
+  const uint32_t f = bf16 ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(bm >> 4) << 24);
+}
+
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = true;
+  explicit DeviceGuard(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
+    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
+  }
+  ~DeviceGuard() {
+    int cur = -1;
+    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+  }
+};
+
+// GEMM_LOG=1: print the configuration of a launch to stderr.
+void log_config(const char* entry, int64_t M, int64_t N, int64_t K, int64_t batch, const gemm_config_t& c);
+
+// Grow the plan's scratch (ws) to at least `bytes`, in stream order.
+gemm_status_t ensure_ws(gemm_plan* plan, size_t bytes, cudaStream_t stream);
+
+// A strided batch of products for an operator that is built of them: D = alpha *
+// op(A) * op(B) + beta * C on the kernels of gemm_run, with operand types of its
+// own (`ab`, `c`, `out`) in place of the plan's.
+gemm_status_t run_product(gemm_plan* plan, gemm_dtype_t ab, gemm_dtype_t c, gemm_dtype_t out, gemm_layout_t la,
+                          gemm_layout_t lb, int64_t M, int64_t N, int64_t K, double alpha, const void* A, int64_t lda,
+                          int64_t stride_a, const void* B, int64_t ldb, int64_t stride_b, double beta, const void* C,
+                          int64_t ldc, int64_t stride_c, void* D, int64_t ldd, int64_t stride_d, int64_t batch,
+                          gemm_stream_t stream);
+
+// A row-pitched tensor of 16-bit elements (inner elements contiguous, `ld`
+// elements between rows of the outer dimension) with a third, outermost
+// dimension: `nbatch` problems `bstride` elements apart (one problem when
+// nbatch == 1).  128-byte swizzle; out-of-bounds elements read as zero.
+bool encode_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
+               uint64_t ld, uint64_t nbatch, uint64_t bstride, uint32_t box_inner, uint32_t box_outer);
+
+}  // namespace gemmlib

@@ -399,7 +399,9 @@ const char* gemm_status_string(gemm_status_t status);
  * gemm_run_strided_batched, gemm_run_diag, gemm_run_complex, gemm_config_t.cluster,
  * gemm_epilogue_t.out_scale and int8 D, gemm_config_t.half_tiles,
  * gemm_noalloc_device_status and gemm_noalloc_set_timeout, the operand
- * transforms gemm_epilogue_t.load_xf / a_act / a_scale / b_act / b_scale). */
+ * transforms gemm_epilogue_t.load_xf / a_act / a_scale / b_act / b_scale).  Entry
+ * points that are added without a change to an older one or to a struct (the
+ * expert-layer operators below) leave it as it is. */
 int gemm_abi_version(void);
 
 /* ---------------------------------------------------------------------------
@@ -462,6 +464,112 @@ gemm_status_t gemm_noalloc_device_status(int32_t* code, gemm_stream_t stream);
  * that runs past it records GEMM_ERR_TIMEOUT and its CTA winds down, as for
  * gemm_plan_set_timeout.  The paper has no counterpart. */
 gemm_status_t gemm_noalloc_set_timeout(uint64_t timeout_ns);
+
+/* ===========================================================================
+ * Expert layers: products grouped by expert, products with 4-bit weights, and
+ * the orthogonalised update of weight matrices.  No page has a counterpart;
+ * they are operators of large language models built on this library's
+ * products.  They use the plan's device, error word and scratch as gemm_run
+ * does, are asynchronous on `stream`, and read the group offsets on the device:
+ * the host never waits for them.
+ *
+ * Groups.  Rows offsets[g] .. offsets[g+1]-1 of a buffer belong to group g (an
+ * expert's tokens, after sorting by expert).  `offsets` is a device array of
+ * groups + 1 int32 that does not decrease and stays within the buffer; a group
+ * may be empty, and rows before the first or after the last offset belong to
+ * none (they are neither read nor written).  At most 1024 groups
+ * (GEMM_ERR_UNSUPPORTED).  Offsets that break the rule are clamped to the buffer
+ * (no access leaves it; the affected results are undefined) and
+ * gemm_plan_device_status then reports GEMM_ERR_INVALID_ARG.
+ * ======================================================================== */
+
+/* ---------------------------------------------------------------------------
+ * gemm_run_grouped -- every row times its group's matrix:
+ *     D[r, :] = act( alpha * A[r, :] * op(B_g) + bias_g ),   r in group g,
+ * the forward product of an expert layer (op(B_g) = W_g) and its input gradient
+ * (A = dY, op(B_g) = W_g transposed: the same W with the other layout letter).
+ *   plan        ab_dtype F16 or BF16 (else GEMM_ERR_UNSUPPORTED).
+ *   layoutB     layout of each B_g (K x N), as for gemm_run.
+ *   M           rows of A and D (the buffer's, not a group's).
+ *   A, lda      row-major M x K.
+ *   B, ldb      B_g = B + g * stride_b elements (stride_b 0: one matrix for all).
+ *   D, ldd      row-major M x N.
+ *   epi         bias: N entries per group (GEMM_BIAS_COL; group g's at
+ *               g * stride_bias elements), act, out_dtype.  NULL: none, out_dtype
+ *               c_dtype.  GEMM_BIAS_ROW and load_xf are GEMM_ERR_UNSUPPORTED.
+ * K == 0 gives D = act(bias).  D must not overlap A.
+ * ------------------------------------------------------------------------- */
+gemm_status_t gemm_run_grouped(gemm_plan_t plan, gemm_layout_t layoutB, int64_t groups, int64_t M, int64_t N,
+                               int64_t K, double alpha, const void* A, int64_t lda, const void* B, int64_t ldb,
+                               int64_t stride_b, void* D, int64_t ldd, const int32_t* offsets,
+                               const gemm_epilogue_t* epi, int64_t stride_bias, gemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gemm_run_grouped_wgrad -- the weight gradient of gemm_run_grouped:
+ *     D_g = alpha * sum over rows r of group g of A[r, :]' * B[r, :] + beta * C_g
+ * (A = X, B = dY: D_g = dW_g).  An empty group gives D_g = beta * C_g.
+ *   M, N        columns of A and of B: D_g is M x N.     K   rows of A and B.
+ *   A, lda      row-major K x M.       B, ldb   row-major K x N.
+ *   C, D        row-major, stride_c / stride_d elements from group to group; C
+ *               has the plan's c_dtype and is read when beta != 0 (C == D with
+ *               equal strides and types accumulates in place).
+ *   out_dtype   type of D: F32, F16 or BF16.
+ * ------------------------------------------------------------------------- */
+gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N, int64_t K,
+                                     double alpha, const void* A, int64_t lda, const void* B, int64_t ldb,
+                                     double beta, const void* C, int64_t ldc, int64_t stride_c, void* D,
+                                     int64_t ldd, int64_t stride_d, const int32_t* offsets,
+                                     gemm_dtype_t out_dtype, gemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gemm_run_q4 -- products with 4-bit weights that have one scale (and zero
+ * point) per output column and group of K:
+ *     D[r, n] = act( alpha * sum_k A[r, k] * w[n, k] + bias[n] ),
+ *     w[n, k] = scale[n, k / group_size] * (q[n, k] - zero[n, k / group_size]).
+ * Any number of rows: one token (each weight is read once) up to a prompt.
+ * With `offsets`, row r uses the weights, scales, zeros and bias of its group
+ * (experts); NULL with groups == 1 is a dense layer.
+ *   plan        ab_dtype F16 or BF16: the type of A (else GEMM_ERR_UNSUPPORTED).
+ *   M, N, K     rows of A and D, output columns, depth.
+ *   D, epi, stride_bias   as for gemm_run_grouped.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const void* values;       /* per column n: ceil(K/2) bytes, the even k in the low four bits */
+    int64_t ld_values;        /* bytes from column to column, >= ceil(K/2) */
+    int64_t stride_values;    /* bytes from group to group */
+    const void* scales;       /* per column: ceil(K / group_size) entries */
+    gemm_dtype_t scale_dtype; /* F32, F16 or BF16 */
+    int64_t ld_scales;        /* entries from column to column */
+    int64_t stride_scales;    /* entries from group to group */
+    const uint8_t* zeros;     /* per column: ceil(K / group_size) bytes, each 0..15 (the low four bits count);
+                                 NULL: 8 everywhere */
+    int64_t ld_zeros, stride_zeros;
+    int64_t group_size;       /* a positive multiple of 32 */
+} gemm_q4_t;
+
+gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N, int64_t K, double alpha,
+                          const void* A, int64_t lda, const gemm_q4_t* B, void* D, int64_t ldd,
+                          const int32_t* offsets, const gemm_epilogue_t* epi, int64_t stride_bias,
+                          gemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gemm_orthogonalize -- Newton-Schulz steps towards the nearest matrix with
+ * orthonormal rows or columns, for `batch` matrices:
+ *     X = G / (||G||_F + eps);   `steps` times:  X = a X + (b X X' + c (X X')^2) X;
+ *     D = X
+ * with coeffs = {a, b, c} (the orthogonalised update of a weight matrix).
+ *   plan        ab_dtype: the type of G (F32, F16 or BF16).
+ *   G, ldg      row-major M x N (M > N runs on the transpose), stride_g elements
+ *               from matrix to matrix (0: one matrix for all).
+ *   D, ldd      row-major, out_dtype F32, F16 or BF16.
+ * X is held in fp16 between the products (times a power of two that keeps it out
+ * of the subnormals); sums are fp32.  A zero matrix gives zero; NaN or infinity
+ * anywhere in a matrix makes that whole result NaN.
+ * ------------------------------------------------------------------------- */
+gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int64_t N, int steps,
+                                 const double* coeffs, double eps, const void* G, int64_t ldg, int64_t stride_g,
+                                 void* D, int64_t ldd, int64_t stride_d, gemm_dtype_t out_dtype,
+                                 gemm_stream_t stream);
 
 #ifdef __cplusplus
 }

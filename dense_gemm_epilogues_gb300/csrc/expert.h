@@ -30,33 +30,55 @@ __device__ __forceinline__ void group_range(const Groups& g, int e, int& lo, int
   hi = min(max(b, lo), g.rows);
   if (lo != a || hi != b) atomicCAS(g.err, 0, (int32_t)GEMM_ERR_INVALID_ARG);
 }
+
+// f(type tag) for an output type: f's argument has it as a constant `value`.
+template <int V>
+struct TypeTag {
+  static constexpr int value = V;
+};
+template <typename F>
+__device__ __forceinline__ void with_type(int dtype, F&& f) {
+  if (dtype == GEMM_F32) f(TypeTag<GEMM_F32>{});
+  else if (dtype == GEMM_F16) f(TypeTag<GEMM_F16>{});
+  else f(TypeTag<GEMM_BF16>{});
+}
+
+// Order this thread's use of a tensor map after its making by another kernel.
+__device__ __forceinline__ void tensormap_acquire(const CUtensorMap* tm) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(tm) : "memory");
+}
 #endif
 
-// D[r, :] = act(alpha * A[r, :] * op(B_g) + bias_g) for the rows r of each group g.
-struct GroupedParams {
-  Groups g;
-  const void* A;                 // rows x K, row-major
-  int64_t lda;
-  const void* B;                 // per group: element (k, n) at k * b_k + n * b_n
-  int64_t b_k, b_n, stride_b;
-  int32_t N, K;
-  int32_t ab_dtype;
-  EpiParams epi;                 // D: rows x N; bias: stride_bias elements from group to group
+// What seg_kernel.cu computes (its head says how).
+enum { SEG_TOKENS = 0, SEG_WGRAD = 1, SEG_SYM = 2, SEG_DENSE = 3 };
+struct SegParams {
+  CUtensorMap tmA;              // M side (WGRAD: the template of every group's map)
+  CUtensorMap tmB[5];           // N side; TOKENS: boxes of 128, 64, 32, 16 and 8 rows
+  Groups groups;                // TOKENS, WGRAD
+  const CUtensorMap* group_maps;   // WGRAD: two per group, made by launch_wgrad_maps
+  uint64_t a_base, b_base;      // WGRAD: the operands' addresses and row pitches in bytes
+  uint64_t a_pitch, b_pitch;
+  int64_t M;                    // rows of the M side
+  int32_t N, K;                 // rows of the N side and depth (what the groups do not give)
+  int32_t tiles_m, tiles_n;     // 128- or 256-wide tiles
+  int32_t tiles_per_group, num_tiles;
+  int32_t a_batched;            // TOKENS: the M side has one slice per group
+  int32_t store_t;              // DENSE: store D transposed
+  uint32_t idesc;               // instruction descriptor without N
+  float shift;                  // SYM: subtracted on the diagonal
+  EpiParams epi;
+  int32_t* err;
+  uint64_t timeout_ns;
 };
-cudaError_t launch_grouped(const GroupedParams& p, cudaStream_t stream);
+// workers: CTAs (cg 1) or CTA pairs (cg 2).
+cudaError_t launch_seg(const SegParams& p, int mode, int cg, bool a_mn, int workers, cudaStream_t stream);
+cudaError_t launch_wgrad_maps(const SegParams& p, CUtensorMap* maps, cudaStream_t stream);
 
-// D_g = alpha * A_g' * B_g + beta * C_g over the rows of each group g (A: rows x M, B: rows x N).
-struct WgradParams {
-  Groups g;
-  const void* A;
-  int64_t lda;
-  const void* B;
-  int64_t ldb;
-  int32_t M, N;
-  int32_t ab_dtype;
-  EpiParams epi;                 // C, D: M x N per group, stride_c / stride_d from group to group
-};
-cudaError_t launch_wgrad(const WgradParams& p, cudaStream_t stream);
+// dst[z][r][c] = src[z][r][c] for 16-bit elements with a pitch that TMA can address
+// (ldd a multiple of 8; columns up to ldd are zero).  offsets != null: the z-th matrix
+// is skipped when group z has no rows.
+cudaError_t launch_repitch(const void* src, int64_t ld, int64_t stride, void* dst, int64_t ldd, int64_t stride_d,
+                           int64_t rows, int64_t cols, int64_t batch, const int32_t* offsets, cudaStream_t stream);
 
 // D[r, n] = act(alpha * sum_k A[r, k] * scale[n, k / group] * (q[n, k] - zero[n, k / group]) + bias[n])
 // with the q, scales and zeros of the row's group.

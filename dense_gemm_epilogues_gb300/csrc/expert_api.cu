@@ -2,6 +2,7 @@
 // include/gemm.h): argument checks, workspaces and launches.  Host code only.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "expert.h"
@@ -39,6 +40,65 @@ EpiParams epilogue_of(const gemm_epilogue_t* epi, gemm_dtype_t out, double alpha
   return e;
 }
 
+// A 16-bit operand as TMA can read it: itself, or a copy with another pitch in scratch.
+struct Operand {
+  const void* p;
+  int64_t ld, stride;
+};
+
+bool addressable(const Operand& x, int64_t batch) {
+  return tma_ok(x.p, x.ld, 2) && (batch <= 1 || x.stride % 8 == 0);
+}
+
+// Scratch bytes of the copy of `batch` rows x cols matrices (0: none needed).
+size_t repitch_bytes(const Operand& x, int64_t rows, int64_t cols, int64_t batch) {
+  return addressable(x, batch) ? 0 : align_up((size_t)(batch * rows * ((cols + 7) / 8 * 8)) * 2, 256);
+}
+
+gemm_status_t repitch(Operand* x, int64_t rows, int64_t cols, int64_t batch, const int32_t* offsets, char* to,
+                      cudaStream_t stream) {
+  if (addressable(*x, batch)) return GEMM_OK;
+  const int64_t ld = (cols + 7) / 8 * 8;
+  if (launch_repitch(x->p, x->ld, x->stride, to, ld, rows * ld, rows, cols, batch, offsets, stream) != cudaSuccess)
+    return GEMM_ERR_CUDA;
+  *x = Operand{to, ld, rows * ld};
+  return GEMM_OK;
+}
+
+// CTAs per tile of a grouped product (GEMM_GROUPED_CG=1 or 2 fixes it).
+int grouped_cg(const gemm_plan* plan, int rule) {
+  if (const char* env = std::getenv("GEMM_GROUPED_CG")) {
+    const int v = std::atoi(env);
+    if (v == 1 || (v == 2 && plan->pair_clusters > 0)) return v;
+  }
+  return plan->pair_clusters > 0 ? rule : 1;
+}
+
+int workers_of(const gemm_plan* plan, int cg, int64_t tiles) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(tiles, cg == 2 ? plan->pair_clusters : plan->sm_count));
+}
+
+CUtensorMapDataType map_type(gemm_dtype_t t) {
+  return t == GEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+constexpr int64_t kMaxTiles = int64_t(1) << 28;   // tile numbers are 32-bit
+
+// What gemm_plan_last_config reports for a product on seg_kernel.
+gemm_config_t seg_config(int cg, int64_t tiles, int workers) {
+  gemm_config_t c{};
+  c.kernel = cg == 2 ? GEMM_KERNEL_TC_PAIR : GEMM_KERNEL_TC;
+  c.bm = c.bn = 128 * cg;
+  c.bk = 2 * TC_BK;
+  c.stages = 3;
+  c.cta_group = c.cluster = cg;
+  c.split_k = 1;
+  c.raster = 8;
+  c.grid = workers * cg;
+  c.tiles = (int32_t)tiles;
+  return c;
+}
+
 bool too_large(std::initializer_list<int64_t> dims) {
   for (int64_t d : dims)
     if (d > kMaxDim - 512) return true;   // tile edges past a size stay within 32 bits
@@ -52,7 +112,7 @@ extern "C" {
 gemm_status_t gemm_run_grouped(gemm_plan_t plan, gemm_layout_t lb, int64_t groups, int64_t M, int64_t N, int64_t K,
                                double alpha, const void* A, int64_t lda, const void* B, int64_t ldb, int64_t stride_b,
                                void* D, int64_t ldd, const int32_t* offsets, const gemm_epilogue_t* epi,
-                               int64_t stride_bias, gemm_stream_t stream) {
+                               int64_t stride_bias, gemm_stream_t stream_) {
   if (!plan) return GEMM_ERR_INVALID_ARG;
   NvtxRange range("gemm_run_grouped");
   if (!is_f16ish(plan->ab)) return GEMM_ERR_UNSUPPORTED;
@@ -67,27 +127,53 @@ gemm_status_t gemm_run_grouped(gemm_plan_t plan, gemm_layout_t lb, int64_t group
   if (K > 0 && (!A || !B || lda < K || ldb < (lb == GEMM_OP_N ? K : N))) return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
-  GroupedParams p{};
-  p.g = Groups{offsets, (int32_t)groups, (int32_t)M, plan->d_err};
-  p.A = A;
-  p.lda = lda;
-  p.B = B;
-  p.b_k = lb == GEMM_OP_N ? 1 : ldb;
-  p.b_n = lb == GEMM_OP_N ? ldb : 1;
-  p.stride_b = stride_b;
-  p.N = (int32_t)N;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const bool a_mn = lb == GEMM_OP_T;
+  const int64_t brows = a_mn ? K : N, bcols = a_mn ? N : K;
+  const int64_t nb = stride_b != 0 ? groups : 1;   // matrices of weights
+  Operand x{A, lda, 0}, w{B, ldb, stride_b};
+  SegParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.groups = Groups{offsets, (int32_t)groups, (int32_t)M, plan->d_err};
+  const int cg = grouped_cg(plan, M >= 128 * groups ? 2 : 1);
+  const int64_t tiles = ((N + 128 * cg - 1) / (128 * cg)) * (M / (128 * cg) + std::min(groups, M));
+  if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
+  if (K > 0) {
+    const size_t xb = repitch_bytes(x, M, K, 1), wb = repitch_bytes(w, brows, bcols, nb);
+    if (xb + wb > 0) {
+      s = ensure_ws(plan, xb + wb, stream);
+      if (s == GEMM_OK) s = repitch(&x, M, K, 1, nullptr, static_cast<char*>(plan->ws), stream);
+      if (s == GEMM_OK)
+        s = repitch(&w, brows, bcols, nb, nb > 1 ? offsets : nullptr, static_cast<char*>(plan->ws) + xb, stream);
+      if (s != GEMM_OK) return s;
+    }
+    const CUtensorMapDataType dt = map_type(plan->ab);
+    bool ok = a_mn ? encode_3d(&p.tmA, dt, w.p, N, K, w.ld, nb, w.stride, 64, 2 * TC_BK)
+                   : encode_3d(&p.tmA, dt, w.p, K, N, w.ld, nb, w.stride, TC_BK, 128);
+    for (int b = 0; b < 5; ++b) ok = ok && encode_3d(&p.tmB[b], dt, x.p, K, M, x.ld, 1, 0, TC_BK, 128u >> b);
+    if (!ok) return GEMM_ERR_CUDA;
+  }
+  p.a_batched = nb > 1 ? 1 : 0;
+  p.M = N;
   p.K = (int32_t)K;
-  p.ab_dtype = plan->ab;
+  p.tiles_m = (int32_t)((N + 128 * cg - 1) / (128 * cg));
+  p.idesc = make_idesc(plan->ab == GEMM_BF16, 0, a_mn, false, 128 * cg);
   p.epi = epilogue_of(epi, out, alpha, D, ldd);
   p.epi.stride_bias = stride_bias;
-  return launch_grouped(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  p.err = plan->d_err;
+  p.timeout_ns = plan->timeout_ns;
+  const int workers = workers_of(plan, cg, tiles);
+  if (launch_seg(p, SEG_TOKENS, cg, a_mn, workers, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  plan->last = seg_config(cg, tiles, workers);
+  log_config("grouped", M, N, K, groups, plan->last);
+  return GEMM_OK;
 }
 
 gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N, int64_t K, double alpha,
                                      const void* A, int64_t lda, const void* B, int64_t ldb, double beta,
                                      const void* C, int64_t ldc, int64_t stride_c, void* D, int64_t ldd,
                                      int64_t stride_d, const int32_t* offsets, gemm_dtype_t out_dtype,
-                                     gemm_stream_t stream) {
+                                     gemm_stream_t stream_) {
   if (!plan) return GEMM_ERR_INVALID_ARG;
   NvtxRange range("gemm_run_grouped_wgrad");
   if (!is_f16ish(plan->ab)) return GEMM_ERR_UNSUPPORTED;
@@ -105,15 +191,42 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
   }
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
-  WgradParams p{};
-  p.g = Groups{offsets, (int32_t)groups, (int32_t)K, plan->d_err};
-  p.A = A;
-  p.lda = lda;
-  p.B = B;
-  p.ldb = ldb;
-  p.M = (int32_t)M;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  Operand x{A, lda, 0}, y{B, ldb, 0};
+  SegParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int cg = grouped_cg(plan, M > 128 && N > 128 ? 2 : 1);
+  p.tiles_m = (int32_t)((M + 128 * cg - 1) / (128 * cg));
+  p.tiles_n = (int32_t)((N + 128 * cg - 1) / (128 * cg));
+  const int64_t tiles = groups * p.tiles_m * (int64_t)p.tiles_n;
+  if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
+  p.tiles_per_group = p.tiles_m * p.tiles_n;
+  p.num_tiles = (int32_t)tiles;
+  p.groups = Groups{offsets, (int32_t)groups, (int32_t)K, plan->d_err};
+  const size_t mb = align_up((size_t)groups * 2 * sizeof(CUtensorMap), 256);
+  const size_t xb = K > 0 ? repitch_bytes(x, K, M, 1) : 0, yb = K > 0 ? repitch_bytes(y, K, N, 1) : 0;
+  gemm_status_t s = ensure_ws(plan, mb + xb + yb, stream);
+  if (s != GEMM_OK) return s;
+  char* ws = static_cast<char*>(plan->ws);
+  CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(ws);
+  if (K > 0) {
+    s = repitch(&x, K, M, 1, nullptr, ws + mb, stream);
+    if (s == GEMM_OK) s = repitch(&y, K, N, 1, nullptr, ws + mb + xb, stream);
+    if (s != GEMM_OK) return s;
+    const CUtensorMapDataType dt = map_type(plan->ab);
+    if (!encode_3d(&p.tmA, dt, x.p, M, K, x.ld, 1, 0, 64, 2 * TC_BK) ||
+        !encode_3d(&p.tmB[0], dt, y.p, N, K, y.ld, 1, 0, 64, 2 * TC_BK))
+      return GEMM_ERR_CUDA;
+    p.a_base = reinterpret_cast<uint64_t>(x.p);
+    p.b_base = reinterpret_cast<uint64_t>(y.p);
+    p.a_pitch = (uint64_t)x.ld * 2;
+    p.b_pitch = (uint64_t)y.ld * 2;
+    if (launch_wgrad_maps(p, maps, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  }
+  p.group_maps = maps;
+  p.M = M;
   p.N = (int32_t)N;
-  p.ab_dtype = plan->ab;
+  p.idesc = make_idesc(plan->ab == GEMM_BF16, 0, true, true, 128 * cg);
   p.epi = epilogue_of(nullptr, out_dtype, alpha, D, ldd);
   p.epi.stride_d = stride_d;
   p.epi.beta = (float)beta;
@@ -122,8 +235,16 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
   p.epi.ldc = ldc;
   p.epi.c_dtype = plan->c;
   p.epi.stride_c = stride_c;
-  p.epi.vec_c = (p.epi.read_c && aligned16(C) && (ldc * dtype_bytes(plan->c)) % 16 == 0) ? 1 : 0;
-  return launch_wgrad(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  const int cs = dtype_bytes(plan->c);
+  p.epi.vec_c = (p.epi.read_c && aligned16(C) && (ldc * cs) % 16 == 0 && (stride_c * cs) % 16 == 0) ? 1 : 0;
+  if (groups > 1 && (stride_d * dtype_bytes(out_dtype)) % 16 != 0) p.epi.vec_d = 0;
+  p.err = plan->d_err;
+  p.timeout_ns = plan->timeout_ns;
+  const int workers = workers_of(plan, cg, tiles);
+  if (launch_seg(p, SEG_WGRAD, cg, true, workers, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  plan->last = seg_config(cg, tiles, workers);
+  log_config("grouped_wgrad", M, N, K, groups, plan->last);
+  return GEMM_OK;
 }
 
 gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N, int64_t K, double alpha,

@@ -4,9 +4,6 @@
 namespace gemmlib {
 namespace {
 
-constexpr int ST = 64;    // output tile edge of the plain tile kernel
-constexpr int SK = 16;    // its depth per step
-
 __device__ __forceinline__ void finish(const EpiParams& e, void* D, const void* C, const void* bias, int64_t i,
                                        int64_t j, float acc) {
   float v = e.alpha * acc;
@@ -17,91 +14,6 @@ __device__ __forceinline__ void finish(const EpiParams& e, void* D, const void* 
   if (e.bias_mode == GEMM_BIAS_COL) v += load_as_float(bias, e.bias_dtype, j);
   if (e.relu) v = fmaxf(v, 0.0f);
   store_float_as(D, e.d_dtype, i * e.ldd + j, v);
-}
-
-// One ST x ST tile: rows [m0, m1) and columns [n0, n0 + ST) with element (i, k) of A at
-// a_i * i + a_k * k and (k, j) of B at b_k * k + b_j * j, k in [k0, k1).
-__device__ void tile_product(const void* A, int64_t a_i, int64_t a_k, const void* B, int64_t b_k, int64_t b_j,
-                             int ab, int64_t m0, int64_t m1, int64_t n0, int64_t N, int64_t k0, int64_t k1,
-                             float (&acc)[4][4]) {
-  __shared__ float sa[SK][ST + 1], sb[SK][ST + 1];
-  const int tx = threadIdx.x, ty = threadIdx.y, t = ty * 16 + tx;
-  for (int64_t k = k0; k < k1; k += SK) {
-    for (int q = t; q < SK * ST; q += 256) {
-      // Consecutive threads run along the operand's contiguous dimension.
-      const int ai = a_k == 1 ? q / SK : q % ST, ak = a_k == 1 ? q % SK : q / ST;
-      const int bj = b_k == 1 ? q / SK : q % ST, bk = b_k == 1 ? q % SK : q / ST;
-      sa[ak][ai] = (m0 + ai < m1 && k + ak < k1) ? load_as_float(A, ab, (m0 + ai) * a_i + (k + ak) * a_k) : 0.0f;
-      sb[bk][bj] = (n0 + bj < N && k + bk < k1) ? load_as_float(B, ab, (k + bk) * b_k + (n0 + bj) * b_j) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < SK; ++kk) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = sa[kk][ty + 16 * i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = sb[kk][tx + 16 * j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-}
-
-__global__ void __launch_bounds__(256) grouped_kernel(const GroupedParams p) {
-  // Tile row blockIdx.y of all groups' tile rows, one group after the other.
-  __shared__ int s_e, s_lo, s_hi, s_t;
-  if (threadIdx.x == 0 && threadIdx.y == 0) {
-    int left = (int)blockIdx.y;
-    s_e = -1;
-    for (int e = 0; e < p.g.count; ++e) {
-      int lo, hi;
-      group_range(p.g, e, lo, hi);
-      const int t = (hi - lo + ST - 1) / ST;
-      if (left < t) {
-        s_e = e;
-        s_lo = lo;
-        s_hi = hi;
-        s_t = left;
-        break;
-      }
-      left -= t;
-    }
-  }
-  __syncthreads();
-  if (s_e < 0) return;
-  const int64_t m0 = s_lo + (int64_t)s_t * ST, n0 = (int64_t)blockIdx.x * ST;
-  float acc[4][4] = {};
-  const char* B = static_cast<const char*>(p.B) + s_e * p.stride_b * dtype_bytes(p.ab_dtype);
-  tile_product(p.A, p.lda, 1, B, p.b_k, p.b_n, p.ab_dtype, m0, s_hi, n0, p.N, 0, p.K, acc);
-  const char* bias = static_cast<const char*>(p.epi.bias) + s_e * p.epi.stride_bias * dtype_bytes(p.epi.bias_dtype);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = m0 + threadIdx.y + 16 * i, n = n0 + threadIdx.x + 16 * j;
-      if (r < s_hi && n < p.N) finish(p.epi, p.epi.D, nullptr, bias, r, n, acc[i][j]);
-    }
-}
-
-__global__ void __launch_bounds__(256) wgrad_kernel(const WgradParams p) {
-  const int e = (int)blockIdx.z;
-  int lo, hi;
-  group_range(p.g, e, lo, hi);
-  const int64_t m0 = (int64_t)blockIdx.y * ST, n0 = (int64_t)blockIdx.x * ST;
-  float acc[4][4] = {};
-  tile_product(p.A, 1, p.lda, p.B, p.ldb, 1, p.ab_dtype, m0, p.M, n0, p.N, lo, hi, acc);
-  const EpiPtrs ptr = epi_ptrs(p.epi, e);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + threadIdx.y + 16 * i, n = n0 + threadIdx.x + 16 * j;
-      if (m < p.M && n < p.N) finish(p.epi, ptr.D, ptr.C, nullptr, m, n, acc[i][j]);
-    }
 }
 
 // One warp per output: lanes stride over K.
@@ -132,21 +44,33 @@ __global__ void __launch_bounds__(256) q4_kernel(const Q4Params p) {
   }
 }
 
-}  // namespace
-
-cudaError_t launch_grouped(const GroupedParams& p, cudaStream_t stream) {
-  const int64_t gy = (int64_t)(p.g.rows + ST - 1) / ST + p.g.count, gx = (p.N + ST - 1) / ST;
-  for (int64_t y = 0; y < 1; ++y) {
-    if (gy > 65535) return cudaErrorInvalidValue;
-    grouped_kernel<<<dim3((unsigned)gx, (unsigned)gy), dim3(16, 16), 0, stream>>>(p);
+// A lane loads the eight elements that it stores: 2-byte loads (the source's rows
+// start anywhere) whose lines the warp uses whole, one 16-byte store.
+__global__ void __launch_bounds__(256) repitch_kernel(const uint16_t* src, int64_t ld, int64_t stride, uint16_t* dst,
+                                                      int64_t ldd, int64_t stride_d, int64_t rows, int64_t cols,
+                                                      const int32_t* offsets) {
+  const int64_t z = blockIdx.y;
+  if (offsets != nullptr && offsets[z + 1] <= offsets[z]) return;
+  src += z * stride;
+  dst += z * stride_d;
+  const int64_t per_row = ldd / 8, total = rows * per_row;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t r = i / per_row, c = i % per_row * 8;
+    uint16_t v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = c + u < cols ? src[r * ld + c + u] : (uint16_t)0;
+    *reinterpret_cast<uint4*>(dst + r * ldd + c) = *reinterpret_cast<uint4*>(v);
   }
-  return cudaGetLastError();
 }
 
-cudaError_t launch_wgrad(const WgradParams& p, cudaStream_t stream) {
-  const dim3 grid((unsigned)((p.N + ST - 1) / ST), (unsigned)((p.M + ST - 1) / ST), (unsigned)p.g.count);
-  if (grid.y > 65535) return cudaErrorInvalidValue;
-  wgrad_kernel<<<grid, dim3(16, 16), 0, stream>>>(p);
+}  // namespace
+
+cudaError_t launch_repitch(const void* src, int64_t ld, int64_t stride, void* dst, int64_t ldd, int64_t stride_d,
+                           int64_t rows, int64_t cols, int64_t batch, const int32_t* offsets, cudaStream_t stream) {
+  const int64_t per = (rows * (ldd / 8) + 255) / 256;
+  const dim3 grid((unsigned)std::min<int64_t>(per, std::max<int64_t>(1, 2432 / batch)), (unsigned)batch);
+  repitch_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(src), ld, stride, static_cast<uint16_t*>(dst),
+                                           ldd, stride_d, rows, cols, offsets);
   return cudaGetLastError();
 }
 

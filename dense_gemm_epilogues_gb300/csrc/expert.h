@@ -95,9 +95,12 @@ struct Q4Params {
   int64_t ldz, stride_z;
   int32_t N, K, group;
   int32_t ab_dtype;
+  int32_t vec_q, vec_a;          // q's rows and A's rows can be read 16 bytes at a time
   EpiParams epi;
 };
-cudaError_t launch_q4(const Q4Params& p, cudaStream_t stream);
+// mt: 16-column tiles per CTA (1, 2, 4); nt: blocks of 8 rows per pass over the weights (1, 2, 4; 4 tiles with nt 1 only).
+cudaError_t launch_q4(const Q4Params& p, int mt, int nt, cudaStream_t stream);
+cudaError_t launch_q4_dequant(const Q4Params& p, void* out, int64_t ldw, int64_t stride_w, cudaStream_t stream);
 
 // Newton-Schulz: the wide matrix X (m <= n) of each input matrix G.
 struct OrthoInput {

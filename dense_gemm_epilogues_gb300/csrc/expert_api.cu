@@ -99,6 +99,48 @@ gemm_config_t seg_config(int cg, int64_t tiles, int workers) {
   return c;
 }
 
+// D[r, :] = epilogue(x[r, :] * W_g) on seg_kernel: x M x K row-major, W_g K x N (w_mn: N
+// contiguous, else K).  ws_used: scratch that holds an operand already.
+gemm_status_t tokens_product(gemm_plan* plan, const Groups& groups, int64_t M, int64_t N, int64_t K, Operand x, Operand w,
+                             bool w_mn, size_t ws_used, const EpiParams& epi, const char* entry, cudaStream_t stream) {
+  const int64_t wrows = w_mn ? K : N, wcols = w_mn ? N : K;
+  const int64_t nw = w.stride != 0 ? groups.count : 1;   // matrices of weights
+  SegParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.groups = groups;
+  const int cg = grouped_cg(plan, M >= 128 * (int64_t)groups.count ? 2 : 1);
+  const int64_t tiles = ((N + 128 * cg - 1) / (128 * cg)) * (M / (128 * cg) + std::min<int64_t>(groups.count, M));
+  if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
+  if (K > 0) {
+    const size_t xb = repitch_bytes(x, M, K, 1), wb = repitch_bytes(w, wrows, wcols, nw);
+    if (xb + wb > 0) {
+      gemm_status_t s = ensure_ws(plan, ws_used + xb + wb, stream);
+      char* ws = static_cast<char*>(plan->ws) + ws_used;
+      if (s == GEMM_OK) s = repitch(&x, M, K, 1, nullptr, ws, stream);
+      if (s == GEMM_OK) s = repitch(&w, wrows, wcols, nw, nw > 1 ? groups.offsets : nullptr, ws + xb, stream);
+      if (s != GEMM_OK) return s;
+    }
+    const CUtensorMapDataType dt = map_type(plan->ab);
+    bool ok = w_mn ? encode_3d(&p.tmA, dt, w.p, N, K, w.ld, nw, w.stride, 64, 2 * TC_BK)
+                   : encode_3d(&p.tmA, dt, w.p, K, N, w.ld, nw, w.stride, TC_BK, 128);
+    for (int b = 0; b < 5; ++b) ok = ok && encode_3d(&p.tmB[b], dt, x.p, K, M, x.ld, 1, 0, TC_BK, 128u >> b);
+    if (!ok) return GEMM_ERR_CUDA;
+  }
+  p.a_batched = nw > 1 ? 1 : 0;
+  p.M = N;
+  p.K = (int32_t)K;
+  p.tiles_m = (int32_t)((N + 128 * cg - 1) / (128 * cg));
+  p.idesc = make_idesc(plan->ab == GEMM_BF16, 0, w_mn, false, 128 * cg);
+  p.epi = epi;
+  p.err = plan->d_err;
+  p.timeout_ns = plan->timeout_ns;
+  const int workers = workers_of(plan, cg, tiles);
+  if (launch_seg(p, SEG_TOKENS, cg, w_mn, workers, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  plan->last = seg_config(cg, tiles, workers);
+  log_config(entry, M, N, K, groups.count, plan->last);
+  return GEMM_OK;
+}
+
 bool too_large(std::initializer_list<int64_t> dims) {
   for (int64_t d : dims)
     if (d > kMaxDim - 512) return true;   // tile edges past a size stay within 32 bits
@@ -127,46 +169,11 @@ gemm_status_t gemm_run_grouped(gemm_plan_t plan, gemm_layout_t lb, int64_t group
   if (K > 0 && (!A || !B || lda < K || ldb < (lb == GEMM_OP_N ? K : N))) return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
-  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  const bool a_mn = lb == GEMM_OP_T;
-  const int64_t brows = a_mn ? K : N, bcols = a_mn ? N : K;
-  const int64_t nb = stride_b != 0 ? groups : 1;   // matrices of weights
-  Operand x{A, lda, 0}, w{B, ldb, stride_b};
-  SegParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.groups = Groups{offsets, (int32_t)groups, (int32_t)M, plan->d_err};
-  const int cg = grouped_cg(plan, M >= 128 * groups ? 2 : 1);
-  const int64_t tiles = ((N + 128 * cg - 1) / (128 * cg)) * (M / (128 * cg) + std::min(groups, M));
-  if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
-  if (K > 0) {
-    const size_t xb = repitch_bytes(x, M, K, 1), wb = repitch_bytes(w, brows, bcols, nb);
-    if (xb + wb > 0) {
-      s = ensure_ws(plan, xb + wb, stream);
-      if (s == GEMM_OK) s = repitch(&x, M, K, 1, nullptr, static_cast<char*>(plan->ws), stream);
-      if (s == GEMM_OK)
-        s = repitch(&w, brows, bcols, nb, nb > 1 ? offsets : nullptr, static_cast<char*>(plan->ws) + xb, stream);
-      if (s != GEMM_OK) return s;
-    }
-    const CUtensorMapDataType dt = map_type(plan->ab);
-    bool ok = a_mn ? encode_3d(&p.tmA, dt, w.p, N, K, w.ld, nb, w.stride, 64, 2 * TC_BK)
-                   : encode_3d(&p.tmA, dt, w.p, K, N, w.ld, nb, w.stride, TC_BK, 128);
-    for (int b = 0; b < 5; ++b) ok = ok && encode_3d(&p.tmB[b], dt, x.p, K, M, x.ld, 1, 0, TC_BK, 128u >> b);
-    if (!ok) return GEMM_ERR_CUDA;
-  }
-  p.a_batched = nb > 1 ? 1 : 0;
-  p.M = N;
-  p.K = (int32_t)K;
-  p.tiles_m = (int32_t)((N + 128 * cg - 1) / (128 * cg));
-  p.idesc = make_idesc(plan->ab == GEMM_BF16, 0, a_mn, false, 128 * cg);
-  p.epi = epilogue_of(epi, out, alpha, D, ldd);
-  p.epi.stride_bias = stride_bias;
-  p.err = plan->d_err;
-  p.timeout_ns = plan->timeout_ns;
-  const int workers = workers_of(plan, cg, tiles);
-  if (launch_seg(p, SEG_TOKENS, cg, a_mn, workers, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-  plan->last = seg_config(cg, tiles, workers);
-  log_config("grouped", M, N, K, groups, plan->last);
-  return GEMM_OK;
+  EpiParams e = epilogue_of(epi, out, alpha, D, ldd);
+  e.stride_bias = stride_bias;
+  return tokens_product(plan, Groups{offsets, (int32_t)groups, (int32_t)M, plan->d_err}, M, N, K, Operand{A, lda, 0},
+                        Operand{B, ldb, stride_b}, lb == GEMM_OP_T, 0, e, "grouped",
+                        reinterpret_cast<cudaStream_t>(stream_));
 }
 
 gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N, int64_t K, double alpha,
@@ -250,7 +257,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
 gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N, int64_t K, double alpha,
                           const void* A, int64_t lda, const gemm_q4_t* B, void* D, int64_t ldd,
                           const int32_t* offsets, const gemm_epilogue_t* epi, int64_t stride_bias,
-                          gemm_stream_t stream) {
+                          gemm_stream_t stream_) {
   if (!plan || !B) return GEMM_ERR_INVALID_ARG;
   NvtxRange range("gemm_run_q4");
   if (!is_f16ish(plan->ab)) return GEMM_ERR_UNSUPPORTED;
@@ -289,7 +296,28 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   p.ab_dtype = plan->ab;
   p.epi = epilogue_of(epi, out, alpha, D, ldd);
   p.epi.stride_bias = stride_bias;
-  return launch_q4(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  p.vec_q = (aligned16(p.q) && p.ldq % 16 == 0 && (groups == 1 || p.stride_q % 16 == 0)) ? 1 : 0;
+  p.vec_a = (aligned16(A) && lda % 8 == 0) ? 1 : 0;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const int64_t per_group = (M + groups - 1) / groups;   // rows of an average group
+  int few = 64;
+  if (const char* env = std::getenv("GEMM_Q4_FEW")) few = std::atoi(env);
+  if (per_group > few && K > 0) {
+    const int64_t ldw = (K + 7) / 8 * 8;
+    const size_t bytes = align_up((size_t)(groups * N * ldw) * 2, 256);
+    s = ensure_ws(plan, bytes + repitch_bytes(Operand{A, lda, 0}, M, K, 1), stream);
+    if (s != GEMM_OK) return s;
+    if (launch_q4_dequant(p, plan->ws, ldw, N * ldw, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+    return tokens_product(plan, p.g, M, N, K, Operand{A, lda, 0}, Operand{plan->ws, ldw, groups > 1 ? N * ldw : 0}, false,
+                          bytes, p.epi, "q4", stream);
+  }
+  const int nt = per_group > 16 ? 4 : per_group > 8 ? 2 : 1;
+  int mt = 1;
+  for (int cand : {4, 2})
+    if (mt == 1 && (cand < 4 || nt == 1) && std::min(groups, M) * ((N + 16 * cand - 1) / (16 * cand)) >= 152) mt = cand;
+  if (const char* env = std::getenv("GEMM_Q4_MT")) mt = std::atoi(env);
+  if (launch_q4(p, mt, nt, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  return GEMM_OK;
 }
 
 gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int64_t N, int steps,

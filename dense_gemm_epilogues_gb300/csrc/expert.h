@@ -74,18 +74,19 @@ struct SegParams {
 cudaError_t launch_seg(const SegParams& p, int mode, int cg, bool a_mn, int workers, cudaStream_t stream);
 cudaError_t launch_wgrad_maps(const SegParams& p, CUtensorMap* maps, cudaStream_t stream);
 
-// dst[z][r][c] = src[z][r][c] for 16-bit elements with a pitch that TMA can address
-// (ldd a multiple of 8; columns up to ldd are zero).  offsets != null: the z-th matrix
+// dst[z][r][c] = src[z][r][c] for elements of one or two bytes, with a pitch that TMA
+// can address (ldd * elem_bytes a multiple of 16; columns up to ldd are zero).  offsets != null: the z-th matrix
 // is skipped when group z has no rows.
 cudaError_t launch_repitch(const void* src, int64_t ld, int64_t stride, void* dst, int64_t ldd, int64_t stride_d,
-                           int64_t rows, int64_t cols, int64_t batch, const int32_t* offsets, cudaStream_t stream);
+                           int64_t rows, int64_t cols, int64_t batch, const int32_t* offsets, int elem_bytes,
+                           cudaStream_t stream);
 
 // D[r, n] = act(alpha * sum_k A[r, k] * scale[n, k / group] * (q[n, k] - zero[n, k / group]) + bias[n])
 // with the q, scales and zeros of the row's group.
 struct Q4Params {
+  CUtensorMap tm_q;              // q: boxes of 64 bytes (128 k) x cta_rows columns, 64-byte swizzle
+  CUtensorMap tm_x;              // A: boxes of 64 k x 8 nt rows, 128-byte swizzle
   Groups g;
-  const void* A;                 // rows x K, row-major
-  int64_t lda;
   const uint8_t* q;              // N rows of ceil(K / 2) bytes, the lower k in the low half
   int64_t ldq, stride_q;         // bytes
   const void* scales;
@@ -95,11 +96,20 @@ struct Q4Params {
   int64_t ldz, stride_z;
   int32_t N, K, group;
   int32_t ab_dtype;
-  int32_t vec_q, vec_a;          // q's rows and A's rows can be read 16 bytes at a time
+  int32_t q_batched;             // tm_q has one slice per group
+  int32_t cta_rows;              // columns of weights per CTA
+  int32_t group_units, group_shift, vec_s, scale_cols;   // set by launch_q4
   EpiParams epi;
+  uint64_t timeout_ns;
 };
-// mt: 16-column tiles per CTA (1, 2, 4); nt: blocks of 8 rows per pass over the weights (1, 2, 4; 4 tiles with nt 1 only).
-cudaError_t launch_q4(const Q4Params& p, int mt, int nt, cudaStream_t stream);
+// How q4_kernel runs a call: blocks of 8 rows per pass over the weights (1, 2, 4) and
+// columns per CTA.  rows_per_group: of an average group; groups_used: at most so many
+// groups have rows.
+struct Q4Shape {
+  int nt, cta_rows;
+};
+Q4Shape q4_shape(int64_t N, int64_t rows_per_group, int64_t groups_used, int sm_count);
+cudaError_t launch_q4(const Q4Params& p, int nt, cudaStream_t stream);
 cudaError_t launch_q4_dequant(const Q4Params& p, void* out, int64_t ldw, int64_t stride_w, cudaStream_t stream);
 
 // Newton-Schulz: the wide matrix X (m <= n) of each input matrix G.

@@ -59,7 +59,8 @@ gemm_status_t repitch(Operand* x, int64_t rows, int64_t cols, int64_t batch, con
                       cudaStream_t stream) {
   if (addressable(*x, batch)) return GEMM_OK;
   const int64_t ld = (cols + 7) / 8 * 8;
-  if (launch_repitch(x->p, x->ld, x->stride, to, ld, rows * ld, rows, cols, batch, offsets, stream) != cudaSuccess)
+  if (launch_repitch(x->p, x->ld, x->stride, to, ld, rows * ld, rows, cols, batch, offsets, 2, stream) !=
+      cudaSuccess)
     return GEMM_ERR_CUDA;
   *x = Operand{to, ld, rows * ld};
   return GEMM_OK;
@@ -265,6 +266,7 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   if (B->group_size <= 0 || B->group_size % 32 != 0 || !is_float_out(B->scale_dtype)) return GEMM_ERR_INVALID_ARG;
   if (B->stride_values < 0 || B->stride_scales < 0 || B->stride_zeros < 0) return GEMM_ERR_INVALID_ARG;
   if (groups > kMaxGroups || too_large({M, N, K})) return GEMM_ERR_UNSUPPORTED;
+  if (B->ld_scales >= (1 << 23) || B->ld_zeros >= (1 << 23)) return GEMM_ERR_UNSUPPORTED;   // 32-bit offsets in a CTA
   const gemm_dtype_t out = epi ? epi->out_dtype : plan->c;
   gemm_status_t s = check_epilogue(epi, out);
   if (s != GEMM_OK) return s;
@@ -276,10 +278,9 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
     return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
-  Q4Params p{};
+  Q4Params p;
+  std::memset(&p, 0, sizeof(p));
   p.g = Groups{offsets, (int32_t)groups, (int32_t)M, plan->d_err};
-  p.A = A;
-  p.lda = lda;
   p.q = static_cast<const uint8_t*>(B->values);
   p.ldq = B->ld_values;
   p.stride_q = B->stride_values;
@@ -296,27 +297,51 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   p.ab_dtype = plan->ab;
   p.epi = epilogue_of(epi, out, alpha, D, ldd);
   p.epi.stride_bias = stride_bias;
-  p.vec_q = (aligned16(p.q) && p.ldq % 16 == 0 && (groups == 1 || p.stride_q % 16 == 0)) ? 1 : 0;
-  p.vec_a = (aligned16(A) && lda % 8 == 0) ? 1 : 0;
+  p.timeout_ns = plan->timeout_ns;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int64_t per_group = (M + groups - 1) / groups;   // rows of an average group
+  Operand x{A, lda, 0};
+  const bool q_ok = aligned16(p.q) && p.ldq % 16 == 0 && (groups == 1 || p.stride_q % 16 == 0);
+  const int64_t ldq = align_up((size_t)(K + 1) / 2, 16);
+  const size_t qb = K == 0 || q_ok ? 0 : align_up((size_t)(groups * N * ldq), 256);
+  const size_t xb = K == 0 ? 0 : repitch_bytes(x, M, K, 1);
   int few = 64;
   if (const char* env = std::getenv("GEMM_Q4_FEW")) few = std::atoi(env);
-  if (per_group > few && K > 0) {
-    const int64_t ldw = (K + 7) / 8 * 8;
-    const size_t bytes = align_up((size_t)(groups * N * ldw) * 2, 256);
-    s = ensure_ws(plan, bytes + repitch_bytes(Operand{A, lda, 0}, M, K, 1), stream);
+  const bool prompt = per_group > few && K > 0;
+  const int64_t ldw = (K + 7) / 8 * 8;
+  const size_t wb = prompt ? align_up((size_t)(groups * N * ldw) * 2, 256) : 0;
+  if (qb + xb + wb > 0) {
+    s = ensure_ws(plan, qb + xb + wb, stream);
     if (s != GEMM_OK) return s;
-    if (launch_q4_dequant(p, plan->ws, ldw, N * ldw, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-    return tokens_product(plan, p.g, M, N, K, Operand{A, lda, 0}, Operand{plan->ws, ldw, groups > 1 ? N * ldw : 0}, false,
-                          bytes, p.epi, "q4", stream);
   }
-  const int nt = per_group > 16 ? 4 : per_group > 8 ? 2 : 1;
-  int mt = 1;
-  for (int cand : {4, 2})
-    if (mt == 1 && (cand < 4 || nt == 1) && std::min(groups, M) * ((N + 16 * cand - 1) / (16 * cand)) >= 152) mt = cand;
-  if (const char* env = std::getenv("GEMM_Q4_MT")) mt = std::atoi(env);
-  if (launch_q4(p, mt, nt, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  char* ws = static_cast<char*>(plan->ws);
+  if (qb > 0) {   // packed weights that TMA cannot address are copied to a pitch it can
+    if (launch_repitch(p.q, p.ldq, p.stride_q, ws, ldq, N * ldq, N, (K + 1) / 2, groups, offsets, 1, stream) != cudaSuccess)
+      return GEMM_ERR_CUDA;
+    p.q = reinterpret_cast<const uint8_t*>(ws);
+    p.ldq = ldq;
+    p.stride_q = N * ldq;
+  }
+  s = K == 0 ? GEMM_OK : repitch(&x, M, K, 1, nullptr, ws + qb, stream);
+  if (s != GEMM_OK) return s;
+  if (prompt) {
+    if (launch_q4_dequant(p, ws + qb + xb, ldw, N * ldw, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+    return tokens_product(plan, p.g, M, N, K, x, Operand{ws + qb + xb, ldw, groups > 1 ? N * ldw : 0}, false, qb + xb + wb,
+                          p.epi, "q4", stream);
+  }
+  const Q4Shape shape = q4_shape(N, per_group, std::min(groups, M), plan->sm_count);
+  p.cta_rows = shape.cta_rows;
+  p.q_batched = groups > 1 && p.stride_q != 0 ? 1 : 0;
+  if (K > 0 &&
+      (!encode_tiled(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.q, (K + 1) / 2, N, p.ldq, p.q_batched ? groups : 1,
+                     p.q_batched ? p.stride_q : N * p.ldq, 64, (uint32_t)shape.cta_rows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+       !encode_tiled(&p.tm_x, map_type(plan->ab), x.p, K, M, x.ld * 2, 1, 0, 64, 8u * shape.nt,
+                     CU_TENSOR_MAP_SWIZZLE_128B)))
+    return GEMM_ERR_CUDA;
+  if (launch_q4(p, shape.nt, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  gemm_config_t cfg{};
+  cfg.kernel = GEMM_KERNEL_SIMT;
+  plan->last = cfg;
   return GEMM_OK;
 }
 

@@ -98,6 +98,19 @@ bool encode_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_
   return r == CUDA_SUCCESS;
 }
 
+bool encode_tiled(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
+                  uint64_t pitch_bytes, uint64_t nbatch, uint64_t bstride_bytes, uint32_t box_inner, uint32_t box_outer,
+                  CUtensorMapSwizzle swizzle) {
+  if (!encode_fn()) return false;
+  const bool flat = nbatch <= 1 && bstride_bytes == 0;
+  cuuint64_t dims[3] = {inner, outer, nbatch};
+  cuuint64_t strides[2] = {pitch_bytes, bstride_bytes};
+  cuuint32_t box[3] = {box_inner, box_outer, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(tm, dt, flat ? 2 : 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace gemmlib
 
 namespace {

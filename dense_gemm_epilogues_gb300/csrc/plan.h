@@ -105,4 +105,10 @@ gemm_status_t run_product(gemm_plan* plan, gemm_dtype_t ab, gemm_dtype_t c, gemm
 bool encode_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
                uint64_t ld, uint64_t nbatch, uint64_t bstride, uint32_t box_inner, uint32_t box_outer);
 
+// The same for any element type: `inner` contiguous elements, pitches in bytes
+// (multiples of 16); two dimensions when nbatch <= 1 and bstride is 0, else three.
+bool encode_tiled(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
+                  uint64_t pitch_bytes, uint64_t nbatch, uint64_t bstride_bytes, uint32_t box_inner, uint32_t box_outer,
+                  CUtensorMapSwizzle swizzle);
+
 }  // namespace gemmlib

@@ -406,218 +406,14 @@ def matmul(a, b, *, c=None, alpha: float = 1.0, beta: float = 0.0, bias=None,
     return out
 
 
-# ---- expert layers: grouped products, 4-bit weights, orthogonalised updates ----
+# ---- expert layers (expert.py): loaded on first use, since they need torch ----
 
-def _stream_of(t, stream) -> int:
-    if stream is not None:
-        return stream
-    import torch
-    return torch.cuda.current_stream(t.device).cuda_stream
+_EXPERT = ("grouped_matmul", "grouped_weight_grad", "quantize_q4", "q4_matmul", "orthogonalize")
 
 
-def _rows(t, name: str) -> int:
-    """Leading dimension of a row-major 2-D tensor."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name} must be row-major and two-dimensional")
-    return max(t.stride(0), t.shape[1], 1)
-
-
-def _check_offsets(offsets, groups: int):
-    import torch
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != groups + 1 or not offsets.is_contiguous():
-        raise ValueError("offsets must be a contiguous int32 tensor of groups + 1 entries")
-
-
-def _same_device(*tensors):
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors are on different devices")
-
-
-def _group_epilogue(bias, groups: int, n: int, relu: bool, out):
-    """(epilogue, bias stride) of a grouped product; bias is [groups, N] or [N] (shared)."""
-    stride = 0
-    if bias is not None:
-        if bias.shape not in ((groups, n), (n,)) or (bias.stride(-1) != 1 and n > 1):
-            raise ValueError("bias must be [N] or [groups, N] with contiguous rows")
-        stride = bias.stride(0) if bias.dim() == 2 else 0
-    return gemm_epilogue_t(bias.data_ptr() if bias is not None else None,
-                           _torch_code(bias) if bias is not None else GEMM_F32,
-                           GEMM_BIAS_COL if bias is not None else GEMM_BIAS_NONE,
-                           GEMM_ACT_RELU if relu else GEMM_ACT_NONE, _torch_code(out), GEMM_ACT_NONE, 1.0), stride
-
-
-def grouped_matmul(x, w, offsets, *, alpha: float = 1.0, bias=None, relu: bool = False, out=None, out_dtype=None,
-                   plan: Optional[Plan] = None, stream=None):
-    """out[r] = act(alpha * x[r] @ w[g] + bias[g]) for the rows r of each group g
-    (gemm_run_grouped): the forward product of an expert layer, and with
-    w.transpose(1, 2) its input gradient.
-
-    x: [rows, K] float16 or bfloat16, rows sorted by group; w: [groups, K, N]
-    with unit stride along K or N; offsets: int32 [groups + 1] on the device,
-    group g owning rows offsets[g] .. offsets[g + 1] - 1 (rows of no group are
-    left as they are in `out`).  bias: [groups, N] or [N].  out_dtype defaults
-    to x's.  Returns `out`."""
-    import torch
-    if w.dim() != 3 or x.dim() != 2 or x.shape[1] != w.shape[1] or w.dtype != x.dtype:
-        raise ValueError("x must be [rows, K] and w [groups, K, N] of the same type")
-    (M, K), (groups, _, N) = x.shape, w.shape
-    _check_offsets(offsets, groups)
-    _same_device(x, w, offsets, bias, out)
-    lda = _rows(x, "x")
-    if w.stride(2) == 1 or N <= 1:
-        lb, ldb = GEMM_OP_T, max(w.stride(1), N, 1)
-    elif w.stride(1) == 1 or K <= 1:
-        lb, ldb = GEMM_OP_N, max(w.stride(2), K, 1)
-    else:
-        raise ValueError("w must have unit stride along K or N")
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or x.dtype, device=x.device)
-    elif tuple(out.shape) != (M, N):
-        raise ValueError("out must be [rows, N]")
-    if plan is None:
-        plan = Plan(_torch_code(x), GEMM_F32, x.device.index or 0)
-    epi, stride_bias = _group_epilogue(bias, groups, N, relu, out)
-    gemm_run_grouped(plan.handle, lb, groups, M, N, K, alpha, x.data_ptr(), lda, w.data_ptr(), ldb,
-                     w.stride(0) if groups > 1 else 0, out.data_ptr(), _rows(out, "out"), offsets.data_ptr(), epi,
-                     stride_bias, _stream_of(x, stream))
-    return out
-
-
-def grouped_weight_grad(x, dy, offsets, *, alpha: float = 1.0, accumulate: bool = False, out=None, out_dtype=None,
-                        plan: Optional[Plan] = None, stream=None):
-    """out[g] = alpha * x[rows of g].T @ dy[rows of g] (+ out[g] if accumulate): the
-    weight gradient of grouped_matmul (gemm_run_grouped_wgrad); an empty group
-    gives zeros.
-
-    x: [rows, K], dy: [rows, N], float16 or bfloat16; offsets as for
-    grouped_matmul.  out: [groups, K, N] with contiguous rows; accumulate needs
-    `out` and a plan whose c_dtype is out's type (made here if none is given).
-    out_dtype defaults to x's.  Returns `out`."""
-    import torch
-    if x.dim() != 2 or dy.dim() != 2 or x.shape[0] != dy.shape[0] or x.dtype != dy.dtype:
-        raise ValueError("x must be [rows, K] and dy [rows, N] of the same type")
-    rows, M, N, groups = x.shape[0], x.shape[1], dy.shape[1], offsets.shape[0] - 1
-    _check_offsets(offsets, groups)
-    _same_device(x, dy, offsets, out)
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs out")
-        out = torch.empty((groups, M, N), dtype=out_dtype or x.dtype, device=x.device)
-    elif tuple(out.shape) != (groups, M, N) or (out.stride(2) != 1 and N > 1):
-        raise ValueError("out must be [groups, K, N] with contiguous rows")
-    if plan is None:
-        plan = Plan(_torch_code(x), _torch_code(out), x.device.index or 0)
-    if accumulate and plan.c_dtype != _torch_code(out):
-        raise ValueError("accumulate needs a plan whose c_dtype is out's type")
-    ldd = max(out.stride(1), N, 1)
-    stride_d = out.stride(0) if groups > 1 else M * ldd
-    gemm_run_grouped_wgrad(plan.handle, groups, M, N, rows, alpha, x.data_ptr(), _rows(x, "x"), dy.data_ptr(),
-                           _rows(dy, "dy"), 1.0 if accumulate else 0.0, out.data_ptr() if accumulate else None, ldd,
-                           stride_d, out.data_ptr(), ldd, stride_d, offsets.data_ptr(), _torch_code(out),
-                           _stream_of(x, stream))
-    return out
-
-
-def quantize_q4(w, group_size: int, *, zero_points: bool = False, scale_dtype=None):
-    """Round-to-nearest 4-bit weights for q4_matmul: (q, scales, zeros) of w
-    [..., N, K] (K a multiple of group_size), zeros None unless zero_points.  One
-    scale per row and group_size entries of K; done once per weight matrix."""
-    import torch
-    if group_size <= 0 or group_size % 32 or w.shape[-1] % group_size:
-        raise ValueError("group_size must be a multiple of 32 that divides K")
-    scale_dtype = scale_dtype or w.dtype
-    g = w.float().unflatten(-1, (-1, group_size))
-    if zero_points:
-        lo, hi = g.amin(-1).clamp(max=0), g.amax(-1).clamp(min=0)
-        scales = ((hi - lo) / 15).to(scale_dtype)
-    else:
-        scales = (g.abs().amax(-1) / 7).to(scale_dtype)
-    div = torch.where(scales == 0, 1.0, scales.float())[..., None]
-    zeros = torch.round(-lo[..., None] / div).clamp(0, 15) if zero_points else torch.full_like(div, 8)
-    v = (torch.round(g / div) + zeros).clamp(0, 15).flatten(-2).to(torch.uint8)
-    return v[..., 0::2] | (v[..., 1::2] << 4), scales, zeros[..., 0].to(torch.uint8) if zero_points else None
-
-
-def q4_matmul(x, q, scales, group_size: int, *, zeros=None, offsets=None, alpha: float = 1.0, bias=None,
-              relu: bool = False, out=None, out_dtype=None, plan: Optional[Plan] = None, stream=None):
-    """out = act(alpha * x @ w.T + bias) with 4-bit weights (gemm_run_q4):
-    w[n, k] = scales[n, k // group_size] * (q[n, k] - zeros[n, k // group_size]).
-
-    x: [rows, K] float16 or bfloat16; q: uint8 [N, ceil(K / 2)], two weights a
-    byte, the even k in the low half; scales: [N, ceil(K / group_size)] of a
-    floating type; zeros: uint8 like scales, or None for 8.  For experts each of
-    them has a leading dimension [groups] and `offsets` gives every group's rows
-    as for grouped_matmul.  bias: [N] or [groups, N].  Returns `out`."""
-    import torch
-    groups = q.shape[0] if q.dim() == 3 else 1
-    if x.dim() != 2 or q.dim() not in (2, 3) or q.dtype != torch.uint8:
-        raise ValueError("x must be [rows, K] and q uint8 [N, K / 2] or [groups, N, K / 2]")
-    if offsets is None and groups != 1:
-        raise ValueError("experts' weights need offsets")
-    (M, K), N = x.shape, q.shape[-2]
-    if group_size <= 0 or group_size % 32:
-        raise ValueError("group_size must be a positive multiple of 32")
-    kg = -(-K // group_size)
-    if q.shape[-1] != (K + 1) // 2 or scales.shape != q.shape[:-1] + (kg,) or \
-            (zeros is not None and (zeros.shape != scales.shape or zeros.dtype != torch.uint8)):
-        raise ValueError("q, scales or zeros do not match x and group_size")
-    for t in (q, scales, zeros):
-        if t is not None and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError("q, scales and zeros need contiguous rows")
-    if offsets is not None:
-        _check_offsets(offsets, groups)
-    _same_device(x, q, scales, zeros, offsets, bias, out)
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or x.dtype, device=x.device)
-    elif tuple(out.shape) != (M, N):
-        raise ValueError("out must be [rows, N]")
-    if plan is None:
-        plan = Plan(_torch_code(x), GEMM_F32, x.device.index or 0)
-    epi, stride_bias = _group_epilogue(bias, groups, N, relu, out)
-    ex = groups > 1
-    B = gemm_q4_t(q.data_ptr(), max(q.stride(-2), q.shape[-1]), q.stride(0) if ex else 0, scales.data_ptr(),
-                  _torch_code(scales), max(scales.stride(-2), kg), scales.stride(0) if ex else 0,
-                  zeros.data_ptr() if zeros is not None else None,
-                  max(zeros.stride(-2), kg) if zeros is not None else 0,
-                  zeros.stride(0) if ex and zeros is not None else 0, group_size)
-    gemm_run_q4(plan.handle, groups, M, N, K, alpha, x.data_ptr(), _rows(x, "x"), B, out.data_ptr(),
-                _rows(out, "out"), offsets.data_ptr() if offsets is not None else None, epi, stride_bias,
-                _stream_of(x, stream))
-    return out
-
-
-def orthogonalize(g, *, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, out=None,
-                  out_dtype=None, plan: Optional[Plan] = None, stream=None):
-    """Newton-Schulz steps X = a X + (b X X' + c (X X')^2) X from X = g / (||g|| + eps)
-    (gemm_orthogonalize): the orthogonalised update of a weight matrix, or of a
-    stack of them.
-
-    g: [m, n] or [batch, m, n], float32, float16 or bfloat16, each matrix row-
-    or column-major.  out has g's shape and out_dtype (bfloat16 by default).
-    Returns `out`."""
-    import torch
-    if g.dim() not in (2, 3):
-        raise ValueError("g must be [m, n] or [batch, m, n]")
-    by_columns = g.stride(-1) != 1 and g.stride(-2) == 1    # then the transposes are row-major
-    if out is None:
-        out = torch.empty(g.mT.shape if by_columns else g.shape, dtype=out_dtype or torch.bfloat16, device=g.device)
-        out = out.mT if by_columns else out
-    elif out.shape != g.shape:
-        raise ValueError("out must have g's shape")
-    _same_device(g, out)
-    gv, ov = (g, out) if g.dim() == 3 else (g[None], out[None])
-    if by_columns:
-        gv, ov = gv.transpose(1, 2), ov.transpose(1, 2)
-    batch, m, n = gv.shape
-    for t, name in ((gv, "g"), (ov, "out")):
-        if (t.stride(2) != 1 and n > 1) or (m > 1 and t.stride(1) < n):
-            raise ValueError(f"{name} must have contiguous rows (or columns) like the other")
-    ldd = max(ov.stride(1), n, 1)
-    if plan is None:
-        plan = Plan(_torch_code(g), GEMM_F32, g.device.index or 0)
-    gemm_orthogonalize(plan.handle, batch, m, n, steps, coeffs, eps, gv.data_ptr(), max(gv.stride(1), n, 1),
-                       gv.stride(0) if batch > 1 else 0, ov.data_ptr(), ldd, ov.stride(0) if batch > 1 else m * ldd,
-                       _torch_code(out), _stream_of(g, stream))
-    return out
+def __getattr__(name):
+    if name in _EXPERT:
+        from . import expert
+        globals().update({n: getattr(expert, n) for n in _EXPERT})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -124,7 +124,6 @@ int ortho_slots(int64_t m, int64_t n);   // partial sums per matrix
 // X = G / (||G|| + eps) times `scale`, in fp16; partials: batch * ortho_slots(m, n) floats.
 cudaError_t launch_ortho_input(const OrthoInput& in, int dtype, int64_t batch, float* partials, float eps, float scale,
                                __half* x, int64_t ldx, int64_t stride_x, cudaStream_t stream);
-cudaError_t launch_identity(__half* d, int64_t m, int64_t ld, cudaStream_t stream);
 // D (M x N) = scale * X (or its transpose), cast.
 cudaError_t launch_unscale(const __half* x, int64_t batch, int64_t M, int64_t N, int64_t ldx, int64_t stride_x,
                            int transpose, float scale, void* D, int dtype, int64_t ldd, int64_t stride_d,

@@ -1398,27 +1398,6 @@ gemm_status_t gemm_run_host(gemm_plan_t plan, gemm_layout_t la, gemm_layout_t lb
 
 }  // extern "C"
 
-gemm_status_t gemmlib::run_product(gemm_plan* plan, gemm_dtype_t ab, gemm_dtype_t c, gemm_dtype_t out, gemm_layout_t la,
-                                   gemm_layout_t lb, int64_t M, int64_t N, int64_t K, double alpha, const void* A,
-                                   int64_t lda, int64_t stride_a, const void* B, int64_t ldb, int64_t stride_b,
-                                   double beta, const void* C, int64_t ldc, int64_t stride_c, void* D, int64_t ldd,
-                                   int64_t stride_d, int64_t batch, gemm_stream_t stream) {
-  const gemm_dtype_t plan_ab = plan->ab, plan_c = plan->c;
-  const gemm_kernel_t forced = plan->forced;
-  plan->ab = ab;
-  plan->c = c;
-  plan->forced = GEMM_KERNEL_AUTO;
-  gemm_epilogue_t epi{};
-  epi.out_dtype = out;
-  const gemm_status_t s =
-      gemm_run_strided_batched(plan, la, lb, M, N, K, alpha, A, lda, stride_a, B, ldb, stride_b, beta, C, ldc, stride_c,
-                               D, ldd, stride_d, batch, &epi, 0, stream);
-  plan->ab = plan_ab;
-  plan->c = plan_c;
-  plan->forced = forced;
-  return s;
-}
-
 // ===========================================================================
 // gemm_run_s8_noalloc: the int8 path with its fp16 staging in a fixed device
 // array instead of plan-owned, allocated scratch (see include/gemm.h).

@@ -157,14 +157,4 @@ cudaError_t launch_unscale(const __half* x, int64_t batch, int64_t M, int64_t N,
   return cudaGetLastError();
 }
 
-__global__ void identity_kernel(__half* d, int64_t m, int64_t ld) {
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < m * ld; i += (int64_t)gridDim.x * blockDim.x)
-    d[i] = __float2half_rn(i / ld == i % ld ? 1.0f : 0.0f);
-}
-
-cudaError_t launch_identity(__half* d, int64_t m, int64_t ld, cudaStream_t stream) {
-  identity_kernel<<<(unsigned)std::min<int64_t>((m * ld + 255) / 256, 1216), 256, 0, stream>>>(d, m, ld);
-  return cudaGetLastError();
-}
-
 }  // namespace gemmlib

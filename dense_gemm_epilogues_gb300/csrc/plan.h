@@ -89,15 +89,6 @@ void log_config(const char* entry, int64_t M, int64_t N, int64_t K, int64_t batc
 // Grow the plan's scratch (ws) to at least `bytes`, in stream order.
 gemm_status_t ensure_ws(gemm_plan* plan, size_t bytes, cudaStream_t stream);
 
-// A strided batch of products for an operator that is built of them: D = alpha *
-// op(A) * op(B) + beta * C on the kernels of gemm_run, with operand types of its
-// own (`ab`, `c`, `out`) in place of the plan's.
-gemm_status_t run_product(gemm_plan* plan, gemm_dtype_t ab, gemm_dtype_t c, gemm_dtype_t out, gemm_layout_t la,
-                          gemm_layout_t lb, int64_t M, int64_t N, int64_t K, double alpha, const void* A, int64_t lda,
-                          int64_t stride_a, const void* B, int64_t ldb, int64_t stride_b, double beta, const void* C,
-                          int64_t ldc, int64_t stride_c, void* D, int64_t ldd, int64_t stride_d, int64_t batch,
-                          gemm_stream_t stream);
-
 // A row-pitched tensor of 16-bit elements (inner elements contiguous, `ld`
 // elements between rows of the outer dimension) with a third, outermost
 // dimension: `nbatch` problems `bstride` elements apart (one problem when

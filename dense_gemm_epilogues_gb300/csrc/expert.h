@@ -50,10 +50,13 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* tm) {
 #endif
 
 // What seg_kernel.cu computes (its head says how).
-enum { SEG_TOKENS = 0, SEG_WGRAD = 1, SEG_SYM = 2, SEG_DENSE = 3 };
+enum { SEG_TOKENS = 0, SEG_WGRAD = 1, SEG_CHAIN = 2 };
+// CHAIN's maps in tmB, beside E as M side in tmA: both X buffers as M side of E, as N side
+// of E, as N side of F X; F as M side; E as N side.
+enum { CHAIN_XK = 0, CHAIN_XB = 2, CHAIN_XN = 4, CHAIN_F = 6, CHAIN_EB = 7, SEG_MAPS = 8 };
 struct SegParams {
   CUtensorMap tmA;              // M side (WGRAD: the template of every group's map)
-  CUtensorMap tmB[5];           // N side; TOKENS: boxes of 128, 64, 32, 16 and 8 rows
+  CUtensorMap tmB[SEG_MAPS];    // N side; TOKENS: boxes of 128, 64, 32, 16 and 8 rows
   Groups groups;                // TOKENS, WGRAD
   const CUtensorMap* group_maps;   // WGRAD: two per group, made by launch_wgrad_maps
   uint64_t a_base, b_base;      // WGRAD: the operands' addresses and row pitches in bytes
@@ -63,9 +66,18 @@ struct SegParams {
   int32_t tiles_m, tiles_n;     // 128- or 256-wide tiles
   int32_t tiles_per_group, num_tiles;
   int32_t a_batched;            // TOKENS: the M side has one slice per group
-  int32_t store_t;              // DENSE: store D transposed
   uint32_t idesc;               // instruction descriptor without N
-  float shift;                  // SYM: subtracted on the diagonal
+  // CHAIN: X is M x N, E and F are M x M; tiles_per_group tiles of E or F (bns columns
+  // each), tiles_m x tiles_n of X (bn columns each) per matrix; num_tiles over all steps.
+  int32_t batch, steps, bns, bn;
+  int32_t store_t;              // the result (epi.D) is stored transposed
+  int32_t* counters;            // 3 * steps * batch * tiles_m, zero at the start
+  struct {
+    __half *x[2], *e, *f;       // step s reads x[s % 2]
+    int64_t ldx, stride_x, lde, stride_e;
+    float a[2], b[2], c;        // early steps, the last two (see gemm_orthogonalize)
+    float inv_scale;            // X is held times 1 / inv_scale
+  } chain;
   EpiParams epi;
   int32_t* err;
   uint64_t timeout_ns;
@@ -122,8 +134,10 @@ struct OrthoInput {
 };
 int ortho_slots(int64_t m, int64_t n);   // partial sums per matrix
 // X = G / (||G|| + eps) times `scale`, in fp16; partials: batch * ortho_slots(m, n) floats.
+// counters[0 .. num_counters) are set to zero.
 cudaError_t launch_ortho_input(const OrthoInput& in, int dtype, int64_t batch, float* partials, float eps, float scale,
-                               __half* x, int64_t ldx, int64_t stride_x, cudaStream_t stream);
+                               __half* x, int64_t ldx, int64_t stride_x, int32_t* counters, int64_t num_counters,
+                               cudaStream_t stream);
 // D (M x N) = scale * X (or its transpose), cast.
 cudaError_t launch_unscale(const __half* x, int64_t batch, int64_t M, int64_t N, int64_t ldx, int64_t stride_x,
                            int transpose, float scale, void* D, int dtype, int64_t ldd, int64_t stride_d,

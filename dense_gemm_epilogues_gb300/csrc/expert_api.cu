@@ -2,6 +2,7 @@
 // include/gemm.h): argument checks, workspaces and launches.  Host code only.
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 
@@ -139,54 +140,6 @@ gemm_status_t tokens_product(gemm_plan* plan, const Groups& groups, int64_t M, i
   if (launch_seg(p, SEG_TOKENS, cg, w_mn, workers, stream) != cudaSuccess) return GEMM_ERR_CUDA;
   plan->last = seg_config(cg, tiles, workers);
   log_config(entry, M, N, K, groups.count, plan->last);
-  return GEMM_OK;
-}
-
-// One product of the Newton-Schulz steps, on fp16 matrices: SEG_SYM D = alpha A A' + beta C -
-// shift I (A: M x K, B the same matrix), SEG_DENSE D = alpha A B + beta C (A: M x K, B: K x N),
-// stored transposed if asked.
-gemm_status_t ortho_product(gemm_plan* plan, int mode, int64_t batch, int64_t M, int64_t N, int64_t K, double alpha,
-                            const void* A, int64_t lda, int64_t sa, const void* B, int64_t ldb, int64_t sb, double beta,
-                            const void* C, int64_t ldc, int64_t sc, void* D, gemm_dtype_t out, int64_t ldd, int64_t sd,
-                            float shift, bool store_t, cudaStream_t stream) {
-  SegParams p;
-  std::memset(&p, 0, sizeof(p));
-  int cg = plan->pair_clusters > 0 && M > 128 ? 2 : 1;
-  if (const char* env = std::getenv("GEMM_ORTHO_CG")) cg = std::atoi(env);
-  const int64_t tm = (M + 128 * cg - 1) / (128 * cg), tn = (N + 128 * cg - 1) / (128 * cg);
-  const int64_t per = mode == SEG_SYM ? tm * (tm + 1) / 2 : tm * tn, tiles = batch * per;
-  if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
-  const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  bool ok = encode_3d(&p.tmA, dt, A, K, M, lda, batch, sa, TC_BK, 128);
-  if (mode == SEG_SYM) p.tmB[0] = p.tmA;
-  else ok = ok && encode_3d(&p.tmB[0], dt, B, N, K, ldb, batch, sb, 64, 2 * TC_BK);
-  if (!ok) return GEMM_ERR_CUDA;
-  p.M = M;
-  p.N = (int32_t)N;
-  p.K = (int32_t)K;
-  p.tiles_m = (int32_t)tm;
-  p.tiles_n = (int32_t)tn;
-  p.tiles_per_group = (int32_t)per;
-  p.num_tiles = (int32_t)tiles;
-  p.store_t = store_t ? 1 : 0;
-  p.idesc = make_idesc(false, 0, false, mode == SEG_DENSE, 128 * cg);
-  p.shift = shift;
-  p.epi = epilogue_of(nullptr, out, alpha, D, ldd);
-  if (batch > 1 && (sd * dtype_bytes(out)) % 16 != 0) p.epi.vec_d = 0;
-  p.epi.stride_d = sd;
-  p.epi.beta = (float)beta;
-  p.epi.read_c = beta != 0.0 ? 1 : 0;
-  p.epi.C = C;
-  p.epi.ldc = ldc;
-  p.epi.c_dtype = GEMM_F16;
-  p.epi.stride_c = sc;
-  p.epi.vec_c = 1;   // the matrices in scratch start on 16 bytes, and so do their rows
-  p.err = plan->d_err;
-  p.timeout_ns = plan->timeout_ns;
-  const int workers = workers_of(plan, cg, tiles);
-  if (launch_seg(p, mode, cg, false, workers, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-  plan->last = seg_config(cg, tiles, workers);
-  log_config(mode == SEG_SYM ? "ortho_sym" : "ortho_dense", M, N, K, batch, plan->last);
   return GEMM_OK;
 }
 
@@ -420,47 +373,88 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   const int64_t ldx = (n + 7) / 8 * 8, lde = (m + 7) / 8 * 8;
   const int64_t sx = m * ldx, se = m * lde;
   const size_t xb = align_up((size_t)(batch * sx) * 2, 256), eb = align_up((size_t)(batch * se) * 2, 256);
+  int cg = plan->pair_clusters > 0 && m > 128 ? 2 : 1;
+  int bns = 128 * cg, bn = 128 * cg;   // columns of a tile of E and F, and of X
+  if (const char* env = std::getenv("GEMM_ORTHO_TILE")) std::sscanf(env, "%d,%d,%d", &cg, &bns, &bn);
+  const int64_t bm = 128 * cg, tm = (m + bm - 1) / bm, tn = (n + bn - 1) / bn;
+  const int64_t per_sym = tm * (tm + 1) / 2 * (bm / bns), per_step = batch * (2 * per_sym + tm * tn);
+  if (per_step > kMaxTiles / std::max(1, steps)) return GEMM_ERR_UNSUPPORTED;
+  const int64_t num_counters = 3 * (int64_t)steps * batch * tm;
   const size_t sb = align_up((size_t)batch * ortho_slots(m, n) * sizeof(float), 256);
-  gemm_status_t s = ensure_ws(plan, 2 * xb + 2 * eb + sb, stream);
+  gemm_status_t s = ensure_ws(plan, 2 * xb + 2 * eb + sb + (size_t)num_counters * sizeof(int32_t), stream);
   if (s != GEMM_OK) return s;
   char* ws = static_cast<char*>(plan->ws);
   __half* X[2] = {reinterpret_cast<__half*>(ws), reinterpret_cast<__half*>(ws + xb)};
   __half* E = reinterpret_cast<__half*>(ws + 2 * xb);
   __half* F = reinterpret_cast<__half*>(ws + 2 * xb + eb);
   float* sums = reinterpret_cast<float*>(ws + 2 * xb + 2 * eb);
+  int32_t* counters = reinterpret_cast<int32_t*>(ws + 2 * xb + 2 * eb + sb);
   // fp16 keeps 11 bits; entries of X are at most ~1 and as small as 1 / sqrt(m n), so
   // they are held times 256, which keeps the small ones out of fp16's subnormals.
-  const double scale = 256.0;
+  const float scale = 256.0f;
   const int es = dtype_bytes(plan->ab);
   const OrthoInput in{G, m, n, ldg, stride_g, tall ? 1 : 0,
                       aligned16(G) && (ldg * es) % 16 == 0 && (batch == 1 || (stride_g * es) % 16 == 0) ? 1 : 0};
-  if (launch_ortho_input(in, plan->ab, batch, sums, (float)eps, (float)scale, X[0], ldx, sx, stream) != cudaSuccess)
+  if (launch_ortho_input(in, plan->ab, batch, sums, (float)eps, scale, X[0], ldx, sx, counters, num_counters, stream) !=
+      cudaSuccess)
     return GEMM_ERR_CUDA;
   if (steps == 0)
-    return launch_unscale(X[0], batch, M, N, ldx, sx, tall, (float)(1.0 / scale), D, out_dtype, ldd, stride_d, stream) ==
+    return launch_unscale(X[0], batch, M, N, ldx, sx, tall, 1.0f / scale, D, out_dtype, ldd, stride_d, stream) ==
                    cudaSuccess
                ? GEMM_OK
                : GEMM_ERR_CUDA;
-  for (int k = 0; k < steps; ++k) {
-    // E = X X' - h I with h = 1 once the singular values have come near one (the
-    // last two steps): E is then small and its rounding with it.  With X X' = E + h I,
-    //   a X + (b X X' + c (X X')^2) X = (a + b h + c h^2) X + ((b + 2 c h) E + c E^2) X.
-    const double h = k >= steps - 2 ? 1.0 : 0.0;
-    const double c = coeffs[2], b = coeffs[1] + 2 * c * h, a = coeffs[0] + coeffs[1] * h + c * h * h;
-    const bool last = k == steps - 1;
-    const double f = last ? 1.0 / scale : 1.0;
-    s = ortho_product(plan, SEG_SYM, batch, m, m, n, 1.0 / (scale * scale), X[0], ldx, sx, X[0], ldx, sx, 0.0, nullptr, 0,
-                      0, E, GEMM_F16, lde, se, (float)h, false, stream);
-    if (s == GEMM_OK)
-      s = ortho_product(plan, SEG_SYM, batch, m, m, m, c, E, lde, se, E, lde, se, b, E, lde, se, F, GEMM_F16, lde, se,
-                        0.0f, false, stream);
-    if (s == GEMM_OK)
-      s = ortho_product(plan, SEG_DENSE, batch, m, n, m, f, F, lde, se, X[0], ldx, sx, a * f, X[0], ldx, sx,
-                        last ? D : X[1], last ? out_dtype : GEMM_F16, last ? ldd : ldx, last ? stride_d : sx, 0.0f,
-                        last && tall, stream);
-    if (s != GEMM_OK) return s;
-    std::swap(X[0], X[1]);
+  SegParams p;
+  std::memset(&p, 0, sizeof(p));
+  const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  bool ok = encode_3d(&p.tmA, dt, E, m, m, lde, batch, se, TC_BK, 128) &&
+            encode_3d(&p.tmB[CHAIN_F], dt, F, m, m, lde, batch, se, TC_BK, 128);
+  ok = ok && encode_3d(&p.tmB[CHAIN_EB], dt, E, m, m, lde, batch, se, TC_BK, (uint32_t)(bns / cg));
+  for (int i = 0; i < 2; ++i)
+    ok = ok && encode_3d(&p.tmB[CHAIN_XK + i], dt, X[i], n, m, ldx, batch, sx, TC_BK, 128) &&
+         encode_3d(&p.tmB[CHAIN_XB + i], dt, X[i], n, m, ldx, batch, sx, TC_BK, (uint32_t)(bns / cg)) &&
+         encode_3d(&p.tmB[CHAIN_XN + i], dt, X[i], n, m, ldx, batch, sx, 64, 2 * TC_BK);
+  if (!ok) return GEMM_ERR_CUDA;
+  p.M = m;
+  p.N = (int32_t)n;
+  p.tiles_m = (int32_t)tm;
+  p.tiles_n = (int32_t)tn;
+  p.tiles_per_group = (int32_t)per_sym;
+  p.num_tiles = (int32_t)(per_step * steps);
+  p.idesc = make_idesc(false, 0, false, false, 128 * cg);
+  p.batch = (int32_t)batch;
+  p.steps = steps;
+  p.bns = bns;
+  p.bn = bn;
+  p.store_t = tall ? 1 : 0;
+  p.counters = counters;
+  for (int i = 0; i < 2; ++i) p.chain.x[i] = X[i];
+  p.chain.e = E;
+  p.chain.f = F;
+  p.chain.ldx = ldx;
+  p.chain.stride_x = sx;
+  p.chain.lde = lde;
+  p.chain.stride_e = se;
+  // E = X X' - h I with h = 1 once the singular values have come near one (the last two
+  // steps): E is then small and its rounding with it.  With X X' = E + h I,
+  //   a X + (b X X' + c (X X')^2) X = (a + b h + c h^2) X + ((b + 2 c h) E + c E^2) X.
+  for (int h = 0; h < 2; ++h) {
+    p.chain.a[h] = (float)(coeffs[0] + coeffs[1] * h + coeffs[2] * h);
+    p.chain.b[h] = (float)(coeffs[1] + 2 * coeffs[2] * h);
   }
+  p.chain.c = (float)coeffs[2];
+  p.chain.inv_scale = 1.0f / scale;
+  p.epi = epilogue_of(nullptr, out_dtype, 1.0, D, ldd);
+  if (batch > 1 && (stride_d * dtype_bytes(out_dtype)) % 16 != 0) p.epi.vec_d = 0;
+  p.epi.stride_d = stride_d;
+  p.epi.read_c = 1;
+  p.epi.c_dtype = GEMM_F16;
+  p.epi.vec_c = 1;   // the matrices in scratch start on 16 bytes, and so do their rows
+  p.err = plan->d_err;
+  p.timeout_ns = plan->timeout_ns;
+  const int workers = workers_of(plan, cg, batch * std::max(per_sym, tm * tn));
+  if (launch_seg(p, SEG_CHAIN, cg, false, workers, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  plan->last = seg_config(cg, p.num_tiles, workers);
+  log_config("orthogonalize", m, n, steps, batch, plan->last);
   return GEMM_OK;
 }
 

@@ -63,7 +63,11 @@ __device__ __forceinline__ float block_sum(float s) {
 
 // partials[matrix][slot]: the squares of tiles slot, slot + slots, ... of X.
 template <typename T>
-__global__ void __launch_bounds__(256) sumsq_kernel(const OrthoInput in, float* partials) {
+__global__ void __launch_bounds__(256) sumsq_kernel(const OrthoInput in, float* partials, int32_t* counters,
+                                                    int64_t num_counters) {
+  for (int64_t i = (blockIdx.y * (int64_t)gridDim.x + blockIdx.x) * 256 + threadIdx.x; i < num_counters;
+       i += (int64_t)gridDim.x * gridDim.y * 256)
+    counters[i] = 0;
   __shared__ float tile[TILE][TILE + 1];
   const T* g = static_cast<const T*>(in.g) + blockIdx.y * in.stride;
   const int64_t tiles_n = (in.n + TILE - 1) / TILE, tiles = (in.m + TILE - 1) / TILE * tiles_n;
@@ -126,10 +130,11 @@ __global__ void __launch_bounds__(256) unscale_kernel(const __half* x, int64_t M
 
 template <typename T>
 cudaError_t launch_ortho_input(const OrthoInput& in, int64_t batch, float* partials, float eps, float scale, __half* x,
-                               int64_t ldx, int64_t stride_x, cudaStream_t stream) {
+                               int64_t ldx, int64_t stride_x, int32_t* counters, int64_t num_counters,
+                               cudaStream_t stream) {
   const int64_t tiles = ((in.m + TILE - 1) / TILE) * ((ldx + TILE - 1) / TILE);
   const int slots = ortho_slots(in.m, in.n);
-  sumsq_kernel<T><<<dim3((unsigned)slots, (unsigned)batch), 256, 0, stream>>>(in, partials);
+  sumsq_kernel<T><<<dim3((unsigned)slots, (unsigned)batch), 256, 0, stream>>>(in, partials, counters, num_counters);
   normalize_kernel<T><<<dim3((unsigned)std::min<int64_t>(tiles, 1216), (unsigned)batch), 256, 0, stream>>>(
       in, partials, slots, eps, scale, x, ldx, stride_x);
   return cudaGetLastError();
@@ -142,10 +147,11 @@ int ortho_slots(int64_t m, int64_t n) {
 }
 
 cudaError_t launch_ortho_input(const OrthoInput& in, int dtype, int64_t batch, float* partials, float eps, float scale,
-                               __half* x, int64_t ldx, int64_t stride_x, cudaStream_t stream) {
-  if (dtype == GEMM_F32) return launch_ortho_input<float>(in, batch, partials, eps, scale, x, ldx, stride_x, stream);
-  if (dtype == GEMM_F16) return launch_ortho_input<__half>(in, batch, partials, eps, scale, x, ldx, stride_x, stream);
-  return launch_ortho_input<__nv_bfloat16>(in, batch, partials, eps, scale, x, ldx, stride_x, stream);
+                               __half* x, int64_t ldx, int64_t stride_x, int32_t* counters, int64_t num_counters,
+                               cudaStream_t stream) {
+  if (dtype == GEMM_F32) return launch_ortho_input<float>(in, batch, partials, eps, scale, x, ldx, stride_x, counters, num_counters, stream);
+  if (dtype == GEMM_F16) return launch_ortho_input<__half>(in, batch, partials, eps, scale, x, ldx, stride_x, counters, num_counters, stream);
+  return launch_ortho_input<__nv_bfloat16>(in, batch, partials, eps, scale, x, ldx, stride_x, counters, num_counters, stream);
 }
 
 cudaError_t launch_unscale(const __half* x, int64_t batch, int64_t M, int64_t N, int64_t ldx, int64_t stride_x,

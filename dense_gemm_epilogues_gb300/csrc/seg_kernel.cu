@@ -2,9 +2,8 @@
 //   TOKENS  D[r, :] = act(alpha * A[r, :] * op(B_g) + bias_g) for the rows r of each
 //           group g (rows found on the device);
 //   WGRAD   D_g = alpha * A_g' * B_g + beta * C_g, the sum over the rows of group g;
-//   SYM     D = alpha * X * X' + beta * C - shift * I, symmetric: tiles on and below
-//           the diagonal are computed, each also stored transposed;
-//   DENSE   D = alpha * A * B + beta * C, optionally stored transposed.
+//   CHAIN   the products of the Newton-Schulz steps, all of them in one launch:
+//           E = X X' - h I,  F = c E E' + b E,  X <- F X + a X  for every matrix of a batch.
 //
 // One structure serves them all, on single CTAs (CG = 1, tiles of 128 x 128) and on
 // CTA pairs (CG = 2, 256 x 256): a producer thread streams 64-deep slabs of both
@@ -26,7 +25,22 @@
 // the device by wgrad_maps_kernel): the last block's rows past the group read as
 // zero, whatever other rows hold.
 //
-// Every mbarrier wait is bounded, as in tc_kernel.cu.
+// CHAIN: E and F are symmetric, so only tiles on and below the diagonal are computed
+// and each is stored twice, as it is and transposed.  The tiles of all phases form one
+// list (step by step, product by product, matrix by matrix) that the workers take in
+// turn.  A tile waits, per 256-row (CG = 1: 128-row) block of the matrices that it
+// reads, for a counter of the finished tiles of that block row:
+//   E(i, j) waits for rows i and j of X (the last step's F X tiles),
+//   F(i, j) for rows i and j of E, and F X (i, n) for row i of F -- which has needed all
+//   of E, and that all of X.
+// The same order makes every buffer free when it is written again: whoever writes a
+// tile of X, E or F has waited, through that chain, for every reader of its old value.
+// Every wait is for earlier tiles of the list only, and all workers are resident (a
+// cooperative launch), so the earliest unfinished tile can always run.  One launch in
+// place of three per step saves the launches' fixed cost (6-8 us each, all of a small
+// matrix's time) and lets the matrices of a batch fill each other's last waves.
+//
+// Every wait is bounded, as in tc_kernel.cu.
 #include "expert.h"
 
 namespace gemmlib {
@@ -39,10 +53,9 @@ constexpr int OPERAND_BYTES = SLABS * SLAB_BYTES;     // one operand of a stage
 constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;        // [M side][N side]
 constexpr uint32_t MN_BOX_BYTES = 64 * 2 * SLABS * TC_BK;   // MN-major box: 64 wide, a stage deep
 constexpr int EPI_WARPS = 8;                          // two per tensor-memory lane quarter
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TURN_BYTES = 2048;                      // an epilogue warp's turn-around buffer
 constexpr int NUM_BARS = 2 * STAGES + 5;
-constexpr size_t FIXED_SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_WARPS * TURN_BYTES + NUM_BARS * 8 + 16;
+constexpr size_t FIXED_SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_WARPS * TURN_BYTES + NUM_BARS * 8 + 16 + EPI_WARPS * 4;
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t user_timeout_ns) {
   const uint64_t timeout_ns = user_timeout_ns > 1000000000ull ? user_timeout_ns : 1000000000ull;
@@ -77,8 +90,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 
 // 32 rows of 64 bytes (lane: its row's 16 words) stored as whole sectors, 8 rows
-// per instruction; `esize`-byte elements, rows r < rows, columns j < cols (64 /
-// esize of them when `vec`, which needs 16-byte aligned rows).
+// per instruction; ES-byte elements, rows r < rows, columns j < cols.  vec: rows are
+// 16-byte aligned and cols is a multiple of 16 bytes.
 template <int ES>
 __device__ __forceinline__ void store_rows64(char* D, int64_t pitch, int rows, int cols, const uint32_t (&w)[16],
                                              uint32_t turn, bool vec) {
@@ -94,12 +107,12 @@ __device__ __forceinline__ void store_rows64(char* D, int64_t pitch, int rows, i
     for (int i = 0; i < 4; ++i) {
       const int r = 8 * i + (lane >> 2);
       const uint4 v = lds128(turn + (uint32_t)(r * 64 + ((pl ^ ((r >> 1) & 3)) << 4)));
-      if (r < rows) *reinterpret_cast<uint4*>(D + r * pitch + pl * 16) = v;
+      if (r < rows && pl * (16 / ES) < cols) *reinterpret_cast<uint4*>(D + r * pitch + pl * 16) = v;
     }
   } else {
     constexpr int PER = 64 / ES, RPI = 32 / PER;   // elements per row, rows per instruction
     const int j = lane % PER;
-#pragma unroll 4
+#pragma unroll 8
     for (int r = lane / PER; r < 32; r += RPI) {
       const uint32_t a = turn + (uint32_t)(r * 64 + (((j * ES >> 4) ^ ((r >> 1) & 3)) << 4) + (j * ES & 15));
       if (r < rows && j < cols) {
@@ -121,7 +134,7 @@ __device__ __forceinline__ void store_rows64(char* D, int64_t pitch, int rows, i
 template <int DT>
 __device__ __forceinline__ void store_chunk(void* D, int64_t ldd, int64_t r0, int64_t c0, int rows, int cols,
                                             const float (&x)[32], uint32_t turn, bool vec) {
-  const bool v = vec && cols >= 32;
+  const bool v = vec && cols % (DT == GEMM_F32 ? 4 : 8) == 0;
   uint32_t w[16];
   if constexpr (DT == GEMM_F32) {
     char* d = reinterpret_cast<char*>(static_cast<float*>(D) + r0 * ldd + c0);
@@ -144,7 +157,7 @@ template <int DT>
 __device__ __forceinline__ void store_chunk_t(void* D, int64_t ldd, int64_t j0, int64_t r0, int rows_out, int cols_out,
                                               const float (&x)[32], uint32_t turn, bool vec) {
   const int lane = threadIdx.x & 31;
-  const bool v = vec && cols_out >= 32;
+  const bool v = vec && cols_out % (DT == GEMM_F32 ? 4 : 8) == 0;
   if constexpr (DT == GEMM_F32) {
     float* d = static_cast<float*>(D) + j0 * ldd + r0;
     if (!v) {
@@ -164,7 +177,8 @@ __device__ __forceinline__ void store_chunk_t(void* D, int64_t ldd, int64_t j0, 
       for (int i = 0; i < 4; ++i) {
         const int j = 4 * i + (lane >> 3);
         const uint4 q = lds128(turn + (uint32_t)(j * 128 + (lane & 7) * 16));
-        if (16 * h + j < rows_out) *reinterpret_cast<uint4*>(d + (16 * h + j) * ldd + (lane & 7) * 4) = q;
+        if (16 * h + j < rows_out && (lane & 7) * 4 < cols_out)
+          *reinterpret_cast<uint4*>(d + (16 * h + j) * ldd + (lane & 7) * 4) = q;
       }
     }
   } else {
@@ -197,78 +211,126 @@ __device__ __forceinline__ void store_chunk_t(void* D, int64_t ldd, int64_t j0, 
                                   __byte_perm(s.x, s.y, 0x5410), __byte_perm(s.z, s.w, 0x5410));
       const uint4 hi = make_uint4(__byte_perm(f.x, f.y, 0x7632), __byte_perm(f.z, f.w, 0x7632),
                                   __byte_perm(s.x, s.y, 0x7632), __byte_perm(s.z, s.w, 0x7632));
-      if (2 * p < rows_out) *reinterpret_cast<uint4*>(d + (2 * p) * ldd + o * 8) = lo;
-      if (2 * p + 1 < rows_out) *reinterpret_cast<uint4*>(d + (2 * p + 1) * ldd + o * 8) = hi;
+      if (2 * p < rows_out && o * 8 < cols_out) *reinterpret_cast<uint4*>(d + (2 * p) * ldd + o * 8) = lo;
+      if (2 * p + 1 < rows_out && o * 8 < cols_out) *reinterpret_cast<uint4*>(d + (2 * p + 1) * ldd + o * 8) = hi;
     }
   }
 }
 
-// x += beta * C for a chunk (lane r = row r): whole rows of 16-bit C turned around
-// through the buffer, other types or edges element by element.
-__device__ __forceinline__ void add_c(const EpiParams& e, const void* C, int64_t r0, int64_t c0, int rows, int cols,
-                                      float (&x)[32], uint32_t turn) {
+// beta * C of a chunk (lane r = row r), in two steps so that the loads run ahead of the
+// accumulator: whole rows of 16-bit C are held in registers as loaded (8 rows per
+// instruction) and turned around through the buffer when they are added; other types
+// and edges are read when they are added, by elements, whole rows per instruction.  All past L1: CHAIN's C was
+// written by other SMs during the launch that reads it.
+struct CChunk {
+  uint4 v[4];
+  bool held;
+};
+__device__ __forceinline__ void load_c(const EpiParams& e, const void* C, int64_t r0, int64_t c0, int rows, int cols,
+                                       CChunk& c) {
+  const int lane = threadIdx.x & 31, pl = lane & 3;
+  c.held = e.vec_c && cols % 8 == 0 && e.c_dtype != GEMM_F32;
+  if (!c.held) return;
+  const uint16_t* src = static_cast<const uint16_t*>(C) + (r0 + (lane >> 2)) * e.ldc + c0 + pl * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c.v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (8 * i + (lane >> 2) < rows && pl * 8 < cols) c.v[i] = __ldcg(reinterpret_cast<const uint4*>(src + 8 * i * e.ldc));
+  }
+}
+// x += beta * this lane's row of 16-bit C in the buffer.
+__device__ __forceinline__ void add_c16(const EpiParams& e, float (&x)[32], uint32_t turn) {
   const int lane = threadIdx.x & 31;
-  if (e.vec_c && cols >= 32 && e.c_dtype != GEMM_F32) {
-    const uint16_t* src = static_cast<const uint16_t*>(C) + r0 * e.ldc + c0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 c = lds128(turn + (uint32_t)(lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      float lo, hi;
+      if (e.c_dtype == GEMM_F16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
+        lo = f.x;
+        hi = f.y;
+      } else {
+        lo = __uint_as_float(w[h] << 16);
+        hi = __uint_as_float(w[h] & 0xffff0000u);
+      }
+      x[8 * q + 2 * h] = fmaf(e.beta, lo, x[8 * q + 2 * h]);
+      x[8 * q + 2 * h + 1] = fmaf(e.beta, hi, x[8 * q + 2 * h + 1]);
+    }
+  }
+}
+__device__ __forceinline__ void add_c(const EpiParams& e, const void* C, int64_t r0, int64_t c0, int rows, int cols,
+                                      const CChunk& ch, float (&x)[32], uint32_t turn) {
+  const int lane = threadIdx.x & 31;
+  if (ch.held) {
     const int pl = lane & 3;
-    uint4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows) v[i] = *reinterpret_cast<const uint4*>(src + r * e.ldc + pl * 8);
-    }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 8 * i + (lane >> 2);
-      sts128(turn + (uint32_t)(r * 64 + ((pl ^ ((r >> 1) & 3)) << 4)), v[i].x, v[i].y, v[i].z, v[i].w);
+      sts128(turn + (uint32_t)(r * 64 + ((pl ^ ((r >> 1) & 3)) << 4)), ch.v[i].x, ch.v[i].y, ch.v[i].z, ch.v[i].w);
     }
     __syncwarp();
+    add_c16(e, x, turn);
+  } else if (e.c_dtype == GEMM_F32) {
+    // 16 columns at a time: two rows per load instruction, turned around like 16-bit rows.
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 c = lds128(turn + (uint32_t)(lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)));
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    for (int h = 0; h < 2; ++h) {
+      const float* src = static_cast<const float*>(C) + r0 * e.ldc + c0 + 16 * h;
+      const int j = lane & 15;
+      __syncwarp();
+#pragma unroll 8
+      for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        const float v = r < rows && 16 * h + j < cols ? __ldcg(src + r * e.ldc + j) : 0.0f;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(turn + (uint32_t)(r * 64 + (((j >> 2) ^ ((r >> 1) & 3)) << 4) + (j & 3) * 4)), "f"(v) : "memory");
+      }
+      __syncwarp();
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        float lo, hi;
-        if (e.c_dtype == GEMM_F16) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-          lo = f.x;
-          hi = f.y;
-        } else {
-          lo = __uint_as_float(w[h] << 16);
-          hi = __uint_as_float(w[h] & 0xffff0000u);
-        }
-        x[8 * q + 2 * h] = fmaf(e.beta, lo, x[8 * q + 2 * h]);
-        x[8 * q + 2 * h + 1] = fmaf(e.beta, hi, x[8 * q + 2 * h + 1]);
+      for (int q = 0; q < 4; ++q) {
+        const uint4 c = lds128(turn + (uint32_t)(lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)));
+        x[16 * h + 4 * q + 0] = fmaf(e.beta, __uint_as_float(c.x), x[16 * h + 4 * q + 0]);
+        x[16 * h + 4 * q + 1] = fmaf(e.beta, __uint_as_float(c.y), x[16 * h + 4 * q + 1]);
+        x[16 * h + 4 * q + 2] = fmaf(e.beta, __uint_as_float(c.z), x[16 * h + 4 * q + 2]);
+        x[16 * h + 4 * q + 3] = fmaf(e.beta, __uint_as_float(c.w), x[16 * h + 4 * q + 3]);
       }
     }
-  } else if (lane < rows) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < cols) x[j] = fmaf(e.beta, load_as_float(C, e.c_dtype, (r0 + lane) * e.ldc + c0 + j), x[j]);
+  } else {
+    const uint16_t* src = static_cast<const uint16_t*>(C) + r0 * e.ldc + c0 + lane;
+    __syncwarp();
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      const uint16_t v = r < rows && lane < cols ? __ldcg(src + r * e.ldc) : (uint16_t)0;
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + (uint32_t)(r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2)), "h"(v) : "memory");
+    }
+    __syncwarp();
+    add_c16(e, x, turn);
   }
 }
 
 // ---------------------------------- tiles -----------------------------------
 
 struct Tile {
-  int e;          // group (TOKENS, WGRAD) or matrix of the batch (SYM, DENSE)
+  int e;          // group (TOKENS, WGRAD) or matrix of the batch (CHAIN)
   int m0, n0;     // first row of the M side and of the N side (TOKENS: the buffer's row)
   int n_valid;    // N-side rows that exist
   int n_mma;      // the MMA's N (a multiple of 16)
   int k;          // depth
+  int step, product;   // CHAIN: the step, and 0: E, 1: F, 2: X
 };
 
-// Shared-memory tables of TOKENS: the groups' first rows, row counts and first tiles.
+// Shared-memory tables: the groups' first rows and row counts (TOKENS, WGRAD) and first
+// tiles (TOKENS).
 struct GroupTable {
   int *lo, *cnt, *cum;
 };
 
 template <int MODE, int CG>
 struct Tiles {
-  static constexpr int BM = 128 * CG, BN = 128 * CG;
+  static constexpr int BM = 128 * CG;
+  static constexpr int BN = BM;   // TOKENS, WGRAD
   const SegParams& p;
   GroupTable g;
   int t, step, e;
@@ -293,31 +355,51 @@ struct Tiles {
       o.n_valid = min(per, cnt - tn * per);
       o.n_mma = (o.n_valid + 15) & ~15;
       o.k = p.K;
-    } else {
+    } else if constexpr (MODE == SEG_WGRAD) {
       if (t >= p.num_tiles) return false;
       o.e = t / p.tiles_per_group;
       const int local = t - o.e * p.tiles_per_group;
-      int tm, tn;
-      if (MODE == SEG_SYM) {
-        tm = (int)((sqrtf(8.0f * (float)local + 1.0f) - 1.0f) * 0.5f);
-        while ((tm + 1) * (tm + 2) / 2 <= local) ++tm;
-        while (tm * (tm + 1) / 2 > local) --tm;
-        tn = local - tm * (tm + 1) / 2;
-      } else {
-        const int band = local / (8 * p.tiles_n), first = band * 8, size = min(8, p.tiles_m - first);
-        const int r = local - first * p.tiles_n;
-        tn = r / size;
-        tm = first + r - tn * size;
-      }
-      o.m0 = tm * BM;
+      const int band = local / (8 * p.tiles_n), first = band * 8, size = min(8, p.tiles_m - first);
+      const int r = local - first * p.tiles_n;
+      const int tn = r / size;
+      o.m0 = (first + r - tn * size) * BM;
       o.n0 = tn * BN;
       o.n_valid = min(BN, p.N - o.n0);
       o.n_mma = BN;
-      o.k = p.K;
-      if constexpr (MODE == SEG_WGRAD) {
-        int lo, hi;
-        group_range(p.groups, o.e, lo, hi);
-        o.k = hi - lo;
+      o.k = g.cnt[o.e];
+    } else {
+      if (t >= p.num_tiles) return false;
+      const int sym = p.batch * p.tiles_per_group, dense = p.batch * p.tiles_m * p.tiles_n;
+      o.step = t / (2 * sym + dense);
+      int local = t - o.step * (2 * sym + dense);
+      if (local < 2 * sym) {
+        o.product = local >= sym ? 1 : 0;
+        local -= o.product * sym;
+        o.e = local / p.tiles_per_group;
+        local -= o.e * p.tiles_per_group;
+        // Block row tm has (tm + 1) * r tiles of bns columns, r to a block.
+        const int r = BM / p.bns, q = local / r;
+        int tm = (int)((sqrtf(8.0f * (float)q + 1.0f) - 1.0f) * 0.5f);
+        while ((tm + 1) * (tm + 2) / 2 <= q) ++tm;
+        while (tm * (tm + 1) / 2 > q) --tm;
+        o.m0 = tm * BM;
+        o.n0 = (local - tm * (tm + 1) / 2 * r) * p.bns;
+        o.n_valid = max(0, (int)min((int64_t)p.bns, p.M - o.n0));
+        o.n_mma = p.bns;
+        o.k = o.product == 0 ? p.N : (int)p.M;
+      } else {
+        local -= 2 * sym;
+        o.product = 2;
+        o.e = local / (p.tiles_m * p.tiles_n);
+        local -= o.e * p.tiles_m * p.tiles_n;
+        // Bands of 8 tile rows; in a band the row runs fastest.
+        const int band = local / (8 * p.tiles_n), first = band * 8, size = min(8, p.tiles_m - first);
+        const int r = local - first * p.tiles_n, tn = r / size;
+        o.m0 = (first + r - tn * size) * BM;
+        o.n0 = tn * p.bn;
+        o.n_valid = min(p.bn, p.N - o.n0);
+        o.n_mma = p.bn;
+        o.k = (int)p.M;
       }
     }
     t += step;
@@ -325,9 +407,73 @@ struct Tiles {
   }
 };
 
+// CHAIN: the counter of the finished tiles of block row i of a product's result.
+__device__ __forceinline__ int32_t* chain_counter(const SegParams& p, int step, int product, int e, int i) {
+  return p.counters + (((int64_t)step * 3 + product) * p.batch + e) * p.tiles_m + i;
+}
+
+// Threads of a mode: producer warp, MMA warp, epilogue warps, and CHAIN's scout and publisher.
+template <int MODE>
+struct SegThreads {
+  static constexpr int COUNT = 64 + 32 * EPI_WARPS + (MODE == SEG_CHAIN ? 64 : 0);
+};
+
+// Wait until block row i of a result is complete.  Bounded like mbar_wait.
+__device__ __forceinline__ bool chain_wait(const int32_t* counter, int32_t target, const WaitCtx& wc) {
+  if (ld_acquire_gpu(counter) >= target) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (ld_acquire_gpu(counter) < target) {
+    if (*wc.abort) return false;
+    if (globaltimer_ns() - t0 > wc.timeout_ns) {
+      atomicCAS(wc.err, 0, (int32_t)GEMM_ERR_TIMEOUT);
+      *wc.abort = 1;
+      __threadfence_block();
+      return false;
+    }
+  }
+  return true;
+}
+
+// CHAIN: wait until the sequence number in shared memory has passed `tile`: the scout has
+// found that tile's operands in place (its acquire and proxy fence, then this release and
+// acquire, order the tile's loads after the stores that they read), or an epilogue warp
+// has stored its part of the tile.
+__device__ __forceinline__ bool chain_seen(const int32_t* seq, int tile, const WaitCtx& wc) {
+  const uint32_t a = smem_u32(seq);
+  for (;;) {
+    int32_t v;
+    asm volatile("ld.acquire.cta.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    if (v > tile) return true;
+    if (*wc.abort) return false;   // (the waits of those who write it are bounded and set this)
+    __nanosleep(20);
+  }
+}
+
+// CHAIN: the operands of tile t in place (see the head of this file).
+template <int CG>
+__device__ __forceinline__ bool chain_ready(const SegParams& p, const Tile& t, const WaitCtx& wc) {
+  constexpr int B = 128 * CG, PER_TILE = CG;   // every CTA of a tile counts once
+  bool ok = true;
+  if (t.product == 0) {
+    if (t.step > 0) {
+      const int32_t target = p.tiles_n * PER_TILE;   // X
+      ok = chain_wait(chain_counter(p, t.step - 1, 2, t.e, t.m0 / B), target, wc) &&
+           chain_wait(chain_counter(p, t.step - 1, 2, t.e, t.n0 / B), target, wc);
+    }
+  } else {
+    const int32_t target = p.tiles_m * (B / p.bns) * PER_TILE;   // E, F
+    ok = chain_wait(chain_counter(p, t.step, t.product - 1, t.e, t.m0 / B), target, wc);
+    if (ok && t.product == 1) ok = chain_wait(chain_counter(p, t.step, 0, t.e, t.n0 / B), target, wc);
+  }
+  // The data was written by ordinary stores and is read by TMA: the proxy fence stands here,
+  // once the stores are known to have happened.
+  fence_proxy_async_smem();
+  return ok;
+}
+
 template <int CG, bool A_MN, bool B_MN, int MODE>
-__global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__ SegParams p) {
-  constexpr int BN = 128 * CG;
+__global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const __grid_constant__ SegParams p) {
+  constexpr int BN = 128 * CG, THREADS = SegThreads<MODE>::COUNT;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;   // the same offset in both CTAs of a pair
@@ -336,7 +482,9 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
   const uint32_t bar0 = base + BAR0;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + BAR0 + NUM_BARS * 8);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
-  int* table = reinterpret_cast<int*>(tmem_slot + 4);
+  int32_t* ready_seq = reinterpret_cast<int32_t*>(tmem_slot + 2);   // CHAIN: tiles whose operands are in place
+  int32_t* stored_seq = reinterpret_cast<int32_t*>(tmem_slot + 4);  // CHAIN: tiles that each epilogue warp has stored
+  int* table = reinterpret_cast<int*>(tmem_slot + 4 + EPI_WARPS);
   const GroupTable groups{table, table + p.groups.count, table + 2 * p.groups.count};
 
   auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
@@ -361,6 +509,8 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
     }
     mbar_init(teardown_bar, 1);
     *abort_flag = 0;
+    *ready_seq = 0;
+    for (int w = 0; w < EPI_WARPS; ++w) stored_seq[w] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -371,9 +521,9 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 2 * BN);
   }
   // The prologue above touches no global data: overlap it with the previous kernel.
-  pdl_launch_dependents();
+  if (MODE != SEG_CHAIN) pdl_launch_dependents();
   pdl_wait();
-  if constexpr (MODE == SEG_TOKENS) {
+  if constexpr (MODE == SEG_TOKENS || MODE == SEG_WGRAD) {
     const int E = p.groups.count;
     for (int e = threadIdx.x; e < E; e += THREADS) {
       int lo, hi;
@@ -381,8 +531,8 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
       groups.lo[e] = lo;
       groups.cnt[e] = hi - lo;
     }
-    __syncthreads();
-    if (warp == 0) {
+    if (MODE == SEG_TOKENS) __syncthreads();
+    if (MODE == SEG_TOKENS && warp == 0) {
       int sum = 0;
       for (int e0 = 0; e0 < E; e0 += 32) {
         int v = e0 + lane < E ? (groups.cnt[e0 + lane] + BN - 1) / BN * p.tiles_m : 0;
@@ -410,10 +560,24 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
       int stage = 0;
       uint32_t phase = 0, issued = 0, last_parity = 0;
       bool ok = true;
-      int map_of = -1;   // WGRAD: the group whose tensor maps were last acquired
+      // WGRAD: a group's tensor maps are acquired and fetched a tile ahead of their use.
+      int map_of = -1;
+      auto acquire_maps = [&](const Tile& a) {
+        if (a.k == 0 || a.e == map_of) return;
+        map_of = a.e;
+        for (int i = 0; i < 2; ++i) {
+          tensormap_acquire(p.group_maps + 2 * a.e + i);
+          tma_prefetch_desc(p.group_maps + 2 * a.e + i);
+        }
+      };
       Tiles<MODE, CG> it(p, groups, worker, workers);
-      Tile t;
-      while (ok && it.next(t)) {
+      int tile_no = 0;   // CHAIN
+      Tile t, ahead;
+      bool more = it.next(ahead);
+      if (MODE == SEG_WGRAD && more) acquire_maps(ahead);
+      while (ok && more) {
+        t = ahead;
+        more = it.next(ahead);
         const CUtensorMap *ma = &p.tmA, *mb = &p.tmB[0];
         int za = 0, zb = 0;
         const int m0 = t.m0 + (int)rank * 128, n0 = t.n0 + (int)rank * (t.n_mma / CG);
@@ -427,20 +591,22 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
         } else if constexpr (MODE == SEG_WGRAD) {
           ma = p.group_maps + 2 * t.e;
           mb = ma + 1;
-          if (map_of != t.e && t.k > 0) {
-            tensormap_acquire(ma);
-            tensormap_acquire(mb);
-            map_of = t.e;
-          }
         } else {
           za = zb = t.e;
+          const int cur = t.step & 1;
+          ma = t.product == 0 ? &p.tmB[CHAIN_XK + cur] : t.product == 1 ? &p.tmA : &p.tmB[CHAIN_F];
+          mb = t.product == 0 ? &p.tmB[CHAIN_XB + cur] : t.product == 1 ? &p.tmB[CHAIN_EB] : &p.tmB[CHAIN_XN + cur];
+          b_slab = t.product == 2 ? (uint32_t)SLAB_BYTES : (uint32_t)(p.bns / CG * TC_BK * 2);
+          if (!chain_seen(ready_seq, tile_no++, wc)) { ok = false; break; }
         }
+        // N side contiguous along N (weights' gradients, X) rather than along K.
+        const bool b_mn = MODE == SEG_CHAIN ? t.product == 2 : B_MN;
         const int num_kb = (t.k + TC_BK - 1) / TC_BK;
         for (int kb = 0; kb < num_kb; kb += SLABS) {
           const int nsl = min(SLABS, num_kb - kb);
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) { ok = false; break; }
           const uint32_t a_bytes = (uint32_t)(A_MN ? SLABS : nsl) * (uint32_t)SLAB_BYTES;
-          const uint32_t b_bytes = (uint32_t)(B_MN ? SLABS : nsl) * b_slab;
+          const uint32_t b_bytes = (uint32_t)(b_mn ? SLABS : nsl) * (MODE == SEG_CHAIN && b_mn && t.n_mma <= 64 * CG ? b_slab / 2 : b_slab);
           if (leader) mbar_expect_tx(full_bar(stage), (uint32_t)CG * (a_bytes + b_bytes));
           const uint32_t fb = leader ? full_bar(stage) : mapa_shared(full_bar(stage), 0);
           const uint32_t sa = base + (uint32_t)(stage * STAGE_BYTES), sb = sa + (uint32_t)OPERAND_BYTES;
@@ -455,16 +621,18 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
           } else {
             for (int sl = 0; sl < nsl; ++sl) load(sa + sl * SLAB_BYTES, ma, k0 + sl * TC_BK, m0, za);
           }
-          if constexpr (B_MN) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) load(sb + h * MN_BOX_BYTES, mb, n0 + h * 64, k0, zb);
+          if (b_mn) {
+            // (CHAIN: a tile of at most 64 columns takes one box)
+            for (int h = 0; h < (MODE == SEG_CHAIN && t.n_mma <= 64 * CG ? 1 : 2); ++h) load(sb + h * MN_BOX_BYTES, mb, n0 + h * 64, k0, zb);
           } else {
             for (int sl = 0; sl < nsl; ++sl) load(sb + sl * SLAB_BYTES, mb, k0 + sl * TC_BK, n0, zb);
           }
           issued |= 1u << stage;
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (MODE == SEG_WGRAD && kb == 0 && more) acquire_maps(ahead);
         }
+        if (MODE == SEG_WGRAD && t.k == 0 && more) acquire_maps(ahead);
       }
       // No copy is in flight when the CTA leaves (the peer of a pair waits at the last
       // cluster barrier: its copies complete on the leader's barriers).
@@ -491,7 +659,9 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
         if (!mbar_wait(tempty_bar(buf), ((acc_it >> 1) & 1u) ^ 1u, wc)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN);
-        const uint32_t idesc = p.idesc | ((uint32_t)(t.n_mma >> 3) << 17);
+        const bool b_mn = MODE == SEG_CHAIN ? t.product == 2 : B_MN;
+        const uint32_t idesc = p.idesc | ((uint32_t)(t.n_mma >> 3) << 17) |
+                               ((MODE == SEG_CHAIN && b_mn ? 1u : 0u) << 16);   // bit 16: N side MN-major
         const int num_kb = (t.k + TC_BK - 1) / TC_BK, num_k16 = (t.k + 15) / 16;
         for (int kb = 0; kb < num_kb; kb += SLABS) {
           if (!mbar_wait(full_bar(stage), phase, wc)) { ok = false; break; }
@@ -503,7 +673,7 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
             if (kb * (TC_BK / 16) + q < num_k16) {
               const uint64_t ad = A_MN ? smem_desc_sw128(sa + q * 2048u, MN_BOX_BYTES, 1024)
                                        : smem_desc_sw128(sa + sl * SLAB_BYTES + kk * 32u, 16, 1024);
-              const uint64_t bd = B_MN ? smem_desc_sw128(sb + q * 2048u, MN_BOX_BYTES, 1024)
+              const uint64_t bd = b_mn ? smem_desc_sw128(sb + q * 2048u, MN_BOX_BYTES, 1024)
                                        : smem_desc_sw128(sb + sl * SLAB_BYTES + kk * 32u, 16, 1024);
               if constexpr (CG == 2) tc_mma_f16_pair(d_tmem, ad, bd, idesc, (kb > 0 || q > 0) ? 1u : 0u);
               else tc_mma_f16(d_tmem, ad, bd, idesc, (kb > 0 || q > 0) ? 1u : 0u);
@@ -523,12 +693,42 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
       else tc_commit(teardown_bar);
       drain_wait(teardown_bar, 0, p.timeout_ns);
     }
+  } else if (MODE == SEG_CHAIN && warp == 2 + EPI_WARPS) {
+    // ---------------------------------- scout ----------------------------------
+    // Walks the same list ahead of the others and waits for each tile's operands, so
+    // that the producer's ring never stands still for a counter's round trip.
+    if (lane == 0) {
+      Tiles<MODE, CG> it(p, groups, worker, workers);
+      Tile t;
+      for (int n = 1; it.next(t); ++n) {
+        if (!chain_ready<CG>(p, t, wc)) break;
+        asm volatile("st.release.cta.shared.b32 [%0], %1;" ::"r"(smem_u32(ready_seq)), "r"(n) : "memory");
+      }
+    }
+  } else if (MODE == SEG_CHAIN && warp == 3 + EPI_WARPS) {
+    // -------------------------------- publisher --------------------------------
+    // Waits until every epilogue warp has stored its part of a tile, then counts the tile
+    // in on its block rows: the fence's wait for the stores delays no epilogue warp.
+    Tiles<MODE, CG> it(p, groups, worker, workers);
+    Tile t;
+    for (int n = 1; it.next(t); ++n) {
+      bool ok = true;
+      if (lane < EPI_WARPS) ok = chain_seen(stored_seq + lane, n - 1, wc);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        __threadfence();
+        atomicAdd(chain_counter(p, t.step, t.product, t.e, t.m0 / (128 * CG)), 1);
+        if (t.product < 2 && t.n0 < t.m0) atomicAdd(chain_counter(p, t.step, t.product, t.e, t.n0 / (128 * CG)), 1);
+      }
+      __syncwarp();
+    }
   } else {
     // -------------------------------- epilogue --------------------------------
     const int q = warp & 3;                 // this warp's tensor-memory lane quarter
     const int c_first = (warp - 2) >> 2;    // it takes every other 32-column chunk
     const uint32_t turn = base + TURN0 + (uint32_t)((warp - 2) * TURN_BYTES);
     uint32_t acc_it = 0;
+    int tile_no = 0;   // CHAIN
     Tiles<MODE, CG> it(p, groups, worker, workers);
     Tile t;
     while (it.next(t)) {
@@ -536,23 +736,87 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
       const int64_t m = (int64_t)t.m0 + rank * 128 + q * 32;   // this warp's first M-side row
       const int m_left = (int)max((int64_t)0, min((int64_t)32, p.M - m));
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
+      EpiParams ep = p.epi;
+      EpiPtrs ptr = epi_ptrs(p.epi, t.e);
+      float shift = 0.0f;
+      bool store_n = true, store_t = false;   // as it is, transposed
+      bool scratch_d = MODE == SEG_CHAIN;     // D is scratch
+      auto ext = [](int cols) { return MODE == SEG_CHAIN ? min(32, (cols + 7) & ~7) : cols; };
+      if constexpr (MODE == SEG_CHAIN) {
+        const bool late = t.step >= p.steps - 2, last = t.step == p.steps - 1;
+        __half *X = p.chain.x[t.step & 1], *Y = p.chain.x[(t.step + 1) & 1];
+        ep.ldc = p.chain.lde;
+        ep.ldd = p.chain.lde;
+        ep.d_dtype = GEMM_F16;
+        ep.vec_d = 1;
+        ptr.C = p.chain.e + t.e * p.chain.stride_e;
+        if (t.product == 0) {
+          ep.alpha = p.chain.inv_scale * p.chain.inv_scale;
+          ep.read_c = 0;
+          shift = late ? 1.0f : 0.0f;
+          ptr.D = p.chain.e + t.e * p.chain.stride_e;
+          store_t = t.n0 < t.m0;
+        } else if (t.product == 1) {
+          ep.alpha = p.chain.c;
+          ep.beta = late ? p.chain.b[1] : p.chain.b[0];
+          ptr.D = p.chain.f + t.e * p.chain.stride_e;
+          store_t = t.n0 < t.m0;
+        } else {
+          ep.alpha = last ? p.chain.inv_scale : 1.0f;
+          ep.beta = (late ? p.chain.a[1] : p.chain.a[0]) * ep.alpha;
+          ptr.C = X + t.e * p.chain.stride_x;
+          ep.ldc = p.chain.ldx;
+          ep.ldd = p.chain.ldx;
+          ptr.D = Y + t.e * p.chain.stride_x;
+          if (last) {
+            ep.ldd = p.epi.ldd;
+            ep.d_dtype = p.epi.d_dtype;
+            ep.vec_d = p.epi.vec_d;
+            ptr.D = static_cast<char*>(p.epi.D) + t.e * p.epi.stride_d * dtype_bytes(p.epi.d_dtype);
+            store_t = p.store_t != 0;
+            store_n = !store_t;
+            scratch_d = false;
+          }
+        }
+      }
+      CChunk cc;
+      cc.held = false;
+      if (MODE == SEG_CHAIN && !chain_seen(ready_seq, tile_no++, wc)) break;
+      if (MODE != SEG_TOKENS && ep.read_c)   // the first C chunk comes in during the MMAs
+        load_c(ep, ptr.C, m, (int64_t)t.n0 + c_first * 32, m_left, ext(t.n_valid - c_first * 32), cc);
       if (t.k > 0) {
         if (!warp_wait(tfull_bar(buf), (acc_it >> 1) & 1u, wc)) break;
         tc_fence_after();
       }
-      auto acc = [&](int c, float (&x)[32]) {
+      // Chunk c of the accumulator into r (asynchronously: tmem_wait_ld before its use).
+      uint32_t r[32];
+      auto fetch = [&](int c) {
         if (t.k > 0) {
-          uint32_t r[32];
           tmem_ld_32x32b_x32(tb + (uint32_t)(c * 32), r);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = p.epi.alpha * __uint_as_float(r[j]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+          for (int j = 0; j < 32; ++j) r[j] = 0u;
         }
       };
+      auto take = [&](float (&x)[32]) {
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = ep.alpha * __uint_as_float(r[j]);
+      };
       const int chunks = (t.n_valid + 31) / 32;
+      // The accumulator is free for the next tile but one as soon as it is read.
+      auto release = [&]() {
+        if (t.k == 0) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(tempty_bar(buf));
+          else mbar_arrive_cluster(mapa_shared(tempty_bar(buf), 0));
+        }
+        ++acc_it;
+      };
+      if (c_first < chunks) fetch(c_first);
+      else release();
       if constexpr (MODE == SEG_TOKENS) {
         float bias = 0.0f;
         if (p.epi.bias_mode == GEMM_BIAS_COL && lane < m_left)
@@ -561,7 +825,9 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
 #pragma unroll 1
           for (int c = c_first; c < chunks; c += 2) {
             float x[32];
-            acc(c, x);
+            take(x);
+            if (c + 2 < chunks) fetch(c + 2);   // the next chunk while this one is stored
+            else release();
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               x[j] += bias;
@@ -573,38 +839,40 @@ __global__ void __launch_bounds__(THREADS, 1) seg_kernel(const __grid_constant__
         };
         with_type(p.epi.d_dtype, run);
       } else {
-        const EpiPtrs ptr = epi_ptrs(p.epi, t.e);
         auto run = [&](auto dt) {
           constexpr int DT = decltype(dt)::value;
 #pragma unroll 1
           for (int c = c_first; c < chunks; c += 2) {
             const int64_t n = (int64_t)t.n0 + c * 32;
-            const int n_left = t.n_valid - c * 32;
+            // (CHAIN's scratch has rows of whole 16-byte pieces: their spare entries may be
+            // read and written)
+            const int n_left = t.n_valid - c * 32, n_ext = scratch_d ? ext(n_left) : n_left;
             float x[32];
-            acc(c, x);
-            if (p.epi.read_c) add_c(p.epi, ptr.C, m, n, m_left, n_left, x, turn);
-            if (MODE == SEG_SYM && p.shift != 0.0f) {
+            take(x);
+            if (c + 2 < chunks) fetch(c + 2);   // the next chunk while this one is stored
+            else release();
+            if (ep.read_c) {
+              add_c(ep, ptr.C, m, n, m_left, ext(n_left), cc, x, turn);
+              if (c + 2 < chunks) load_c(ep, ptr.C, m, n + 64, m_left, ext(n_left - 64), cc);
+            }
+            if (MODE == SEG_CHAIN && shift != 0.0f) {
               const int64_t d = m + lane - n;   // the diagonal crosses this row of the chunk at column d
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (j == d) x[j] -= p.shift;
+                if (j == d) x[j] -= shift;
             }
-            if (MODE != SEG_DENSE || !p.store_t)
-              store_chunk<DT>(ptr.D, p.epi.ldd, m, n, m_left, n_left, x, turn, p.epi.vec_d);
-            if ((MODE == SEG_SYM && t.m0 != t.n0) || (MODE == SEG_DENSE && p.store_t))
-              store_chunk_t<DT>(ptr.D, p.epi.ldd, n, m, n_left, m_left, x, turn, p.epi.vec_d);
+            if (store_n) store_chunk<DT>(ptr.D, ep.ldd, m, n, m_left, n_ext, x, turn, ep.vec_d);
+            if (MODE == SEG_CHAIN && store_t)
+              store_chunk_t<DT>(ptr.D, ep.ldd, n, m, n_left, scratch_d ? ext(m_left) : m_left, x, turn, ep.vec_d);
           }
         };
-        with_type(p.epi.d_dtype, run);
+        with_type(ep.d_dtype, run);
       }
-      if (t.k > 0) {
-        tc_fence_before();
+      if constexpr (MODE == SEG_CHAIN) {
+        // This warp's part of the tile is stored: tell the publisher.
         __syncwarp();
-        if (lane == 0) {
-          if (leader) mbar_arrive(tempty_bar(buf));
-          else mbar_arrive_cluster(mapa_shared(tempty_bar(buf), 0));
-        }
-        ++acc_it;
+        if (lane == 0)
+          asm volatile("st.release.cta.shared.b32 [%0], %1;" ::"r"(smem_u32(stored_seq + warp - 2)), "r"(tile_no) : "memory");
       }
     }
   }
@@ -642,8 +910,9 @@ __global__ void __launch_bounds__(32) wgrad_maps_kernel(const __grid_constant__ 
 
 template <int CG, bool A_MN, bool B_MN, int MODE>
 cudaError_t launch_mode(const SegParams& p, int workers, cudaStream_t stream) {
-  const size_t smem = FIXED_SMEM + (MODE == SEG_TOKENS ? (3 * (size_t)p.groups.count + 1) * sizeof(int) : 0);
-  constexpr size_t MOST = FIXED_SMEM + (MODE == SEG_TOKENS ? (3 * (size_t)kMaxGroups + 1) * sizeof(int) : 0);
+  constexpr bool GROUPED = MODE == SEG_TOKENS || MODE == SEG_WGRAD;
+  const size_t smem = FIXED_SMEM + (GROUPED ? (3 * (size_t)p.groups.count + 1) * sizeof(int) : 0);
+  constexpr size_t MOST = FIXED_SMEM + (GROUPED ? (3 * (size_t)kMaxGroups + 1) * sizeof(int) : 0);
   static_assert(MOST <= 232448, "shared memory budget");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -656,12 +925,17 @@ cudaError_t launch_mode(const SegParams& p, int workers, cudaStream_t stream) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(CG * workers), 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.blockDim = dim3(SegThreads<MODE>::COUNT, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  if (MODE == SEG_CHAIN) {   // its CTAs wait for one another: all of them are resident, or none runs
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = CG;
   attr[1].val.clusterDim.y = 1;
@@ -678,8 +952,7 @@ cudaError_t launch_cg(const SegParams& p, int mode, bool a_mn, int workers, cuda
       return a_mn ? launch_mode<CG, true, false, SEG_TOKENS>(p, workers, stream)
                   : launch_mode<CG, false, false, SEG_TOKENS>(p, workers, stream);
     case SEG_WGRAD: return launch_mode<CG, true, true, SEG_WGRAD>(p, workers, stream);
-    case SEG_SYM: return launch_mode<CG, false, false, SEG_SYM>(p, workers, stream);
-    default: return launch_mode<CG, false, true, SEG_DENSE>(p, workers, stream);
+    default: return launch_mode<CG, false, false, SEG_CHAIN>(p, workers, stream);
   }
 }
 

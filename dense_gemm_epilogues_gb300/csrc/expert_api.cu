@@ -2,7 +2,6 @@
 // include/gemm.h): argument checks, workspaces and launches.  Host code only.
 #include <algorithm>
 #include <cmath>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 
@@ -373,9 +372,19 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   const int64_t ldx = (n + 7) / 8 * 8, lde = (m + 7) / 8 * 8;
   const int64_t sx = m * ldx, se = m * lde;
   const size_t xb = align_up((size_t)(batch * sx) * 2, 256), eb = align_up((size_t)(batch * se) * 2, 256);
-  int cg = plan->pair_clusters > 0 && m > 128 ? 2 : 1;
-  int bns = 128 * cg, bn = 128 * cg;   // columns of a tile of E and F, and of X
-  if (const char* env = std::getenv("GEMM_ORTHO_TILE")) std::sscanf(env, "%d,%d,%d", &cg, &bns, &bn);
+  // Tiles: CTA pairs with 256 columns cost the least per product; with too few of them
+  // for all pairs, narrower ones on E and F fill the chip, and small problems (whose time
+  // is the chain of tile latencies) run narrow tiles on single CTAs.  Measured, best
+  // against next: 4096 x 11008 2.16 / 2.65 ms (256 / 128 columns), 2048^2 271 / 295 us
+  // (128 / 256), 1024 x 4096 250 / 298 us (pairs, 64 / single CTAs), 1024^2 146 / 172 us
+  // and 256 x 384 88 / 113 us (single CTAs / pairs, 64).
+  const int64_t m256 = (m + 255) / 256, sym256 = batch * m256 * (m256 + 1) / 2, dense256 = batch * m256 * ((n + 255) / 256);
+  int cg = 1, bns = 64, bn = 64;   // columns of a tile of E and F, and of X
+  if (plan->pair_clusters > 0 && (sym256 >= 24 || dense256 >= 48)) {
+    cg = 2;
+    bn = 256;
+    bns = sym256 >= plan->pair_clusters ? 256 : sym256 >= 24 ? 128 : 64;
+  }
   const int64_t bm = 128 * cg, tm = (m + bm - 1) / bm, tn = (n + bn - 1) / bn;
   const int64_t per_sym = tm * (tm + 1) / 2 * (bm / bns), per_step = batch * (2 * per_sym + tm * tn);
   if (per_step > kMaxTiles / std::max(1, steps)) return GEMM_ERR_UNSUPPORTED;

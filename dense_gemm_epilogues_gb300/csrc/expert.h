@@ -6,6 +6,24 @@
 
 namespace gemmlib {
 
+#if defined(__CUDACC__)
+// Launch a kernel as a programmatic dependent of the stream's last one (it calls
+// pdl_wait before it touches global memory).
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+#endif
+
 constexpr int kMaxGroups = 1024;   // experts of one call (their tile counts are kept in shared memory)
 
 // Rows [offsets[g], offsets[g + 1]) of a buffer of `rows` rows belong to group g.

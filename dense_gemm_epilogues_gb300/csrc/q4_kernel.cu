@@ -393,11 +393,18 @@ __global__ void __launch_bounds__(32 * WARPS, Q4Cfg<MT, NT>::CTAS) q4_kernel(con
 }
 
 // Weights as 16-bit values s * (q - z), K-major with pitch ldw (zeros past K); groups
-// without rows are skipped.  Eight weights (one word) per thread and step.
+// without rows are skipped.  A thread takes one word (8 k) of a column; a warp stores
+// 512 consecutive bytes.  Bound by memory (the store is four times the load): many
+// light threads keep more of it in flight than several words per thread (2 and 8
+// columns per thread took 43 and 62 us for 4096 x 11008, this 38 before it used packed
+// arithmetic).  With scales of A's own type the product s * (q - z) is one packed
+// multiplication: its exact value is rounded once, as in fp32.
 template <bool BF16>
 __global__ void __launch_bounds__(256) q4_dequant_kernel(const __grid_constant__ Q4Params p, uint16_t* out, int64_t ldw,
                                                          int64_t stride_w) {
-  const int e = (int)blockIdx.y;
+  // (No early start for the products: their CTAs' registers would keep this kernel's out.)
+  pdl_wait();
+  const int e = (int)blockIdx.z;
   int lo, hi;
   group_range(p.g, e, lo, hi);
   if (lo == hi) return;
@@ -405,35 +412,38 @@ __global__ void __launch_bounds__(256) q4_dequant_kernel(const __grid_constant__
   const char* scales = static_cast<const char*>(p.scales) + e * p.stride_s * dtype_bytes(p.scale_dtype);
   const uint8_t* zeros = p.zeros ? p.zeros + e * p.stride_z : nullptr;
   out += e * stride_w;
-  const int64_t per_row = ldw / 8, total = (int64_t)p.N * per_row;
   const int row_bytes = (p.K + 1) / 2;
-  const bool words = ((reinterpret_cast<uintptr_t>(q) | (uintptr_t)p.ldq) & 3) == 0;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t n = i / per_row;
-    const int k = (int)(i - n * per_row) * 8;
-    const uint8_t* src = q + n * p.ldq + k / 2;
-    uint32_t w = 0;
-    if (words && k / 2 + 4 <= row_bytes) {
-      w = *reinterpret_cast<const uint32_t*>(src);
-    } else {
+  const int k = (int)(blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  if (k >= ldw) return;
+  const bool packed = ((reinterpret_cast<uintptr_t>(q) | (uintptr_t)p.ldq) & 3) == 0 && k + 8 <= p.K && p.scale_dtype == p.ab_dtype;
+  const int gk = k < p.K ? k / p.group : 0;
+  for (int64_t n = blockIdx.y; n < p.N; n += gridDim.y) {
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    if (packed) {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q + n * p.ldq + k / 2));
+      uint32_t s = __ldg(reinterpret_cast<const uint16_t*>(scales) + n * p.lds + gk), h[4];
+      s |= s << 16;
+      unpack<BF16>(w, zero_const<BF16>(zeros ? zeros[n * p.ldz + gk] & 15u : 8u), h);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (k / 2 + u < row_bytes) w |= (uint32_t)src[u] << (8 * u);
-    }
-    float s = 0.0f;
-    int z = 8;
-    if (k < p.K) {
-      const int64_t gk = k / p.group;
-      s = load_as_float(scales, p.scale_dtype, n * p.lds + gk);
-      if (zeros) z = zeros[n * p.ldz + gk] & 15;
-    }
-    uint32_t o[4];
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(h[i]), "r"(s));
+        else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(h[i]), "r"(s));
+      }
+      o[0] = __byte_perm(h[0], h[1], 0x5410);   // pairs (k, k + 4) back to neighbours
+      o[1] = __byte_perm(h[2], h[3], 0x5410);
+      o[2] = __byte_perm(h[0], h[1], 0x7632);
+      o[3] = __byte_perm(h[2], h[3], 0x7632);
+    } else if (k < p.K) {
+      const float s = load_as_float(scales, p.scale_dtype, n * p.lds + gk);
+      const int z = zeros ? zeros[n * p.ldz + gk] & 15 : 8;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float a = k + 2 * u < p.K ? s * (float)((int)((w >> (8 * u)) & 15) - z) : 0.0f;
-      const float b = k + 2 * u + 1 < p.K ? s * (float)((int)((w >> (8 * u + 4)) & 15) - z) : 0.0f;
-      if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[u]) : "f"(b), "f"(a));
-      else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[u]) : "f"(b), "f"(a));
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t b = k / 2 + u < row_bytes ? q[n * p.ldq + k / 2 + u] : 0u;
+        const float lo4 = k + 2 * u < p.K ? s * (float)((int)(b & 15) - z) : 0.0f;
+        const float hi4 = k + 2 * u + 1 < p.K ? s * (float)((int)(b >> 4) - z) : 0.0f;
+        if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[u]) : "f"(hi4), "f"(lo4));
+        else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[u]) : "f"(hi4), "f"(lo4));
+      }
     }
     *reinterpret_cast<uint4*>(out + n * ldw + k) = make_uint4(o[0], o[1], o[2], o[3]);
   }
@@ -520,13 +530,11 @@ cudaError_t launch_q4(const Q4Params& p, int nt, cudaStream_t stream) {
 }
 
 cudaError_t launch_q4_dequant(const Q4Params& p, void* out, int64_t ldw, int64_t stride_w, cudaStream_t stream) {
-  const int64_t per = ((int64_t)p.N * (ldw / 8) + 255) / 256;
-  const dim3 grid((unsigned)std::min<int64_t>(per, std::max(152, 4864 / p.g.count)), (unsigned)p.g.count);
-  if (p.ab_dtype == GEMM_BF16)
-    q4_dequant_kernel<true><<<grid, 256, 0, stream>>>(p, static_cast<uint16_t*>(out), ldw, stride_w);
-  else
-    q4_dequant_kernel<false><<<grid, 256, 0, stream>>>(p, static_cast<uint16_t*>(out), ldw, stride_w);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)((ldw / 8 + 255) / 256), (unsigned)std::min(p.N, 65535),
+                  (unsigned)p.g.count);
+  uint16_t* o = static_cast<uint16_t*>(out);
+  return p.ab_dtype == GEMM_BF16 ? launch_dependent(q4_dequant_kernel<true>, grid, 256, stream, p, o, ldw, stride_w)
+                                 : launch_dependent(q4_dequant_kernel<false>, grid, 256, stream, p, o, ldw, stride_w);
 }
 
 }  // namespace gemmlib

@@ -891,6 +891,8 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
 // Per group and operand a copy of the operand's tensor map with the group's first
 // row as its base and the group's row count as its extent.  One warp per map.
 __global__ void __launch_bounds__(32) wgrad_maps_kernel(const __grid_constant__ SegParams p, CUtensorMap* maps) {
+  pdl_launch_dependents();   // the products' prologue may begin
+  pdl_wait();
   const int e = (int)blockIdx.x >> 1, which = (int)blockIdx.x & 1, lane = threadIdx.x;
   int lo, hi;
   group_range(p.groups, e, lo, hi);
@@ -959,8 +961,7 @@ cudaError_t launch_cg(const SegParams& p, int mode, bool a_mn, int workers, cuda
 }  // namespace
 
 cudaError_t launch_wgrad_maps(const SegParams& p, CUtensorMap* maps, cudaStream_t stream) {
-  wgrad_maps_kernel<<<2 * p.groups.count, 32, 0, stream>>>(p, maps);
-  return cudaGetLastError();
+  return launch_dependent(wgrad_maps_kernel, dim3(2u * (unsigned)p.groups.count), 32, stream, p, maps);
 }
 
 cudaError_t launch_seg(const SegParams& p, int mode, int cg, bool a_mn, int workers, cudaStream_t stream) {

@@ -369,7 +369,7 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   // X is kept as the wide one of the matrix and its transpose: m <= n.
   const bool tall = M > N;
   const int64_t m = tall ? N : M, n = tall ? M : N;
-  const int64_t ldx = (n + 7) / 8 * 8, lde = (m + 7) / 8 * 8;
+  const int64_t ldx = (n + 15) / 16 * 16, lde = (m + 15) / 16 * 16;   // rows on 32 bytes
   const int64_t sx = m * ldx, se = m * lde;
   const size_t xb = align_up((size_t)(batch * sx) * 2, 256), eb = align_up((size_t)(batch * se) * 2, 256);
   // Tiles: CTA pairs with 256 columns cost the least per product; with too few of them

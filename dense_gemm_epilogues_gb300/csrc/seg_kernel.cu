@@ -89,66 +89,71 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
-// 32 rows of 64 bytes (lane: its row's 16 words) stored as whole sectors, 8 rows
-// per instruction; ES-byte elements, rows r < rows, columns j < cols.  vec: rows are
-// 16-byte aligned and cols is a multiple of 16 bytes.
+// 32 rows of 64 bytes (lane: its row's 16 words) of ES-byte elements at any alignment:
+// turned around in the warp's buffer, whole rows per instruction; rows r < rows, columns
+// j < cols.
 template <int ES>
 __device__ __forceinline__ void store_rows64(char* D, int64_t pitch, int rows, int cols, const uint32_t (&w)[16],
-                                             uint32_t turn, bool vec) {
+                                             uint32_t turn) {
   const int lane = threadIdx.x & 31;
   __syncwarp();   // the buffer's last readers are done
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     sts128(turn + (uint32_t)(lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)), w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
   __syncwarp();
-  if (vec) {
-    const int pl = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      const uint4 v = lds128(turn + (uint32_t)(r * 64 + ((pl ^ ((r >> 1) & 3)) << 4)));
-      if (r < rows && pl * (16 / ES) < cols) *reinterpret_cast<uint4*>(D + r * pitch + pl * 16) = v;
-    }
-  } else {
-    constexpr int PER = 64 / ES, RPI = 32 / PER;   // elements per row, rows per instruction
-    const int j = lane % PER;
+  constexpr int PER = 64 / ES, RPI = 32 / PER;   // elements per row, rows per instruction
+  const int j = lane % PER;
 #pragma unroll 8
-    for (int r = lane / PER; r < 32; r += RPI) {
-      const uint32_t a = turn + (uint32_t)(r * 64 + (((j * ES >> 4) ^ ((r >> 1) & 3)) << 4) + (j * ES & 15));
-      if (r < rows && j < cols) {
-        if constexpr (ES == 2) {
-          uint16_t v;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-          *reinterpret_cast<uint16_t*>(D + r * pitch + j * 2) = v;
-        } else {
-          uint32_t v;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-          *reinterpret_cast<uint32_t*>(D + r * pitch + j * 4) = v;
-        }
+  for (int r = lane / PER; r < 32; r += RPI) {
+    const uint32_t a = turn + (uint32_t)(r * 64 + (((j * ES >> 4) ^ ((r >> 1) & 3)) << 4) + (j * ES & 15));
+    if (r < rows && j < cols) {
+      if constexpr (ES == 2) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+        *reinterpret_cast<uint16_t*>(D + r * pitch + j * 2) = v;
+      } else {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+        *reinterpret_cast<uint32_t*>(D + r * pitch + j * 4) = v;
       }
     }
   }
 }
 
 // A warp's 32 x 32 chunk, lane r = row r, x = its columns: D[r][j], r < rows, j < cols.
+// Aligned rows are stored straight from registers, 32 bytes (a whole sector) per lane:
+// the MMAs' operand reads and the ring's writes leave little shared-memory bandwidth, and
+// turning the chunk around there cost more than the wider pattern of the stores does.
 template <int DT>
 __device__ __forceinline__ void store_chunk(void* D, int64_t ldd, int64_t r0, int64_t c0, int rows, int cols,
                                             const float (&x)[32], uint32_t turn, bool vec) {
-  const bool v = vec && cols % (DT == GEMM_F32 ? 4 : 8) == 0;
-  uint32_t w[16];
+  constexpr int ES = DT == GEMM_F32 ? 4 : 2, PIECE = 32 / ES;   // columns of 32 bytes
+  const int lane = threadIdx.x & 31;
+  uint32_t w[32 * ES / 4];
   if constexpr (DT == GEMM_F32) {
-    char* d = reinterpret_cast<char*>(static_cast<float*>(D) + r0 * ldd + c0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(x[16 * h + j]);
-      store_rows64<4>(d + h * 64, ldd * 4, rows, cols - 16 * h, w, turn, v);
-    }
+    for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(x[j]);
   } else {
-    char* d = reinterpret_cast<char*>(static_cast<uint16_t*>(D) + r0 * ldd + c0);
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack2<DT>(x[2 * j], x[2 * j + 1]);
-    store_rows64<2>(d, ldd * 2, rows, cols, w, turn, v);
+  }
+  char* d = static_cast<char*>(D) + (r0 * ldd + c0) * ES;
+  if (vec && cols % (16 / ES) == 0) {
+    if (lane >= rows) return;
+    d += lane * ldd * ES;
+#pragma unroll
+    for (int q = 0; q < 32 / PIECE; ++q) {
+      if ((q + 1) * PIECE <= cols) st_row_32b(d + 32 * q, w + 8 * q);
+      else if (q * PIECE < cols) *reinterpret_cast<uint4*>(d + 32 * q) = make_uint4(w[8 * q], w[8 * q + 1], w[8 * q + 2], w[8 * q + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < ES / 2; ++h) {
+      uint32_t u[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) u[j] = w[16 * h + j];
+      store_rows64<ES>(d + h * 64, ldd * ES, rows, cols - h * 16, u, turn);
+    }
   }
 }
 
@@ -218,62 +223,68 @@ __device__ __forceinline__ void store_chunk_t(void* D, int64_t ldd, int64_t j0, 
 }
 
 // beta * C of a chunk (lane r = row r), in two steps so that the loads run ahead of the
-// accumulator: whole rows of 16-bit C are held in registers as loaded (8 rows per
-// instruction) and turned around through the buffer when they are added; other types
-// and edges are read when they are added, by elements, whole rows per instruction.  All past L1: CHAIN's C was
-// written by other SMs during the launch that reads it.
+// accumulator: aligned rows of 16-bit C straight into registers, 32 bytes per load; other
+// types and edges are read when they are added, by elements, whole rows per instruction.
+// All coherent at L2: CHAIN's C was written by other SMs during the launch that reads it.
 struct CChunk {
-  uint4 v[4];
+  uint32_t w[16];
   bool held;
 };
-__device__ __forceinline__ void load_c(const EpiParams& e, const void* C, int64_t r0, int64_t c0, int rows, int cols,
-                                       CChunk& c) {
-  const int lane = threadIdx.x & 31, pl = lane & 3;
-  c.held = e.vec_c && cols % 8 == 0 && e.c_dtype != GEMM_F32;
-  if (!c.held) return;
-  const uint16_t* src = static_cast<const uint16_t*>(C) + (r0 + (lane >> 2)) * e.ldc + c0 + pl * 8;
+__device__ __forceinline__ void ld_32b(const void* p, uint32_t* w) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("ld.relaxed.gpu.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c.v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (8 * i + (lane >> 2) < rows && pl * 8 < cols) c.v[i] = __ldcg(reinterpret_cast<const uint4*>(src + 8 * i * e.ldc));
+    for (int h = 0; h < 2; ++h) {
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p) + h);
+      w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+    }
   }
 }
-// x += beta * this lane's row of 16-bit C in the buffer.
-__device__ __forceinline__ void add_c16(const EpiParams& e, float (&x)[32], uint32_t turn) {
+__device__ __forceinline__ void load_c(const EpiParams& e, const void* C, int64_t r0, int64_t c0, int rows, int cols,
+                                       CChunk& c) {
   const int lane = threadIdx.x & 31;
+  c.held = e.vec_c && cols % 8 == 0 && e.c_dtype != GEMM_F32;
+  if (!c.held) return;
+  const uint16_t* src = static_cast<const uint16_t*>(C) + (r0 + lane) * e.ldc + c0;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 c = lds128(turn + (uint32_t)(lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)));
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  for (int q = 0; q < 2; ++q) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      float lo, hi;
-      if (e.c_dtype == GEMM_F16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-        lo = f.x;
-        hi = f.y;
-      } else {
-        lo = __uint_as_float(w[h] << 16);
-        hi = __uint_as_float(w[h] & 0xffff0000u);
-      }
-      x[8 * q + 2 * h] = fmaf(e.beta, lo, x[8 * q + 2 * h]);
-      x[8 * q + 2 * h + 1] = fmaf(e.beta, hi, x[8 * q + 2 * h + 1]);
+    for (int u = 0; u < 8; ++u) c.w[8 * q + u] = 0u;
+    if (lane >= rows) continue;
+    if (16 * q + 16 <= cols) {
+      ld_32b(src + 16 * q, c.w + 8 * q);
+    } else if (16 * q < cols) {
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src + 16 * q));
+      c.w[8 * q] = v.x, c.w[8 * q + 1] = v.y, c.w[8 * q + 2] = v.z, c.w[8 * q + 3] = v.w;
     }
+  }
+}
+// x += beta * 16 words of 16-bit C.
+__device__ __forceinline__ void fma_c16(const EpiParams& e, float (&x)[32], const uint32_t* w, int j0, int n) {
+#pragma unroll
+  for (int h = 0; h < n; ++h) {
+    float lo, hi;
+    if (e.c_dtype == GEMM_F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
+      lo = f.x;
+      hi = f.y;
+    } else {
+      lo = __uint_as_float(w[h] << 16);
+      hi = __uint_as_float(w[h] & 0xffff0000u);
+    }
+    x[j0 + 2 * h] = fmaf(e.beta, lo, x[j0 + 2 * h]);
+    x[j0 + 2 * h + 1] = fmaf(e.beta, hi, x[j0 + 2 * h + 1]);
   }
 }
 __device__ __forceinline__ void add_c(const EpiParams& e, const void* C, int64_t r0, int64_t c0, int rows, int cols,
                                       const CChunk& ch, float (&x)[32], uint32_t turn) {
   const int lane = threadIdx.x & 31;
   if (ch.held) {
-    const int pl = lane & 3;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      sts128(turn + (uint32_t)(r * 64 + ((pl ^ ((r >> 1) & 3)) << 4)), ch.v[i].x, ch.v[i].y, ch.v[i].z, ch.v[i].w);
-    }
-    __syncwarp();
-    add_c16(e, x, turn);
+    fma_c16(e, x, ch.w, 0, 16);
   } else if (e.c_dtype == GEMM_F32) {
     // 16 columns at a time: two rows per load instruction, turned around like 16-bit rows.
 #pragma unroll
@@ -306,7 +317,12 @@ __device__ __forceinline__ void add_c(const EpiParams& e, const void* C, int64_t
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + (uint32_t)(r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2)), "h"(v) : "memory");
     }
     __syncwarp();
-    add_c16(e, x, turn);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 c = lds128(turn + (uint32_t)(lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)));
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      fma_c16(e, x, w, 8 * q, 4);
+    }
   }
 }
 

@@ -12,8 +12,8 @@ from typing import Optional
 
 import torch
 
-from . import (GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_BF16, GEMM_BIAS_COL, GEMM_BIAS_NONE, GEMM_F16, GEMM_F32, GEMM_OP_N,
-               GEMM_OP_T, GemmError, Plan, gemm_epilogue_t, gemm_q4_t, load_library)
+from . import (GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_BF16, GEMM_BIAS_COL, GEMM_BIAS_NONE, GEMM_ERR_UNSUPPORTED, GEMM_F16,
+               GEMM_F32, GEMM_OP_N, GEMM_OP_T, GemmError, Plan, gemm_epilogue_t, gemm_q4_t, load_library)
 
 _CODES = {torch.float32: GEMM_F32, torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16}
 _LIB = load_library()
@@ -27,10 +27,10 @@ def _code(dtype) -> int:
         raise ValueError(f"type {dtype} is not float32, float16 or bfloat16") from None
 
 
-def _call(where, *args):
-    status = getattr(_LIB, where)(*args)
-    if status:
-        raise GemmError(status, where)
+# The epilogues without a bias, by (ReLU, output type): they hold no pointer.
+_PLAIN = {(relu, code): gemm_epilogue_t(None, GEMM_F32, GEMM_BIAS_NONE, GEMM_ACT_RELU if relu else GEMM_ACT_NONE, code,
+                                        GEMM_ACT_NONE, 1.0)
+          for relu in (False, True) for code in _CODES.values()}
 
 
 def _device(x, *others) -> int:
@@ -42,6 +42,17 @@ def _device(x, *others) -> int:
         if t is not None and t.get_device() != d:
             raise ValueError("tensors are on different devices")
     return d
+
+
+def _plan_for(plan, ab_code: int, c_code: int, device: int) -> Plan:
+    """The caller's plan, which has to be for these operands, or a new one."""
+    if plan is None:
+        return Plan(ab_code, c_code, device)
+    if plan.ab_dtype != ab_code:
+        raise GemmError(GEMM_ERR_UNSUPPORTED, "a plan of another operand type")
+    if plan.device != device:
+        raise ValueError("the plan is on another device")
+    return plan
 
 
 def _pitch(shape, stride, name: str) -> int:
@@ -59,9 +70,9 @@ def _check_offsets(offsets, groups: int):
 
 def _epilogue(bias, groups: int, n: int, relu: bool, out_code: int):
     """(epilogue, bias stride) of a grouped product; bias is [groups, N] or [N] (shared)."""
-    act = GEMM_ACT_RELU if relu else GEMM_ACT_NONE
     if bias is None:
-        return gemm_epilogue_t(None, GEMM_F32, GEMM_BIAS_NONE, act, out_code, GEMM_ACT_NONE, 1.0), 0
+        return _PLAIN[bool(relu), out_code], 0
+    act = GEMM_ACT_RELU if relu else GEMM_ACT_NONE
     if bias.shape not in ((groups, n), (n,)) or (bias.stride(-1) != 1 and n > 1):
         raise ValueError("bias must be [N] or [groups, N] with contiguous rows")
     return (gemm_epilogue_t(bias.data_ptr(), _code(bias.dtype), GEMM_BIAS_COL, act, out_code, GEMM_ACT_NONE, 1.0),
@@ -104,12 +115,13 @@ def grouped_matmul(x, w, offsets, *, alpha: float = 1.0, bias=None, relu: bool =
     else:
         raise ValueError("w must have unit stride along K or N")
     out, ldd, code = _output(out, M, N, out_dtype or dtype, x)
-    if plan is None:
-        plan = Plan(_code(dtype), GEMM_F32, device)
+    plan = _plan_for(plan, _code(dtype), GEMM_F32, device)
     epi, stride_bias = _epilogue(bias, groups, N, relu, code)
-    _call("gemm_run_grouped", plan.handle, lb, groups, M, N, K, alpha, x.data_ptr(), lda, w.data_ptr(), ldb,
-          ws if groups > 1 else 0, out.data_ptr(), ldd, offsets.data_ptr(), epi, stride_bias,
-          _raw_stream(device) if stream is None else stream)
+    status = _LIB.gemm_run_grouped(plan.handle, lb, groups, M, N, K, alpha, x.data_ptr(), lda, w.data_ptr(), ldb,
+                                   ws if groups > 1 else 0, out.data_ptr(), ldd, offsets.data_ptr(), epi, stride_bias,
+                                   _raw_stream(device) if stream is None else stream)
+    if status:
+        raise GemmError(status, "gemm_run_grouped")
     return out
 
 
@@ -138,17 +150,19 @@ def grouped_weight_grad(x, dy, offsets, *, alpha: float = 1.0, accumulate: bool 
     elif out.shape != (groups, M, N) or (out.stride(2) != 1 and N > 1):
         raise ValueError("out must be [groups, K, N] with contiguous rows")
     code = _code(out.dtype)
-    if plan is None:
-        plan = Plan(_code(dtype), code, device)
+    plan = _plan_for(plan, _code(dtype), code, device)
     if accumulate and plan.c_dtype != code:
         raise ValueError("accumulate needs a plan whose c_dtype is out's type")
     ldd = max(out.stride(1), N, 1)
     stride_d = out.stride(0) if groups > 1 else M * ldd
     p = out.data_ptr()
-    _call("gemm_run_grouped_wgrad", plan.handle, groups, M, N, rows, alpha, x.data_ptr(),
-          _pitch((rows, M), x.stride(), "x"), dy.data_ptr(), _pitch((rows, N), dy.stride(), "dy"),
-          1.0 if accumulate else 0.0, p if accumulate else None, ldd, stride_d, p, ldd, stride_d, offsets.data_ptr(),
-          code, _raw_stream(device) if stream is None else stream)
+    status = _LIB.gemm_run_grouped_wgrad(plan.handle, groups, M, N, rows, alpha, x.data_ptr(),
+                                         _pitch((rows, M), x.stride(), "x"), dy.data_ptr(),
+                                         _pitch((rows, N), dy.stride(), "dy"), 1.0 if accumulate else 0.0,
+                                         p if accumulate else None, ldd, stride_d, p, ldd, stride_d,
+                                         offsets.data_ptr(), code, _raw_stream(device) if stream is None else stream)
+    if status:
+        raise GemmError(status, "gemm_run_grouped_wgrad")
     return out
 
 
@@ -205,17 +219,18 @@ def q4_matmul(x, q, scales, group_size: int, *, zeros=None, offsets=None, alpha:
     if (qs[-1] != 1 and shape[-1] > 1) or (kg > 1 and (ss[-1] != 1 or (zs is not None and zs[-1] != 1))):
         raise ValueError("q, scales and zeros need contiguous rows")
     out, ldd, code = _output(out, M, N, out_dtype or dtype, x)
-    if plan is None:
-        plan = Plan(_code(dtype), GEMM_F32, device)
+    plan = _plan_for(plan, _code(dtype), GEMM_F32, device)
     epi, stride_bias = _epilogue(bias, groups, N, relu, code)
     ex = groups > 1
     weights = gemm_q4_t(q.data_ptr(), max(qs[-2], shape[-1]), qs[0] if ex else 0, scales.data_ptr(),
                         _code(scales.dtype), max(ss[-2], kg), ss[0] if ex else 0,
                         zeros.data_ptr() if zeros is not None else None, max(zs[-2], kg) if zs is not None else 0,
                         zs[0] if ex and zs is not None else 0, group_size)
-    _call("gemm_run_q4", plan.handle, groups, M, N, K, alpha, x.data_ptr(), _pitch((M, K), x.stride(), "x"), weights,
-          out.data_ptr(), ldd, offsets.data_ptr() if offsets is not None else None, epi, stride_bias,
-          _raw_stream(device) if stream is None else stream)
+    status = _LIB.gemm_run_q4(plan.handle, groups, M, N, K, alpha, x.data_ptr(), _pitch((M, K), x.stride(), "x"),
+                              weights, out.data_ptr(), ldd, offsets.data_ptr() if offsets is not None else None, epi,
+                              stride_bias, _raw_stream(device) if stream is None else stream)
+    if status:
+        raise GemmError(status, "gemm_run_q4")
     return out
 
 
@@ -245,9 +260,11 @@ def orthogonalize(g, *, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: f
         if (t.stride(2) != 1 and n > 1) or (m > 1 and t.stride(1) < n):
             raise ValueError(f"{name} must have contiguous rows (or columns) like the other")
     ldd = max(ov.stride(1), n, 1)
-    if plan is None:
-        plan = Plan(_code(g.dtype), GEMM_F32, device)
-    _call("gemm_orthogonalize", plan.handle, batch, m, n, steps, (ctypes.c_double * 3)(*coeffs), eps, gv.data_ptr(),
-          max(gv.stride(1), n, 1), gv.stride(0) if batch > 1 else 0, ov.data_ptr(), ldd,
-          ov.stride(0) if batch > 1 else m * ldd, _code(out.dtype), _raw_stream(device) if stream is None else stream)
+    plan = _plan_for(plan, _code(g.dtype), GEMM_F32, device)
+    status = _LIB.gemm_orthogonalize(plan.handle, batch, m, n, steps, (ctypes.c_double * 3)(*coeffs), eps,
+                                     gv.data_ptr(), max(gv.stride(1), n, 1), gv.stride(0) if batch > 1 else 0,
+                                     ov.data_ptr(), ldd, ov.stride(0) if batch > 1 else m * ldd, _code(out.dtype),
+                                     _raw_stream(device) if stream is None else stream)
+    if status:
+        raise GemmError(status, "gemm_orthogonalize")
     return out

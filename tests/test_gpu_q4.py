@@ -164,3 +164,17 @@ def test_q4_empty_and_refusals():
                dict(group_size=0), dict(scale_dtype=G.GEMM_S8), dict(values=None), dict(scales=None),
                dict(zeros=z.data_ptr(), ld_zeros=1), dict(stride_values=-1)):
         assert code(**kw) == G.GEMM_ERR_INVALID_ARG, kw
+
+
+def test_a_plan_of_another_type_is_refused():
+    gen = _gen(8)
+    q, s, _ = random_q4(32, 64, 32, DT["f16"], False, gen)
+    x = torch.randn((4, 64), device="cuda", generator=gen).half()
+    w = torch.zeros((1, 64, 32), device="cuda", dtype=DT["f16"])
+    off = offsets_of([4])
+    plan = G.Plan(G.GEMM_BF16, G.GEMM_F32)
+    for call in (lambda: G.q4_matmul(x, q, s, 32, plan=plan), lambda: G.grouped_matmul(x, w, off, plan=plan),
+                 lambda: G.grouped_weight_grad(x, x, off, plan=plan), lambda: G.orthogonalize(x, plan=plan)):
+        with pytest.raises(G.GemmError) as e:
+            call()
+        assert e.value.status == G.GEMM_ERR_UNSUPPORTED

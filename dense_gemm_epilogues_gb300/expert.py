@@ -108,12 +108,12 @@ def grouped_matmul(x, w, offsets, *, alpha: float = 1.0, bias=None, relu: bool =
     device = _device(x, w, offsets, bias, out)
     lda = _pitch((M, K), x.stride(), "x")
     ws, wk, wn = w.stride()
-    if wn == 1 or N <= 1:
+    if (wn == 1 or N <= 1) and (wk >= N or K <= 1):
         lb, ldb = GEMM_OP_T, max(wk, N, 1)
-    elif wk == 1 or K <= 1:
+    elif (wk == 1 or K <= 1) and (wn >= K or N <= 1):
         lb, ldb = GEMM_OP_N, max(wn, K, 1)
     else:
-        raise ValueError("w must have unit stride along K or N")
+        raise ValueError("w must have unit stride along K or N and no overlapping rows")
     out, ldd, code = _output(out, M, N, out_dtype or dtype, x)
     plan = _plan_for(plan, _code(dtype), GEMM_F32, device)
     epi, stride_bias = _epilogue(bias, groups, N, relu, code)
@@ -147,7 +147,7 @@ def grouped_weight_grad(x, dy, offsets, *, alpha: float = 1.0, accumulate: bool 
         if accumulate:
             raise ValueError("accumulate needs out")
         out = torch.empty((groups, M, N), dtype=out_dtype or dtype, device=x.device)
-    elif out.shape != (groups, M, N) or (out.stride(2) != 1 and N > 1):
+    elif out.shape != (groups, M, N) or (out.stride(2) != 1 and N > 1) or (out.stride(1) < N and M > 1):
         raise ValueError("out must be [groups, K, N] with contiguous rows")
     code = _code(out.dtype)
     plan = _plan_for(plan, _code(dtype), code, device)
@@ -216,8 +216,9 @@ def q4_matmul(x, q, scales, group_size: int, *, zeros=None, offsets=None, alpha:
         raise ValueError("experts' weights need offsets")
     device = _device(x, q, scales, zeros, offsets, bias, out)
     qs, ss, zs = q.stride(), scales.stride(), zeros.stride() if zeros is not None else None
-    if (qs[-1] != 1 and shape[-1] > 1) or (kg > 1 and (ss[-1] != 1 or (zs is not None and zs[-1] != 1))):
-        raise ValueError("q, scales and zeros need contiguous rows")
+    if (qs[-1] != 1 and shape[-1] > 1) or (kg > 1 and (ss[-1] != 1 or (zs is not None and zs[-1] != 1))) or \
+            (N > 1 and (qs[-2] < shape[-1] or ss[-2] < kg or (zs is not None and zs[-2] < kg))):
+        raise ValueError("q, scales and zeros need contiguous rows that do not overlap")
     out, ldd, code = _output(out, M, N, out_dtype or dtype, x)
     plan = _plan_for(plan, _code(dtype), GEMM_F32, device)
     epi, stride_bias = _epilogue(bias, groups, N, relu, code)

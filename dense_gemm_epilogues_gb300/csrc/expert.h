@@ -10,10 +10,10 @@ namespace gemmlib {
 // Launch a kernel as a programmatic dependent of the stream's last one (it calls
 // pdl_wait before it touches global memory).
 template <typename... P, typename... A>
-inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.blockDim = block;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

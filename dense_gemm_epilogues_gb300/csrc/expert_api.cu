@@ -2,7 +2,6 @@
 // include/gemm.h): argument checks, workspaces and launches.  Host code only.
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <cstring>
 
 #include "expert.h"
@@ -62,18 +61,13 @@ gemm_status_t repitch(Operand* x, int64_t rows, int64_t cols, int64_t batch, con
   if (launch_repitch(x->p, x->ld, x->stride, to, ld, rows * ld, rows, cols, batch, offsets, 2, stream) !=
       cudaSuccess)
     return GEMM_ERR_CUDA;
-  *x = Operand{to, ld, rows * ld};
+  *x = Operand{to, ld, batch > 1 ? rows * ld : 0};
   return GEMM_OK;
 }
 
-// CTAs per tile of a grouped product (GEMM_GROUPED_CG=1 or 2 fixes it).
-int grouped_cg(const gemm_plan* plan, int rule) {
-  if (const char* env = std::getenv("GEMM_GROUPED_CG")) {
-    const int v = std::atoi(env);
-    if (v == 1 || (v == 2 && plan->pair_clusters > 0)) return v;
-  }
-  return plan->pair_clusters > 0 ? rule : 1;
-}
+// Rows of an average expert up to which 4-bit weights are decoded inside the product;
+// beyond, they are decoded once into scratch and multiplied on the tensor-core kernel.
+constexpr int64_t kQ4Few = 64;
 
 int workers_of(const gemm_plan* plan, int cg, int64_t tiles) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(tiles, cg == 2 ? plan->pair_clusters : plan->sm_count));
@@ -101,26 +95,19 @@ gemm_config_t seg_config(int cg, int64_t tiles, int workers) {
 }
 
 // D[r, :] = epilogue(x[r, :] * W_g) on seg_kernel: x M x K row-major, W_g K x N (w_mn: N
-// contiguous, else K).  ws_used: scratch that holds an operand already.
-gemm_status_t tokens_product(gemm_plan* plan, const Groups& groups, int64_t M, int64_t N, int64_t K, Operand x, Operand w,
-                             bool w_mn, size_t ws_used, const EpiParams& epi, const char* entry, cudaStream_t stream) {
-  const int64_t wrows = w_mn ? K : N, wcols = w_mn ? N : K;
+// contiguous, else K); TMA can address both.
+gemm_status_t tokens_product(gemm_plan* plan, const Groups& groups, int64_t M, int64_t N, int64_t K, const Operand& x,
+                             const Operand& w, bool w_mn, const EpiParams& epi, const char* entry, cudaStream_t stream) {
   const int64_t nw = w.stride != 0 ? groups.count : 1;   // matrices of weights
   SegParams p;
   std::memset(&p, 0, sizeof(p));
   p.groups = groups;
-  const int cg = grouped_cg(plan, M >= 128 * (int64_t)groups.count ? 2 : 1);
+  // CTA pairs from 128 rows per expert on.  Single CTAs / pairs: 64 experts of 256 rows
+  // (2048 x 4096) 355 / 256 us, of one row 20.6 / 21.5 us.
+  const int cg = plan->pair_clusters > 0 && M >= 128 * (int64_t)groups.count ? 2 : 1;
   const int64_t tiles = ((N + 128 * cg - 1) / (128 * cg)) * (M / (128 * cg) + std::min<int64_t>(groups.count, M));
   if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
   if (K > 0) {
-    const size_t xb = repitch_bytes(x, M, K, 1), wb = repitch_bytes(w, wrows, wcols, nw);
-    if (xb + wb > 0) {
-      gemm_status_t s = ensure_ws(plan, ws_used + xb + wb, stream);
-      char* ws = static_cast<char*>(plan->ws) + ws_used;
-      if (s == GEMM_OK) s = repitch(&x, M, K, 1, nullptr, ws, stream);
-      if (s == GEMM_OK) s = repitch(&w, wrows, wcols, nw, nw > 1 ? groups.offsets : nullptr, ws + xb, stream);
-      if (s != GEMM_OK) return s;
-    }
     const CUtensorMapDataType dt = map_type(plan->ab);
     bool ok = w_mn ? encode_3d(&p.tmA, dt, w.p, N, K, w.ld, nw, w.stride, 64, 2 * TC_BK)
                    : encode_3d(&p.tmA, dt, w.p, K, N, w.ld, nw, w.stride, TC_BK, 128);
@@ -170,11 +157,24 @@ gemm_status_t gemm_run_grouped(gemm_plan_t plan, gemm_layout_t lb, int64_t group
   if (K > 0 && (!A || !B || lda < K || ldb < (lb == GEMM_OP_N ? K : N))) return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   EpiParams e = epilogue_of(epi, out, alpha, D, ldd);
   e.stride_bias = stride_bias;
-  return tokens_product(plan, Groups{offsets, (int32_t)groups, (int32_t)M, plan->d_err}, M, N, K, Operand{A, lda, 0},
-                        Operand{B, ldb, stride_b}, lb == GEMM_OP_T, 0, e, "grouped",
-                        reinterpret_cast<cudaStream_t>(stream_));
+  Operand x{A, lda, 0}, w{B, ldb, stride_b};
+  const bool w_mn = lb == GEMM_OP_T;
+  if (K > 0) {   // operands that TMA cannot address are copied to a pitch it can
+    const int64_t wrows = w_mn ? K : N, wcols = w_mn ? N : K, nw = stride_b != 0 ? groups : 1;
+    const size_t xb = repitch_bytes(x, M, K, 1), wb = repitch_bytes(w, wrows, wcols, nw);
+    if (xb + wb > 0) {
+      s = ensure_ws(plan, xb + wb, stream);
+      char* ws = static_cast<char*>(plan->ws);
+      if (s == GEMM_OK) s = repitch(&x, M, K, 1, nullptr, ws, stream);
+      if (s == GEMM_OK) s = repitch(&w, wrows, wcols, nw, nw > 1 ? offsets : nullptr, ws + xb, stream);
+      if (s != GEMM_OK) return s;
+    }
+  }
+  return tokens_product(plan, Groups{offsets, (int32_t)groups, (int32_t)M, plan->d_err}, M, N, K, x, w, w_mn, e, "grouped",
+                        stream);
 }
 
 gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N, int64_t K, double alpha,
@@ -203,7 +203,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
   Operand x{A, lda, 0}, y{B, ldb, 0};
   SegParams p;
   std::memset(&p, 0, sizeof(p));
-  const int cg = grouped_cg(plan, M > 128 && N > 128 ? 2 : 1);
+  const int cg = plan->pair_clusters > 0 && M > 128 && N > 128 ? 2 : 1;   // a pair's tile is 256 x 256
   p.tiles_m = (int32_t)((M + 128 * cg - 1) / (128 * cg));
   p.tiles_n = (int32_t)((N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = groups * p.tiles_m * (int64_t)p.tiles_n;
@@ -305,10 +305,8 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   const int64_t ldq = align_up((size_t)(K + 1) / 2, 16);
   const size_t qb = K == 0 || q_ok ? 0 : align_up((size_t)(groups * N * ldq), 256);
   const size_t xb = K == 0 ? 0 : repitch_bytes(x, M, K, 1);
-  int few = 64;
-  if (const char* env = std::getenv("GEMM_Q4_FEW")) few = std::atoi(env);
-  const bool prompt = per_group > few && K > 0;
-  const int64_t ldw = (K + 7) / 8 * 8;
+  const bool prompt = per_group > kQ4Few && K > 0;
+  const int64_t ldw = (K + 15) / 16 * 16;
   const size_t wb = prompt ? align_up((size_t)(groups * N * ldw) * 2, 256) : 0;
   if (qb + xb + wb > 0) {
     s = ensure_ws(plan, qb + xb + wb, stream);
@@ -326,8 +324,8 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   if (s != GEMM_OK) return s;
   if (prompt) {
     if (launch_q4_dequant(p, ws + qb + xb, ldw, N * ldw, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-    return tokens_product(plan, p.g, M, N, K, x, Operand{ws + qb + xb, ldw, groups > 1 ? N * ldw : 0}, false, qb + xb + wb,
-                          p.epi, "q4", stream);
+    return tokens_product(plan, p.g, M, N, K, x, Operand{ws + qb + xb, ldw, groups > 1 ? N * ldw : 0}, false, p.epi,
+                          "q4", stream);
   }
   const Q4Shape shape = q4_shape(N, per_group, std::min(groups, M), plan->sm_count);
   p.cta_rows = shape.cta_rows;

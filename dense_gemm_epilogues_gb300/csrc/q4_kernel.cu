@@ -24,8 +24,6 @@
 //
 // Many rows (a prompt): the weights are written once as 16-bit values s * (q - z)
 // into scratch and the products run on the tensor cores (seg_kernel.cu).
-#include <cstdlib>
-
 #include "expert.h"
 
 namespace gemmlib {
@@ -392,13 +390,28 @@ __global__ void __launch_bounds__(32 * WARPS, Q4Cfg<MT, NT>::CTAS) q4_kernel(con
   }
 }
 
-// Weights as 16-bit values s * (q - z), K-major with pitch ldw (zeros past K); groups
-// without rows are skipped.  A thread takes one word (8 k) of a column; a warp stores
-// 512 consecutive bytes.  Bound by memory (the store is four times the load): many
-// light threads keep more of it in flight than several words per thread (2 and 8
-// columns per thread took 43 and 62 us for 4096 x 11008, this 38 before it used packed
-// arithmetic).  With scales of A's own type the product s * (q - z) is one packed
-// multiplication: its exact value is rounded once, as in fp32.
+// A word's weights as neighbours (2 k, 2 k + 1): its bytes and those of the word shifted
+// by a nibble side by side.
+template <bool BF16>
+__device__ __forceinline__ void unpack_pairs(uint32_t w, uint32_t zero, uint32_t (&h)[4]) {
+  const uint32_t odd = w >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = (__byte_perm(w, odd, 0x0400u + 0x0101u * (uint32_t)i) & 0x000f000fu) | (BF16 ? 0x43004300u : 0x64006400u);
+    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(h[i]) : "r"(v), "r"(0x3F803F80u), "r"(zero));
+    else asm("add.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(v), "r"(zero));
+  }
+}
+
+// Weights as 16-bit values s * (q - z), K-major with pitch ldw (a multiple of 16; zeros
+// past K); groups without rows are skipped.  Bound by memory (the store is four times the
+// load): a thread takes 16 k of DQ_COLS columns, all of its loads before the first use and
+// 32 bytes to a store: 4096 x 11008 in 17 us, 6.6 TB/s of loads and stores (with 1, 2 or 8
+// columns a prompt of 2000 rows takes 11, 3.5 and 2.4 us longer).  With scales of A's own
+// type the product s * (q - z) is one packed multiplication: its exact value is rounded
+// once, as in fp32.
+constexpr int DQ_COLS = 4;
+
 template <bool BF16>
 __global__ void __launch_bounds__(256) q4_dequant_kernel(const __grid_constant__ Q4Params p, uint16_t* out, int64_t ldw,
                                                          int64_t stride_w) {
@@ -412,40 +425,50 @@ __global__ void __launch_bounds__(256) q4_dequant_kernel(const __grid_constant__
   const char* scales = static_cast<const char*>(p.scales) + e * p.stride_s * dtype_bytes(p.scale_dtype);
   const uint8_t* zeros = p.zeros ? p.zeros + e * p.stride_z : nullptr;
   out += e * stride_w;
-  const int row_bytes = (p.K + 1) / 2;
-  const int k = (int)(blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  const int64_t k = (int64_t)(blockIdx.x * blockDim.x + threadIdx.x) * 16;
   if (k >= ldw) return;
-  const bool packed = ((reinterpret_cast<uintptr_t>(q) | (uintptr_t)p.ldq) & 3) == 0 && k + 8 <= p.K && p.scale_dtype == p.ab_dtype;
-  const int gk = k < p.K ? k / p.group : 0;
-  for (int64_t n = blockIdx.y; n < p.N; n += gridDim.y) {
-    uint32_t o[4] = {0u, 0u, 0u, 0u};
+  const int64_t gk = k < p.K ? k / p.group : 0, step = (int64_t)gridDim.y * blockDim.y * DQ_COLS;
+  const bool packed = k + 16 <= p.K && p.scale_dtype == p.ab_dtype;
+  for (int64_t n0 = (int64_t)(blockIdx.y * blockDim.y + threadIdx.y) * DQ_COLS; n0 < p.N; n0 += step) {
     if (packed) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q + n * p.ldq + k / 2));
-      uint32_t s = __ldg(reinterpret_cast<const uint16_t*>(scales) + n * p.lds + gk), h[4];
-      s |= s << 16;
-      unpack<BF16>(w, zero_const<BF16>(zeros ? zeros[n * p.ldz + gk] & 15u : 8u), h);
+      uint2 w[DQ_COLS];
+      uint32_t s[DQ_COLS], z[DQ_COLS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(h[i]), "r"(s));
-        else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(h[i]), "r"(s));
+      for (int i = 0; i < DQ_COLS; ++i) {
+        const int64_t n = min(n0 + i, (int64_t)p.N - 1);
+        w[i] = __ldg(reinterpret_cast<const uint2*>(q + n * p.ldq + k / 2));
+        s[i] = __ldg(reinterpret_cast<const uint16_t*>(scales) + n * p.lds + gk);
+        z[i] = zeros ? __ldg(zeros + n * p.ldz + gk) : 8u;
       }
-      o[0] = __byte_perm(h[0], h[1], 0x5410);   // pairs (k, k + 4) back to neighbours
-      o[1] = __byte_perm(h[2], h[3], 0x5410);
-      o[2] = __byte_perm(h[0], h[1], 0x7632);
-      o[3] = __byte_perm(h[2], h[3], 0x7632);
-    } else if (k < p.K) {
-      const float s = load_as_float(scales, p.scale_dtype, n * p.lds + gk);
-      const int z = zeros ? zeros[n * p.ldz + gk] & 15 : 8;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t b = k / 2 + u < row_bytes ? q[n * p.ldq + k / 2 + u] : 0u;
-        const float lo4 = k + 2 * u < p.K ? s * (float)((int)(b & 15) - z) : 0.0f;
-        const float hi4 = k + 2 * u + 1 < p.K ? s * (float)((int)(b >> 4) - z) : 0.0f;
-        if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[u]) : "f"(hi4), "f"(lo4));
-        else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[u]) : "f"(hi4), "f"(lo4));
+      for (int i = 0; i < DQ_COLS; ++i) {
+        const uint32_t zc = zero_const<BF16>(z[i] & 15u).lo, s2 = s[i] * 0x00010001u;
+        uint32_t h[2][4], o[8];
+        unpack_pairs<BF16>(w[i].x, zc, h[0]);
+        unpack_pairs<BF16>(w[i].y, zc, h[1]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[j]) : "r"(h[j >> 2][j & 3]), "r"(s2));
+          else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[j]) : "r"(h[j >> 2][j & 3]), "r"(s2));
+        }
+        if (n0 + i < p.N) st_row_32b(reinterpret_cast<char*>(out + (n0 + i) * ldw + k), o);
+      }
+    } else {
+      for (int64_t n = n0; n < min(n0 + DQ_COLS, (int64_t)p.N); ++n) {
+        const float s = load_as_float(scales, p.scale_dtype, n * p.lds + gk);
+        const int z = zeros ? zeros[n * p.ldz + gk] & 15 : 8;
+        uint32_t o[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t b = k + 2 * u < p.K ? q[n * p.ldq + k / 2 + u] : 0u;
+          const float lo4 = k + 2 * u < p.K ? s * (float)((int)(b & 15) - z) : 0.0f;
+          const float hi4 = k + 2 * u + 1 < p.K ? s * (float)((int)(b >> 4) - z) : 0.0f;
+          if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[u]) : "f"(hi4), "f"(lo4));
+          else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[u]) : "f"(hi4), "f"(lo4));
+        }
+        st_row_32b(reinterpret_cast<char*>(out + n * ldw + k), o);
       }
     }
-    *reinterpret_cast<uint4*>(out + n * ldw + k) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -519,8 +542,7 @@ Q4Shape q4_shape(int64_t N, int64_t rows_per_group, int64_t groups_used, int sm_
   const int64_t most = s.nt == 1 ? 48 : 32, resident = (int64_t)sm_count * (s.nt == 4 ? 1 : 2);
   const int64_t columns = groups_used * N, waves = (columns + resident * most - 1) / (resident * most);
   const int64_t per_group = std::max<int64_t>(1, waves * resident / groups_used);   // CTAs of a group
-  int64_t rows = std::max<int64_t>(8, (N + per_group - 1) / per_group);
-  if (const char* env = std::getenv("GEMM_Q4_ROWS")) rows = std::max(1, std::atoi(env));
+  const int64_t rows = std::max<int64_t>(8, (N + per_group - 1) / per_group);
   s.cta_rows = (int)std::min(std::min(most, rows), N);
   return s;
 }
@@ -530,11 +552,16 @@ cudaError_t launch_q4(const Q4Params& p, int nt, cudaStream_t stream) {
 }
 
 cudaError_t launch_q4_dequant(const Q4Params& p, void* out, int64_t ldw, int64_t stride_w, cudaStream_t stream) {
-  const dim3 grid((unsigned)((ldw / 8 + 255) / 256), (unsigned)std::min(p.N, 65535),
+  int tx = 1;   // threads along K
+  while (tx < 256 && tx * 16 < ldw) tx *= 2;
+  const int ty = 256 / tx;
+  const int64_t per_cta = (int64_t)ty * DQ_COLS;
+  const dim3 grid((unsigned)((ldw / 16 + tx - 1) / tx), (unsigned)std::min<int64_t>((p.N + per_cta - 1) / per_cta, 65535),
                   (unsigned)p.g.count);
   uint16_t* o = static_cast<uint16_t*>(out);
-  return p.ab_dtype == GEMM_BF16 ? launch_dependent(q4_dequant_kernel<true>, grid, 256, stream, p, o, ldw, stride_w)
-                                 : launch_dependent(q4_dequant_kernel<false>, grid, 256, stream, p, o, ldw, stride_w);
+  const dim3 block((unsigned)tx, (unsigned)ty);
+  return p.ab_dtype == GEMM_BF16 ? launch_dependent(q4_dequant_kernel<true>, grid, block, stream, p, o, ldw, stride_w)
+                                 : launch_dependent(q4_dequant_kernel<false>, grid, block, stream, p, o, ldw, stride_w);
 }
 
 }  // namespace gemmlib

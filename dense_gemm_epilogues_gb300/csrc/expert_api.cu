@@ -65,9 +65,24 @@ gemm_status_t repitch(Operand* x, int64_t rows, int64_t cols, int64_t batch, con
   return GEMM_OK;
 }
 
-// Rows of an average expert up to which 4-bit weights are decoded inside the product;
-// beyond, they are decoded once into scratch and multiplied on the tensor-core kernel.
-constexpr int64_t kQ4Few = 64;
+// Are 4-bit weights decoded once into scratch and multiplied on the tensor-core kernel,
+// rather than inside the product, once per 32 rows?  Up to 32 rows never (one pass over
+// the weights, exact integers).  Beyond, by the times that both take: a pass inside the
+// product 0.5 ps per weight on the whole chip; decoding once 0.38, and each wave of
+// 128 x 128 tiles 0.7 us per 128 k.  Measured, inside / once, us:
+//                                 33 rows        64             96             128 per expert
+//   4096 -> 11008                 45.0 / 40.5    47.0 / 40.9    68.6 / 41.5    90.4 / 43.2
+//   4096 -> 4096                  17.2 / 29.0    17.7 / 29.1    25.8 / 29.5    33.7 / 31.2
+//   11008 -> 4096                 33.7 / 70.1    34.3 / 70.2    50.4 / 70.8    66.8 / 72.6
+//   2048 -> 1408, 16 experts      43.0 / 45.3    70.4 / 46.2    97.6 / 46.6    124 / 49.7
+bool q4_decode_once(int64_t N, int64_t K, int64_t rows, int64_t groups, int sm_count) {
+  if (rows <= 32 || K == 0) return false;
+  const double weights = (double)N * (double)K * (double)groups;
+  const int64_t tiles = (N + 127) / 128 * ((rows + 127) / 128) * groups, waves = (tiles + sm_count - 1) / sm_count;
+  const double inside = 0.5e-6 * weights * (double)((rows + 31) / 32);
+  const double once = 0.38e-6 * weights + 0.7 * (double)((K + 127) / 128) * (double)waves + 4.0;
+  return once < inside;
+}
 
 int workers_of(const gemm_plan* plan, int cg, int64_t tiles) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(tiles, cg == 2 ? plan->pair_clusters : plan->sm_count));
@@ -305,7 +320,7 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   const int64_t ldq = align_up((size_t)(K + 1) / 2, 16);
   const size_t qb = K == 0 || q_ok ? 0 : align_up((size_t)(groups * N * ldq), 256);
   const size_t xb = K == 0 ? 0 : repitch_bytes(x, M, K, 1);
-  const bool prompt = per_group > kQ4Few && K > 0;
+  const bool prompt = q4_decode_once(N, K, per_group, std::min(groups, M), plan->sm_count);
   const int64_t ldw = (K + 15) / 16 * 16;
   const size_t wb = prompt ? align_up((size_t)(groups * N * ldw) * 2, 256) : 0;
   if (qb + xb + wb > 0) {

@@ -483,6 +483,14 @@ gemm_status_t gemm_noalloc_set_timeout(uint64_t timeout_ns);
  * gemm_plan_device_status then reports GEMM_ERR_INVALID_ARG.
  * ======================================================================== */
 
+/* In PyTorch terms these are grouped_matmul, grouped_weight_grad, q4_matmul (with
+ * quantize_q4) and orthogonalize of the Python package.  Operands at any alignment and
+ * pitch are taken; one that TMA cannot address (a base off 16 bytes, or rows that are not
+ * a multiple of 16 bytes apart) costs a copy into the plan's scratch.  As for gemm_run,
+ * calls that overlap on the GPU need a plan each.
+ * gemm_plan_last_config describes the tensor-core launch; gemm_run_q4 with few rows
+ * reports GEMM_KERNEL_SIMT. */
+
 /* ---------------------------------------------------------------------------
  * gemm_run_grouped -- every row times its group's matrix:
  *     D[r, :] = act( alpha * A[r, :] * op(B_g) + bias_g ),   r in group g,
@@ -527,8 +535,14 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
  *     D[r, n] = act( alpha * sum_k A[r, k] * w[n, k] + bias[n] ),
  *     w[n, k] = scale[n, k / group_size] * (q[n, k] - zero[n, k / group_size]).
  * Any number of rows: one token (each weight is read once) up to a prompt.
+ * Up to 32 rows per expert on average every term is exact up to the fp32 sum: q - zero is
+ * an integer and the scale multiplies the sum of its group.  Beyond, where that is
+ * faster, each w is rounded once to A's type, into scratch of 2 bytes per weight (so such
+ * a call's first use in a stream capture needs an earlier one of its size), and multiplied
+ * on the tensor cores.
  * With `offsets`, row r uses the weights, scales, zeros and bias of its group
  * (experts); NULL with groups == 1 is a dense layer.
+ * ld_scales and ld_zeros below 2^23 (else GEMM_ERR_UNSUPPORTED).
  *   plan        ab_dtype F16 or BF16: the type of A (else GEMM_ERR_UNSUPPORTED).
  *   M, N, K     rows of A and D, output columns, depth.
  *   D, epi, stride_bias   as for gemm_run_grouped.
@@ -562,8 +576,15 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
  *   G, ldg      row-major M x N (M > N runs on the transpose), stride_g elements
  *               from matrix to matrix (0: one matrix for all).
  *   D, ldd      row-major, out_dtype F32, F16 or BF16.
- * X is held in fp16 between the products (times a power of two that keeps it out
- * of the subnormals); sums are fp32.  A zero matrix gives zero; NaN or infinity
+ * At most 65535 matrices and 64 steps.  X is held in fp16 between the products (times a
+ * power of two that keeps it out of the subnormals); sums are fp32.  Directions that
+ * a matrix lacks (the gradient of fewer rows than its sizes) collect that rounding, which
+ * every step multiplies by a: with the usual coefficients and 5 steps a noise of a few
+ * per cent of the result's norm.  The sum of squares has
+ * one order, so a matrix gives the same bits alone, in a batch, and transposed.
+ * All products of all steps are one cooperative launch whose CTAs wait for one another's
+ * tiles; as everywhere each wait ends after the plan's bound, and
+ * gemm_plan_device_status then reports GEMM_ERR_TIMEOUT.  A zero matrix gives zero; NaN or infinity
  * anywhere in a matrix makes that whole result NaN.
  * ------------------------------------------------------------------------- */
 gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int64_t N, int steps,

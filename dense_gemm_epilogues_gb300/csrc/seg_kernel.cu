@@ -385,14 +385,38 @@ struct Tiles {
       o.k = g.cnt[o.e];
     } else {
       if (t >= p.num_tiles) return false;
-      const int sym = p.batch * p.tiles_per_group, dense = p.batch * p.tiles_m * p.tiles_n;
-      o.step = t / (2 * sym + dense);
-      int local = t - o.step * (2 * sym + dense);
-      if (local < 2 * sym) {
-        o.product = local >= sym ? 1 : 0;
-        local -= o.product * sym;
-        o.e = local / p.tiles_per_group;
-        local -= o.e * p.tiles_per_group;
+      // Segments of one turn over the two halves A, B of the batch (B one phase and a half
+      // behind): E_A, B's X of the step before, F_A, E_B, X_A, F_B.
+      const int a = (p.batch + 1) / 2, b = p.batch - a, sym = p.tiles_per_group, dense = p.tiles_m * p.tiles_n;
+      const int turn = p.batch * (2 * sym + dense);
+      int local = t;
+      if (local >= a * sym) local += b * dense;            // the first turn has no X_B,
+      if (local >= p.steps * turn) local += a * sym;       // the one after the last nothing else
+      o.step = local / turn;
+      local -= o.step * turn;
+      o.e = 0;
+      if (local < a * sym) {
+        o.product = 0;
+      } else if ((local -= a * sym) < b * dense) {
+        o.product = 2;
+        o.e = a;
+        --o.step;
+      } else if ((local -= b * dense) < a * sym) {
+        o.product = 1;
+      } else if ((local -= a * sym) < b * sym) {
+        o.product = 0;
+        o.e = a;
+      } else if ((local -= b * sym) < a * dense) {
+        o.product = 2;
+      } else {
+        local -= a * dense;
+        o.product = 1;
+        o.e = a;
+      }
+      if (o.product < 2) {
+        const int z = local / sym;
+        o.e += z;
+        local -= z * sym;
         // Block row tm has (tm + 1) * r tiles of bns columns, r to a block.
         const int r = BM / p.bns, q = local / r;
         int tm = (int)((sqrtf(8.0f * (float)q + 1.0f) - 1.0f) * 0.5f);
@@ -404,10 +428,9 @@ struct Tiles {
         o.n_mma = p.bns;
         o.k = o.product == 0 ? p.N : (int)p.M;
       } else {
-        local -= 2 * sym;
-        o.product = 2;
-        o.e = local / (p.tiles_m * p.tiles_n);
-        local -= o.e * p.tiles_m * p.tiles_n;
+        const int z = local / dense;
+        o.e += z;
+        local -= z * dense;
         // Bands of 8 tile rows; in a band the row runs fastest.
         const int band = local / (8 * p.tiles_n), first = band * 8, size = min(8, p.tiles_m - first);
         const int r = local - first * p.tiles_n, tn = r / size;
@@ -760,7 +783,7 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
       auto ext = [](int cols) { return MODE == SEG_CHAIN ? min(32, (cols + 7) & ~7) : cols; };
       if constexpr (MODE == SEG_CHAIN) {
         const bool late = t.step >= p.steps - 2, last = t.step == p.steps - 1;
-        __half *X = p.chain.x[t.step & 1], *Y = p.chain.x[(t.step + 1) & 1];
+        __half* Y = p.chain.x[(t.step + 1) & 1];
         ep.ldc = p.chain.lde;
         ep.ldd = p.chain.lde;
         ep.d_dtype = GEMM_F16;
@@ -775,13 +798,12 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
         } else if (t.product == 1) {
           ep.alpha = p.chain.c;
           ep.beta = late ? p.chain.b[1] : p.chain.b[0];
+          shift = late ? -p.chain.a[1] : -p.chain.a[0];
           ptr.D = p.chain.f + t.e * p.chain.stride_e;
           store_t = t.n0 < t.m0;
         } else {
           ep.alpha = last ? p.chain.inv_scale : 1.0f;
-          ep.beta = (late ? p.chain.a[1] : p.chain.a[0]) * ep.alpha;
-          ptr.C = X + t.e * p.chain.stride_x;
-          ep.ldc = p.chain.ldx;
+          ep.read_c = 0;
           ep.ldd = p.chain.ldx;
           ptr.D = Y + t.e * p.chain.stride_x;
           if (last) {

@@ -8,13 +8,14 @@ namespace {
 
 // Both passes over G work on TILE x TILE tiles of the wide matrix X (G or its
 // transpose), in units of 8 consecutive entries of a row of X, two units per thread.  A
-// unit lies contiguous in G when X is G; when X is G's transpose, or G's rows are not on 16 bytes, the
-// tile is loaded along G's rows and arranged in shared memory.  Either way every thread meets the
+// unit lies contiguous in G when X is G, at any alignment (then it is put together from
+// aligned words); when X is G's transpose, the tile is loaded along G's rows and arranged
+// in shared memory.  Either way every thread meets the
 // same units in the same order, so the sum of squares has one order, fixed by X's shape
 // alone: a matrix, its transpose, and any batch around it give the same bits.
 // Bound by memory: G is read twice (the second time from L2 when it fits) and X
-// written once.  Many light threads, one tile's two units in flight each: four tiles' units
-// per thread halved the warps and took 47 and 69 us for 4096 x 11008 (this: 30 and 37).
+// written once.  Many light threads; the next tile's units are under way while one tile
+// is worked on, and the first of the second pass while the norm is added up.
 constexpr int TILE = 64;
 
 template <typename T>
@@ -32,37 +33,60 @@ __device__ __forceinline__ int unit_col() { return (int)(threadIdx.x & 7) * 8; }
 template <typename T>
 __device__ __forceinline__ void load_unit(const T* g, const OrthoInput& in, int64_t r, int64_t c, T (&v)[8]) {
   const T* src = g + r * in.ld + c;
-  if (r < in.m && c + 8 <= in.n) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(v);
+  // (aligned words around a 16-bit unit reach two bytes past it: not at the matrix's ends)
+  if (in.vec && r < in.m && c + 8 <= in.n) {
     constexpr int W = (int)sizeof(T) * 8 / 16;
 #pragma unroll
-    for (int w = 0; w < W; ++w) reinterpret_cast<uint4*>(v)[w] = reinterpret_cast<const uint4*>(src)[w];
+    for (int i = 0; i < W; ++i) reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(src)[i];
+  } else if (!in.vec && r < in.m && c + 8 < in.n && r + c > 0) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
+    constexpr int W = (int)sizeof(T) * 8 / 4;
+    uint32_t u[W + 1];
+#pragma unroll
+    for (int i = 0; i < W; ++i) u[i] = p[i];
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t shift = (uint32_t)(at & 3) * 8;
+      u[W] = shift ? p[W] : 0u;
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(u[i], u[i + 1], shift);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = u[i];
+    }
   } else {
 #pragma unroll
     for (int u = 0; u < 8; ++u) v[u] = r < in.m && c + u < in.n ? src[u] : T(0.0f);
   }
 }
 
-// tile[r][c] = X[r0 + r, c0 + c] (zero outside) by way of shared memory: G's rows 16 bytes
+// This thread's units of tile t.
+template <typename T>
+__device__ __forceinline__ void load_units(const T* g, const OrthoInput& in, int t, int tiles_n, T (&v)[2][8]) {
+  const int64_t r0 = (int64_t)(t / tiles_n) * TILE, c = (int64_t)(t % tiles_n) * TILE + unit_col();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) load_unit(g, in, r0 + unit_row(u), c, v[u]);
+}
+
+// tile[r][c] = X[r0 + r, c0 + c] (zero outside), X being G's transpose: G's rows 16 bytes
 // at a time where they lie on 16 bytes, else element by element, 64 to a row.
 template <typename T>
 __device__ __forceinline__ void load_turned(const T* g, const OrthoInput& in, int64_t r0, int64_t c0,
                                             float (&tile)[TILE][TILE + 1]) {
   constexpr int V = 16 / (int)sizeof(T), PER_ROW = TILE / V;
   if (!in.vec) {
-    const int64_t i0 = in.transpose ? c0 : r0, j0 = in.transpose ? r0 : c0;
-    const int64_t ni = in.transpose ? in.n : in.m, nj = in.transpose ? in.m : in.n;
     const int j = (int)threadIdx.x & 63;
     T v[16];
 #pragma unroll
     for (int h = 0; h < 16; ++h) {
       const int i = 4 * h + (int)(threadIdx.x >> 6);
-      v[h] = i0 + i < ni && j0 + j < nj ? g[(i0 + i) * in.ld + j0 + j] : T(0.0f);
+      v[h] = c0 + i < in.n && r0 + j < in.m ? g[(c0 + i) * in.ld + r0 + j] : T(0.0f);
     }
 #pragma unroll
     for (int h = 0; h < 16; ++h) {
       const int i = 4 * h + (int)(threadIdx.x >> 6);
-      if (in.transpose) tile[j][i] = widen(v[h]);
-      else tile[i][j] = widen(v[h]);
+      tile[j][i] = widen(v[h]);
     }
     return;
   }
@@ -116,12 +140,12 @@ __global__ void __launch_bounds__(256) sumsq_kernel(const OrthoInput in, float* 
        i += (int64_t)gridDim.x * gridDim.y * 256)
     counters[i] = 0;
   const T* g = static_cast<const T*>(in.g) + blockIdx.y * in.stride;
-  const int64_t tiles_n = (in.n + TILE - 1) / TILE, tiles = (in.m + TILE - 1) / TILE * tiles_n;
+  const int tiles_n = (int)((in.n + TILE - 1) / TILE), tiles = (int)((in.m + TILE - 1) / TILE) * tiles_n;
   float s = 0.0f, x[2][8];
-  if (in.transpose || !in.vec) {
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+  if (in.transpose) {
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       __syncthreads();
-      load_turned(g, in, t / tiles_n * TILE, t % tiles_n * TILE, tile);
+      load_turned(g, in, (int64_t)(t / tiles_n) * TILE, (int64_t)(t % tiles_n) * TILE, tile);
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -130,14 +154,14 @@ __global__ void __launch_bounds__(256) sumsq_kernel(const OrthoInput in, float* 
       s += squares(x);
     }
   } else {
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-      __align__(16) T v[2][8];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) load_unit(g, in, t / tiles_n * TILE + unit_row(u), t % tiles_n * TILE + unit_col(), v[u]);
+    __align__(16) T v[2][8];
+    load_units(g, in, blockIdx.x, tiles_n, v);
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[u][k] = widen(v[u][k]);
+      if (t + (int)gridDim.x < tiles) load_units(g, in, t + (int)gridDim.x, tiles_n, v);
       s += squares(x);
     }
   }
@@ -152,12 +176,14 @@ __global__ void __launch_bounds__(256) normalize_kernel(const OrthoInput in, con
                                                         int64_t stride_x) {
   __shared__ float tile[TILE][TILE + 1];
   pdl_wait();
+  const T* g = static_cast<const T*>(in.g) + blockIdx.y * in.stride;
+  const int tiles_n = (int)((ldx + TILE - 1) / TILE), tiles = (int)((in.m + TILE - 1) / TILE) * tiles_n;
+  __align__(16) T v[2][8];
+  if (!in.transpose) load_units(g, in, blockIdx.x, tiles_n, v);
   float s = 0.0f;
   for (int i = threadIdx.x; i < slots; i += 256) s += partials[blockIdx.y * slots + i];
   const float f = scale / (sqrtf(block_sum(s)) + eps);
-  const T* g = static_cast<const T*>(in.g) + blockIdx.y * in.stride;
   x += blockIdx.y * stride_x;
-  const int64_t tiles_n = (ldx + TILE - 1) / TILE, tiles = (in.m + TILE - 1) / TILE * tiles_n;
   auto store = [&](int64_t r, int64_t c, const float (&e)[8]) {
     if (r >= in.m || c >= ldx) return;
     __half2 h[4];
@@ -165,33 +191,26 @@ __global__ void __launch_bounds__(256) normalize_kernel(const OrthoInput in, con
     for (int k = 0; k < 4; ++k) h[k] = __floats2half2_rn(e[2 * k] * f, e[2 * k + 1] * f);
     *reinterpret_cast<uint4*>(x + r * ldx + c) = *reinterpret_cast<uint4*>(h);
   };
-  float e[8];
-  if (in.transpose || !in.vec) {
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const int64_t r0 = t / tiles_n * TILE, c0 = t % tiles_n * TILE;
+  float e[2][8];
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t r0 = (int64_t)(t / tiles_n) * TILE, c0 = (int64_t)(t % tiles_n) * TILE;
+    if (in.transpose) {
       __syncthreads();
       load_turned(g, in, r0, c0, tile);
       __syncthreads();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = tile[unit_row(u)][unit_col() + k];
-        store(r0 + unit_row(u), c0 + unit_col(), e);
-      }
+        for (int k = 0; k < 8; ++k) e[u][k] = tile[unit_row(u)][unit_col() + k];
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[u][k] = widen(v[u][k]);
+      if (t + (int)gridDim.x < tiles) load_units(g, in, t + (int)gridDim.x, tiles_n, v);
     }
-  } else {
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const int64_t r0 = t / tiles_n * TILE, c0 = t % tiles_n * TILE + unit_col();
-      __align__(16) T v[2][8];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) load_unit(g, in, r0 + unit_row(u), c0, v[u]);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = widen(v[u][k]);
-        store(r0 + unit_row(u), c0, e);
-      }
-    }
+    for (int u = 0; u < 2; ++u) store(r0 + unit_row(u), c0 + unit_col(), e[u]);
   }
 }
 
@@ -215,14 +234,16 @@ cudaError_t launch_ortho_input(const OrthoInput& in, int64_t batch, float* parti
   cudaError_t e = launch_dependent(sumsq_kernel<T>, dim3((unsigned)slots, (unsigned)batch), 256, stream, in, partials,
                                    counters, num_counters);
   if (e != cudaSuccess) return e;
-  return launch_dependent(normalize_kernel<T>, dim3((unsigned)std::min<int64_t>(tiles, 1216), (unsigned)batch), 256, stream,
+  return launch_dependent(normalize_kernel<T>, dim3((unsigned)std::min<int64_t>(tiles, std::max<int64_t>(1216 / batch, 76)), (unsigned)batch), 256, stream,
                           in, (const float*)partials, slots, eps, scale, x, ldx, stride_x);
 }
 
 }  // namespace
 
 int ortho_slots(int64_t m, int64_t n) {
-  return (int)std::min<int64_t>(((m + TILE - 1) / TILE) * ((n + TILE - 1) / TILE), 608);
+  // (by the shape alone, whatever the batch) four tiles each, once that fills the chip
+  const int64_t tiles = ((m + TILE - 1) / TILE) * ((n + TILE - 1) / TILE);
+  return (int)std::min<int64_t>(1216, std::max<int64_t>(std::min<int64_t>(tiles, 152), (tiles + 3) / 4));
 }
 
 cudaError_t launch_ortho_input(const OrthoInput& in, int dtype, int64_t batch, float* partials, float eps, float scale,

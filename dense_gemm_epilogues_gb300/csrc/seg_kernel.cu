@@ -29,8 +29,9 @@
 // CHAIN: E and F are symmetric, so only tiles on and below the diagonal are computed
 // and each is stored twice, as it is and transposed.  The tiles of all phases form one
 // list (step by step, product by product, matrix by matrix, the two halves of a batch a
-// phase apart) that the workers take in turn.  A tile waits, per 256-row (CG = 1: 128-row) block of the matrices that it
-// reads, for a counter of the finished tiles of that block row:
+// phase apart) that the workers take in turn.  A tile waits, per 256-row (CG = 1:
+// 128-row) block of the matrices that it reads, for a counter of the finished tiles of
+// that block row:
 //   E(i, j) waits for rows i and j of X (the last step's F X tiles),
 //   F(i, j) for rows i and j of E, and F X (i, n) for row i of F -- which has needed all
 //   of E, and that all of X.
@@ -40,6 +41,16 @@
 // cooperative launch), so the earliest unfinished tile can always run.  One launch in
 // place of three per step saves the launches' fixed cost (6-8 us each, all of a small
 // matrix's time) and lets the matrices of a batch fill each other's last waves.
+//
+// Measured (graph replays): 16384 rows over 64 experts, 2048 to 4096, bf16: 242 us, 5.3 TB/s
+// of the operands' bytes, 78 % of a copy; over 32 experts, 4096 x 2048, input and weight
+// gradient together: 431 us, 1.28 PFLOP/s, held by operand supply; 16 rows over 8 experts,
+// 1024 to 2048: 10.1 us, the latency of a launch and eight stages.  Newton-Schulz, five
+// steps: 4096 x 11008 2.16 ms with its input passes, 1.44 PFLOP/s (the symmetric products
+// counted half), at the power cap; 16 x 768 x 2001 390 us (a tile of 768 k takes 6.3 us
+// for 3.9 us of MMAs: L2 traffic); 384 x 256 90 us, 15 dependent products of 5.5 us.
+// Why three stages of two slabs, one producer: six stages of one slab 257 us for the first
+// case above, stages as small as the tile 250, a second producer thread 242.
 //
 // Every wait is bounded, as in tc_kernel.cu.
 #include "expert.h"

@@ -77,6 +77,19 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
     if (globaltimer_ns() - t0 > timeout_ns) return;
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(one));
+  return one != 0;
+}
+
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
   const bool ok = mbar_wait(bar, parity, wc);
   return __all_sync(0xffffffffu, ok) != 0;
@@ -544,7 +557,7 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
   auto tempty_bar = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 + b); };
   const uint32_t teardown_bar = bar0 + 8u * (uint32_t)(2 * STAGES + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (uniform)
   const uint32_t rank = CG == 2 ? (cluster_ctarank() & 1u) : 0u;
   const bool leader = rank == 0;
   const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
@@ -698,7 +711,11 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
     }
   } else if (warp == 1) {
     // ------------------------ MMA issuer (the leader's) -----------------------
-    if (leader && lane == 0) {
+    // The whole warp walks the list and waits; one lane issues.  A stage's eight MMAs stand
+    // in a row, their descriptors a constant apart: computed one by one, behind a test
+    // each, they took 100 clocks apiece to issue, more than tiles of 64 columns take to run.
+    if (leader) {
+      const bool one = elect_one();
       int stage = 0;
       uint32_t phase = 0, acc_it = 0;
       bool ok = true;
@@ -707,7 +724,7 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
       while (ok && it.next(t)) {
         if (t.k == 0) continue;
         const int buf = (int)(acc_it & 1u);
-        if (!mbar_wait(tempty_bar(buf), ((acc_it >> 1) & 1u) ^ 1u, wc)) { ok = false; break; }
+        if (!warp_wait(tempty_bar(buf), ((acc_it >> 1) & 1u) ^ 1u, wc)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN);
         const bool b_mn = MODE == SEG_CHAIN ? t.product == 2 : B_MN;
@@ -715,34 +732,54 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
                                ((MODE == SEG_CHAIN && b_mn ? 1u : 0u) << 16);   // bit 16: N side MN-major
         const int num_kb = (t.k + TC_BK - 1) / TC_BK, num_k16 = (t.k + 15) / 16;
         for (int kb = 0; kb < num_kb; kb += SLABS) {
-          if (!mbar_wait(full_bar(stage), phase, wc)) { ok = false; break; }
+          if (!warp_wait(full_bar(stage), phase, wc)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sa = base + (uint32_t)(stage * STAGE_BYTES), sb = sa + (uint32_t)OPERAND_BYTES;
+          auto issue = [&](auto mn, int count) {
+            constexpr bool MN = decltype(mn)::value != 0;
+            const uint64_t ad = A_MN ? smem_desc_sw128(sa, MN_BOX_BYTES, 1024) : smem_desc_sw128(sa, 16, 1024);
+            const uint64_t bd = MN ? smem_desc_sw128(sb, MN_BOX_BYTES, 1024) : smem_desc_sw128(sb, 16, 1024);
+            auto mma = [&](int q) {
+              // Steps of 16 k: 2048 bytes of an MN-major operand; 32 bytes of a K-major slab's rows.
+              const uint32_t km = (uint32_t)(q / (TC_BK / 16) * SLAB_BYTES + q % (TC_BK / 16) * 32) >> 4;
+              const uint32_t mm = (uint32_t)q * 2048u >> 4;
+              const uint32_t acc = q > 0 || kb > 0 ? 1u : 0u;
+              if constexpr (CG == 2) tc_mma_f16_pair(d_tmem, ad + (A_MN ? mm : km), bd + (MN ? mm : km), idesc, acc);
+              else tc_mma_f16(d_tmem, ad + (A_MN ? mm : km), bd + (MN ? mm : km), idesc, acc);
+            };
+            if (count >= SLABS * (TC_BK / 16)) {
 #pragma unroll
-          for (int q = 0; q < SLABS * (TC_BK / 16); ++q) {
-            const int sl = q / (TC_BK / 16), kk = q % (TC_BK / 16);
-            if (kb * (TC_BK / 16) + q < num_k16) {
-              const uint64_t ad = A_MN ? smem_desc_sw128(sa + q * 2048u, MN_BOX_BYTES, 1024)
-                                       : smem_desc_sw128(sa + sl * SLAB_BYTES + kk * 32u, 16, 1024);
-              const uint64_t bd = b_mn ? smem_desc_sw128(sb + q * 2048u, MN_BOX_BYTES, 1024)
-                                       : smem_desc_sw128(sb + sl * SLAB_BYTES + kk * 32u, 16, 1024);
-              if constexpr (CG == 2) tc_mma_f16_pair(d_tmem, ad, bd, idesc, (kb > 0 || q > 0) ? 1u : 0u);
-              else tc_mma_f16(d_tmem, ad, bd, idesc, (kb > 0 || q > 0) ? 1u : 0u);
+              for (int q = 0; q < SLABS * (TC_BK / 16); ++q) mma(q);
+            } else {
+#pragma unroll 1
+              for (int q = 0; q < count; ++q) mma(q);
             }
+          };
+          if (one) {
+            const int count = num_k16 - kb * (TC_BK / 16);
+            if (MODE == SEG_CHAIN ? b_mn : B_MN) issue(TypeTag<1>{}, count);
+            else issue(TypeTag<0>{}, count);
+            if constexpr (CG == 2) tc_commit_pair_mask(empty_bar(stage), 0x3);
+            else tc_commit(empty_bar(stage));
           }
-          if constexpr (CG == 2) tc_commit_pair_mask(empty_bar(stage), 0x3);
-          else tc_commit(empty_bar(stage));
+          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        if constexpr (CG == 2) tc_commit_pair_mask(tfull_bar(buf), 0x3);
-        else tc_commit(tfull_bar(buf));
+        if (one) {
+          if constexpr (CG == 2) tc_commit_pair_mask(tfull_bar(buf), 0x3);
+          else tc_commit(tfull_bar(buf));
+        }
+        __syncwarp();
         ++acc_it;
       }
       // Every MMA is complete before tensor memory is freed.
-      if constexpr (CG == 2) tc_commit_pair(teardown_bar);
-      else tc_commit(teardown_bar);
-      drain_wait(teardown_bar, 0, p.timeout_ns);
+      if (one) {
+        if constexpr (CG == 2) tc_commit_pair(teardown_bar);
+        else tc_commit(teardown_bar);
+        drain_wait(teardown_bar, 0, p.timeout_ns);
+      }
+      __syncwarp();
     }
   } else if (MODE == SEG_CHAIN && warp == 2 + EPI_WARPS) {
     // ---------------------------------- scout ----------------------------------

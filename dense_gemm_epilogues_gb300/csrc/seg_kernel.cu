@@ -620,95 +620,104 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
 
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, last_parity = 0;
-      bool ok = true;
-      // WGRAD: a group's tensor maps are acquired and fetched a tile ahead of their use.
-      int map_of = -1;
-      auto acquire_maps = [&](const Tile& a) {
-        if (a.k == 0 || a.e == map_of) return;
-        map_of = a.e;
+    // (The whole warp walks the list and waits, one lane issues: see the MMA issuer.)
+    const bool one = elect_one();
+    int stage = 0, issued = 0;   // stages filled so far
+    uint32_t phase = 0;
+    bool ok = true;
+    // WGRAD: a group's tensor maps are acquired and fetched a tile ahead of their use.
+    int map_of = -1;
+    auto acquire_maps = [&](const Tile& a) {
+      if (a.k == 0 || a.e == map_of) return;
+      map_of = a.e;
+      if (one) {
         for (int i = 0; i < 2; ++i) {
           tensormap_acquire(p.group_maps + 2 * a.e + i);
           tma_prefetch_desc(p.group_maps + 2 * a.e + i);
         }
-      };
-      Tiles<MODE, CG> it(p, groups, worker, workers);
-      int tile_no = 0;   // CHAIN
-      Tile t, ahead;
-      bool more = it.next(ahead);
-      if (MODE == SEG_WGRAD && more) acquire_maps(ahead);
-      while (ok && more) {
-        t = ahead;
-        more = it.next(ahead);
-        const CUtensorMap *ma = &p.tmA, *mb = &p.tmB[0];
-        int za = 0, zb = 0;
-        const int m0 = t.m0 + (int)rank * 128, n0 = t.n0 + (int)rank * (t.n_mma / CG);
-        uint32_t b_slab = (uint32_t)SLAB_BYTES;   // N-side bytes of one K-major slab
-        if constexpr (MODE == SEG_TOKENS) {
-          za = p.a_batched ? t.e : 0;
-          int box = 0;                            // boxes of 128, 64, 32, 16, 8 rows: the smallest that holds the tile's
-          while (box < 4 && (64 >> box) >= t.n_mma / CG) ++box;
-          mb = &p.tmB[box];
-          b_slab >>= box;
-        } else if constexpr (MODE == SEG_WGRAD) {
-          ma = p.group_maps + 2 * t.e;
-          mb = ma + 1;
-        } else {
-          za = zb = t.e;
-          const int cur = t.step & 1;
-          ma = t.product == 0 ? &p.tmB[CHAIN_XK + cur] : t.product == 1 ? &p.tmA : &p.tmB[CHAIN_F];
-          mb = t.product == 0 ? &p.tmB[CHAIN_XB + cur] : t.product == 1 ? &p.tmB[CHAIN_EB] : &p.tmB[CHAIN_XN + cur];
-          b_slab = t.product == 2 ? (uint32_t)SLAB_BYTES : (uint32_t)(p.bns / CG * TC_BK * 2);
-          if (!chain_seen(ready_seq, tile_no++, wc)) { ok = false; break; }
-        }
-        // N side contiguous along N (weights' gradients, X) rather than along K.
-        const bool b_mn = MODE == SEG_CHAIN ? t.product == 2 : B_MN;
-        const int num_kb = (t.k + TC_BK - 1) / TC_BK;
-        for (int kb = 0; kb < num_kb; kb += SLABS) {
-          const int nsl = min(SLABS, num_kb - kb);
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) { ok = false; break; }
-          const uint32_t a_bytes = (uint32_t)(A_MN ? SLABS : nsl) * (uint32_t)SLAB_BYTES;
-          const uint32_t b_bytes = (uint32_t)(b_mn ? SLABS : nsl) * (MODE == SEG_CHAIN && b_mn && t.n_mma <= 64 * CG ? b_slab / 2 : b_slab);
-          if (leader) mbar_expect_tx(full_bar(stage), (uint32_t)CG * (a_bytes + b_bytes));
+      }
+      __syncwarp();
+    };
+    Tiles<MODE, CG> it(p, groups, worker, workers);
+    int tile_no = 0;   // CHAIN
+    Tile t, ahead;
+    bool more = it.next(ahead);
+    if (MODE == SEG_WGRAD && more) acquire_maps(ahead);
+    while (ok && more) {
+      t = ahead;
+      more = it.next(ahead);
+      const CUtensorMap *ma = &p.tmA, *mb = &p.tmB[0];
+      int za = 0, zb = 0;
+      const int m0 = t.m0 + (int)rank * 128, n0 = t.n0 + (int)rank * (t.n_mma / CG);
+      uint32_t b_slab = (uint32_t)SLAB_BYTES;   // N-side bytes of one K-major slab
+      if constexpr (MODE == SEG_TOKENS) {
+        za = p.a_batched ? t.e : 0;
+        int box = 0;                            // boxes of 128, 64, 32, 16, 8 rows: the smallest that holds the tile's
+        while (box < 4 && (64 >> box) >= t.n_mma / CG) ++box;
+        mb = &p.tmB[box];
+        b_slab >>= box;
+      } else if constexpr (MODE == SEG_WGRAD) {
+        ma = p.group_maps + 2 * t.e;
+        mb = ma + 1;
+      } else {
+        za = zb = t.e;
+        const int cur = t.step & 1;
+        ma = t.product == 0 ? &p.tmB[CHAIN_XK + cur] : t.product == 1 ? &p.tmA : &p.tmB[CHAIN_F];
+        mb = t.product == 0 ? &p.tmB[CHAIN_XB + cur] : t.product == 1 ? &p.tmB[CHAIN_EB] : &p.tmB[CHAIN_XN + cur];
+        b_slab = t.product == 2 ? (uint32_t)SLAB_BYTES : (uint32_t)(p.bns / CG * TC_BK * 2);
+        if (!__all_sync(0xffffffffu, chain_seen(ready_seq, tile_no++, wc))) { ok = false; break; }
+      }
+      // N side contiguous along N (weights' gradients, X) rather than along K.
+      const bool b_mn = MODE == SEG_CHAIN ? t.product == 2 : B_MN;
+      const bool b_two = !(MODE == SEG_CHAIN && t.n_mma <= 64 * CG);   // MN-major: two boxes of 64 columns
+      const uint32_t a_one = (uint32_t)(A_MN ? SLABS : 1) * (uint32_t)SLAB_BYTES;
+      const uint32_t b_one = (uint32_t)(b_mn ? SLABS : 1) * (b_mn && !b_two ? b_slab / 2 : b_slab);
+      const int num_kb = (t.k + TC_BK - 1) / TC_BK;
+      for (int kb = 0; kb < num_kb; kb += SLABS) {
+        const bool two = kb + 1 < num_kb;   // K-major: two slabs
+        if (!warp_wait(empty_bar(stage), phase ^ 1u, wc)) { ok = false; break; }
+        if (one) {
           const uint32_t fb = leader ? full_bar(stage) : mapa_shared(full_bar(stage), 0);
           const uint32_t sa = base + (uint32_t)(stage * STAGE_BYTES), sb = sa + (uint32_t)OPERAND_BYTES;
+          if (leader) mbar_expect_tx(full_bar(stage), (uint32_t)CG * ((A_MN || !two ? a_one : 2 * a_one) + (b_mn || !two ? b_one : 2 * b_one)));
           auto load = [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
             if constexpr (CG == 2) tma_load_3d_pair(dst, tm, x, y, z, fb);
             else tma_load_3d(dst, tm, x, y, z, fb);
           };
           const int k0 = kb * TC_BK;
           if constexpr (A_MN) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) load(sa + h * MN_BOX_BYTES, ma, m0 + h * 64, k0, za);
+            load(sa, ma, m0, k0, za);
+            load(sa + MN_BOX_BYTES, ma, m0 + 64, k0, za);
           } else {
-            for (int sl = 0; sl < nsl; ++sl) load(sa + sl * SLAB_BYTES, ma, k0 + sl * TC_BK, m0, za);
+            load(sa, ma, k0, m0, za);
+            if (two) load(sa + SLAB_BYTES, ma, k0 + TC_BK, m0, za);
           }
           if (b_mn) {
-            // (CHAIN: a tile of at most 64 columns takes one box)
-            for (int h = 0; h < (MODE == SEG_CHAIN && t.n_mma <= 64 * CG ? 1 : 2); ++h) load(sb + h * MN_BOX_BYTES, mb, n0 + h * 64, k0, zb);
+            load(sb, mb, n0, k0, zb);
+            if (b_two) load(sb + MN_BOX_BYTES, mb, n0 + 64, k0, zb);
           } else {
-            for (int sl = 0; sl < nsl; ++sl) load(sb + sl * SLAB_BYTES, mb, k0 + sl * TC_BK, n0, zb);
+            load(sb, mb, k0, n0, zb);
+            if (two) load(sb + SLAB_BYTES, mb, k0 + TC_BK, n0, zb);
           }
-          issued |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-          if (MODE == SEG_WGRAD && kb == 0 && more) acquire_maps(ahead);
         }
-        if (MODE == SEG_WGRAD && t.k == 0 && more) acquire_maps(ahead);
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (MODE == SEG_WGRAD && kb == 0 && more) acquire_maps(ahead);
       }
-      // No copy is in flight when the CTA leaves (the peer of a pair waits at the last
-      // cluster barrier: its copies complete on the leader's barriers).
-      if (leader) {
-        for (int s = 0; s < STAGES; ++s)
-          if (issued & (1u << s)) drain_wait(full_bar(s), (last_parity >> s) & 1u, p.timeout_ns);
-      } else if (!ok) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 200000ull) {
-        }
+      if (MODE == SEG_WGRAD && t.k == 0 && more) acquire_maps(ahead);
+    }
+    // No copy is in flight when the CTA leaves (the peer of a pair waits at the last
+    // cluster barrier: its copies complete on the leader's barriers).
+    if (one && leader) {
+      for (int i = max(0, issued - STAGES); i < issued; ++i)
+        drain_wait(full_bar(i % STAGES), (uint32_t)(i / STAGES) & 1u, p.timeout_ns);
+    } else if (one && !ok) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 200000ull) {
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------ MMA issuer (the leader's) -----------------------
     // The whole warp walks the list and waits; one lane issues.  A stage's eight MMAs stand

@@ -67,20 +67,21 @@ gemm_status_t repitch(Operand* x, int64_t rows, int64_t cols, int64_t batch, con
 
 // Are 4-bit weights decoded once into scratch and multiplied on the tensor-core kernel,
 // rather than inside the product, once per 32 rows?  Up to 32 rows never (one pass over
-// the weights, exact integers).  Beyond, by the times that both take: a pass inside the
-// product 0.5 ps per weight on the whole chip; decoding once 0.38, and each wave of
-// 128 x 128 tiles 0.7 us per 128 k.  Measured, inside / once, us:
+// the weights, exact integers).  Beyond, by the times that both take, in us: a pass inside
+// the product 3 and 0.4 per million weights; decoding once 0.38 per million, and each
+// wave of 128 x 128 tiles 0.45 per 128 k.  Measured, inside / once:
 //                                 33 rows        64             96             128 per expert
-//   4096 -> 11008                 45.0 / 40.5    47.0 / 40.9    68.6 / 41.5    90.4 / 43.2
-//   4096 -> 4096                  17.2 / 29.0    17.7 / 29.1    25.8 / 29.5    33.7 / 31.2
-//   11008 -> 4096                 33.7 / 70.1    34.3 / 70.2    50.4 / 70.8    66.8 / 72.6
-//   2048 -> 1408, 16 experts      43.0 / 45.3    70.4 / 46.2    97.6 / 46.6    124 / 49.7
+//   4096 -> 11008                 44.8 / 36.4    46.9 / 37.3    68.6 / 38.5    90.3 / 40.5
+//   4096 -> 4096                  17.2 / 21.6    17.8 / 22.2    25.7 / 23.4    33.6 / 25.7
+//   1024 -> 1024                  8.2 / 7.5      7.8 / 7.7      11.2 / 8.2     14.6 / 9.9
+//   11008 -> 4096                 33.5 / 54.8    34.2 / 56.5    50.3 / 59.1    66.5 / 62.5
+//   2048 -> 1408, 16 experts      42.9 / 39.8    70.4 / 41.3    97.6 / 42.3    123 / 46.7
 bool q4_decode_once(int64_t N, int64_t K, int64_t rows, int64_t groups, int sm_count) {
   if (rows <= 32 || K == 0) return false;
-  const double weights = (double)N * (double)K * (double)groups;
+  const double millions = 1e-6 * (double)N * (double)K * (double)groups;
   const int64_t tiles = (N + 127) / 128 * ((rows + 127) / 128) * groups, waves = (tiles + sm_count - 1) / sm_count;
-  const double inside = 0.5e-6 * weights * (double)((rows + 31) / 32);
-  const double once = 0.38e-6 * weights + 0.7 * (double)((K + 127) / 128) * (double)waves + 4.0;
+  const double inside = (3.0 + 0.4 * millions) * (double)((rows + 31) / 32);
+  const double once = 0.38 * millions + 0.45 * (double)((K + 127) / 128) * (double)waves + 3.0;
   return once < inside;
 }
 
@@ -117,10 +118,13 @@ gemm_status_t tokens_product(gemm_plan* plan, const Groups& groups, int64_t M, i
   SegParams p;
   std::memset(&p, 0, sizeof(p));
   p.groups = groups;
-  // CTA pairs from 128 rows per expert on.  Single CTAs / pairs: 64 experts of 256 rows
-  // (2048 to 4096) 348 / 240 us, 16 of 62 (1000 to 2048) 18.5 / 19.9, 8 of 2 (1024 to 2048)
-  // 10.3 / 10.9.
-  const int cg = plan->pair_clusters > 0 && M >= 128 * (int64_t)groups.count ? 2 : 1;
+  // CTA pairs from 128 rows per expert on, if their tiles (256 x 256) occupy three quarters
+  // of the chip.  Single CTAs / pairs, us: 64 experts of 256 rows (2048 to 4096) 348 / 240,
+  // 32 of 128 100 / 94, of 64 86.0 / 86.6; 16 of 300 (1000 to 2048) 32.0 / 26.1, of 96
+  // 18.1 / 18.3; 8 of 128 (1024 to 2048) 13.4 / 12.4; one matrix 4096 to 4096, 300 rows
+  // (32 tiles) 18.1 / 21.5.
+  const int64_t tiles256 = (N + 255) / 256 * std::max((M + 255) / 256, std::min<int64_t>(groups.count, M));
+  const int cg = M >= 128 * (int64_t)groups.count && plan->pair_clusters > 0 && 4 * tiles256 >= 3 * plan->pair_clusters ? 2 : 1;
   const int64_t tiles = ((N + 128 * cg - 1) / (128 * cg)) * (M / (128 * cg) + std::min<int64_t>(groups.count, M));
   if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
   if (K > 0) {
@@ -219,10 +223,10 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
   Operand x{A, lda, 0}, y{B, ldb, 0};
   SegParams p;
   std::memset(&p, 0, sizeof(p));
-  // CTA pairs (tiles of 256 x 256) from 128 rows per expert on, as for the forward product.
-  // Both gradients on single CTAs / pairs: 32 experts of 512 rows (4096 x 2048) 646 / 427 us,
-  // 8 of 97 (512 x 1368) 25.7 / 27.9.
-  const int cg = plan->pair_clusters > 0 && M > 128 && N > 128 && K >= 128 * groups ? 2 : 1;
+  // CTA pairs (tiles of 256 x 256) from 256 rows per expert on.  Both gradients on single
+  // CTAs / pairs, us: 32 experts of 512 rows (4096 x 2048) 646 / 427, 16 of 300 (1000 x 2048)
+  // 74.2 / 69.3, of 192 61.6 / 61.3, of 96 51.2 / 53.6; 8 of 192 (1024 x 2048) 35.4 / 41.7.
+  const int cg = plan->pair_clusters > 0 && M > 128 && N > 128 && K >= 256 * groups ? 2 : 1;
   p.tiles_m = (int32_t)((M + 128 * cg - 1) / (128 * cg));
   p.tiles_n = (int32_t)((N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = groups * p.tiles_m * (int64_t)p.tiles_n;
@@ -391,16 +395,17 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   const size_t xb = align_up((size_t)(batch * sx) * 2, 256), eb = align_up((size_t)(batch * se) * 2, 256);
   // Tiles: CTA pairs with 256 columns cost the least per product; with too few of them
   // for all pairs, narrower ones on E and F fill the chip, and small problems (whose time
-  // is the chain of tile latencies) run narrow tiles on single CTAs.  Measured, best
-  // against next: 4096 x 11008 2.16 / 2.65 ms (256 / 128 columns), 2048^2 271 / 295 us
-  // (128 / 256), 1024 x 4096 250 / 298 us (pairs, 64 / single CTAs), 1024^2 146 / 172 us
-  // and 256 x 384 88 / 113 us (single CTAs / pairs, 64).
+  // is the chain of tile latencies) run narrow tiles on single CTAs.  Measured, us, single
+  // CTAs / pairs with E and F tiles of 64 / 128 / 256 columns:
+  //   256 x 384 74 / 94 / 106 / 128;  1024^2 108 / 138 / 156 / 197;  700 x 2800 141 / 150 / 170 / 217;
+  //   1024 x 4096 193 / 179 / 204 / 270;  2048^2 282 / 249 / 223 / 274;  32 of 300 x 500
+  //   186 / 228 / 169 / 178;  16 of 768 x 2001 548 / 470 / 387 / 386;  4096 x 11008 - / - / 2650 / 2160.
   const int64_t m256 = (m + 255) / 256, sym256 = batch * m256 * (m256 + 1) / 2, dense256 = batch * m256 * ((n + 255) / 256);
   int cg = 1, bns = 64, bn = 64;   // columns of a tile of E and F, and of X
   if (plan->pair_clusters > 0 && (sym256 >= 24 || dense256 >= 48)) {
     cg = 2;
     bn = 256;
-    bns = sym256 >= plan->pair_clusters ? 256 : sym256 >= 24 ? 128 : 64;
+    bns = 2 * sym256 >= 3 * plan->pair_clusters ? 256 : sym256 >= 24 ? 128 : 64;
   }
   const int64_t bm = 128 * cg, tm = (m + bm - 1) / bm, tn = (n + bn - 1) / bn;
   const int64_t per_sym = tm * (tm + 1) / 2 * (bm / bns), per_step = batch * (2 * per_sym + tm * tn);

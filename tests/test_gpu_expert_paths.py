@@ -25,8 +25,8 @@ def _gen(seed):
 
 # Single CTAs; pairs with 64-, 128- and 256-wide tiles of the symmetric products, in one
 # block row per matrix (batches) and in several.
-@pytest.mark.parametrize("batch,m,n,cta_group", [(3, 130, 140, 1), (20, 200, 800, 2), (30, 130, 140, 2), (80, 130, 140, 2),
-                                                 (1, 600, 1500, 1), (1, 1100, 3000, 2), (1, 1700, 1801, 2), (1, 3301, 3400, 2)])
+@pytest.mark.parametrize("batch,m,n,cta_group", [(3, 130, 140, 1), (20, 200, 800, 2), (30, 130, 140, 2), (80, 130, 140, 2), (120, 130, 140, 2),
+                                                 (1, 600, 1500, 1), (1, 1100, 3000, 2), (1, 1700, 1801, 2), (1, 3301, 3400, 2), (1, 3841, 3900, 2)])
 @pytest.mark.parametrize("tall", [False, True])
 def test_orthogonalize_tiles(batch, m, n, cta_group, tall):
     g = _matrix(batch, m, n, "bf16", 11)
@@ -37,18 +37,47 @@ def test_orthogonalize_tiles(batch, m, n, cta_group, tall):
     _check(d, g, "bf16")
 
 
-@pytest.mark.parametrize("counts,cta_group", [([100, 0, 200], 1), ([500, 0, 13], 2), ([128], 2), ([127], 1)], ids=str)
-@pytest.mark.parametrize("K,N", [(200, 264), (64, 1000)])
-def test_grouped_tiles(counts, cta_group, K, N):
+@pytest.mark.parametrize("counts,K,N,cta_group", [([100, 0, 200], 200, 264, 1), ([123], 64, 20000, 1), ([300], 72, 4096, 1),
+                                                  ([500, 0, 13, 257], 200, 4101, 2), ([600], 72, 12000, 2),
+                                                  ([128, 1, 255, 128], 64, 5000, 2)], ids=str)
+@pytest.mark.parametrize("layout", ["N", "K"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_grouped_tiles(counts, K, N, cta_group, layout, dtype):
     gen = _gen(1)
     R, E = sum(counts), len(counts)
-    off = offsets_of(counts)
-    x = torch.randn((R, K), device="cuda", generator=gen).half()
-    w = torch.randn((E, K, N), device="cuda", generator=gen).half()
-    plan = G.Plan(G.GEMM_F16, G.GEMM_F32)
-    y = G.grouped_matmul(x, w, off, plan=plan)
-    assert plan.last_config()["cta_group"] == cta_group
-    check(y, *grouped_ref(x, w, off), K, "f16")
+    off = offsets_of(counts, 3)
+    x = torch.randn((R + 4, K), device="cuda", generator=gen).to(DT[dtype])
+    x[:3] = float("nan")
+    w = torch.randn((E, K, N), device="cuda", generator=gen).to(DT[dtype])
+    if layout == "K":
+        w = w.transpose(1, 2).contiguous().transpose(1, 2)
+    b = torch.randn((E, N), device="cuda", generator=gen)
+    plan = G.Plan(G.DTYPE_CODES[dtype], G.GEMM_F32)
+    y = torch.full((R + 4, N), 5.0, device="cuda", dtype=DT[dtype])
+    G.grouped_matmul(x, w, off, bias=b, relu=True, out=y, plan=plan)
+    assert plan.last_config()["cta_group"] == cta_group and plan.device_status() == 0
+    ref, mag = grouped_ref(x, w, off, b, True)
+    check(y[3:-1], ref[3:-1], mag[3:-1], K, dtype)
+    assert (y[:3] == 5).all() and (y[-1] == 5).all()
+
+
+@pytest.mark.parametrize("counts,cta_group", [([700, 3, 300], 2), ([256], 2), ([2000, 0, 0, 1], 2), ([251], 1), ([90, 0, 300], 1)],
+                         ids=str)
+@pytest.mark.parametrize("K,N", [(200, 264), (130, 1000), (129, 131)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_weight_gradient_tiles(counts, cta_group, K, N, out):
+    gen = _gen(6)
+    R, E = sum(counts), len(counts)
+    off = offsets_of(counts, 3)
+    x = torch.randn((R + 4, K), device="cuda", generator=gen).bfloat16()
+    dy = torch.randn((R + 4, N), device="cuda", generator=gen).bfloat16()
+    for t in (x, dy):
+        t[:3] = float("nan")
+        t[-1] = float("inf")
+    plan = G.Plan(G.GEMM_BF16, G.GEMM_F32)
+    dw = G.grouped_weight_grad(x, dy, off, out_dtype=DT[out], plan=plan)
+    assert plan.last_config()["cta_group"] == cta_group and plan.device_status() == 0
+    check(dw, *wgrad_ref(x, dy, off), max(counts), out)
 
 
 # Decoded inside the product in one, two and four passes, and decoded once for the

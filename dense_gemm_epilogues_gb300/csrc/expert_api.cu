@@ -119,12 +119,15 @@ gemm_status_t tokens_product(gemm_plan* plan, const Groups& groups, int64_t M, i
   std::memset(&p, 0, sizeof(p));
   p.groups = groups;
   // CTA pairs from 128 rows per expert on, if their tiles (256 x 256) occupy three quarters
-  // of the chip.  Single CTAs / pairs, us: 64 experts of 256 rows (2048 to 4096) 348 / 240,
-  // 32 of 128 100 / 94, of 64 86.0 / 86.6; 16 of 300 (1000 to 2048) 32.0 / 26.1, of 96
-  // 18.1 / 18.3; 8 of 128 (1024 to 2048) 13.4 / 12.4; one matrix 4096 to 4096, 300 rows
-  // (32 tiles) 18.1 / 21.5.
-  const int64_t tiles256 = (N + 255) / 256 * std::max((M + 255) / 256, std::min<int64_t>(groups.count, M));
-  const int cg = M >= 128 * (int64_t)groups.count && plan->pair_clusters > 0 && 4 * tiles256 >= 3 * plan->pair_clusters ? 2 : 1;
+  // of the chip or single ones need a second wave.  Single CTAs / pairs, us: 64 experts of
+  // 256 rows (2048 to 4096) 348 / 240, 32 of 128 100 / 94, of 64 86.0 / 86.6; 16 of 300 (1000
+  // to 2048) 32.0 / 26.1, of 96 18.1 / 18.3; 8 of 128 (1024 to 2048) 13.4 / 12.4; one matrix
+  // 4096 to 11008, 256 rows 36.8 / 29.2; 4096 to 4096, 300 rows 18.1 / 21.5.
+  const int64_t groups_used = std::min<int64_t>(groups.count, M);
+  const int64_t tiles256 = (N + 255) / 256 * std::max((M + 255) / 256, groups_used);
+  const int64_t tiles128 = (N + 127) / 128 * std::max((M + 127) / 128, groups_used);
+  const bool fill = 4 * tiles256 >= 3 * plan->pair_clusters || tiles128 > plan->sm_count;
+  const int cg = plan->pair_clusters > 0 && M >= 128 * (int64_t)groups.count && fill ? 2 : 1;
   const int64_t tiles = ((N + 128 * cg - 1) / (128 * cg)) * (M / (128 * cg) + std::min<int64_t>(groups.count, M));
   if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
   if (K > 0) {

@@ -42,15 +42,15 @@
 // place of three per step saves the launches' fixed cost (6-8 us each, all of a small
 // matrix's time) and lets the matrices of a batch fill each other's last waves.
 //
-// Measured (graph replays): 16384 rows over 64 experts, 2048 to 4096, bf16: 242 us, 5.3 TB/s
-// of the operands' bytes, 78 % of a copy; over 32 experts, 4096 x 2048, input and weight
-// gradient together: 431 us, 1.28 PFLOP/s, held by operand supply; 16 rows over 8 experts,
-// 1024 to 2048: 10.1 us, the latency of a launch and eight stages.  Newton-Schulz, five
-// steps: 4096 x 11008 2.16 ms with its input passes, 1.44 PFLOP/s (the symmetric products
-// counted half), at the power cap; 16 x 768 x 2001 390 us (a tile of 768 k takes 6.3 us
-// for 3.9 us of MMAs: L2 traffic); 384 x 256 90 us, 15 dependent products of 5.5 us.
-// Why three stages of two slabs, one producer: six stages of one slab 257 us for the first
-// case above, stages as small as the tile 250, a second producer thread 242.
+// Measured (graph replays): 16384 rows over 64 experts, 2048 to 4096, bf16: 222 us, 5.7 TB/s
+// of the operands' bytes, 85 % of a copy; over 32 experts, 4096 x 2048, input and weight
+// gradient together: 399 us, 1.38 PFLOP/s, held by operand supply; 16 rows over 8 experts,
+// 1024 to 2048: 9.0 us, the latency of a launch and eight stages.  Newton-Schulz, five
+// steps: 4096 x 11008 2.14 ms with its input passes, 1.45 PFLOP/s (the symmetric products
+// counted half), at the power cap; 16 x 768 x 2001 384 us (a tile of 768 k takes about 6 us
+// for 3.9 us of MMAs: L2 traffic); 384 x 256 75 us, 15 dependent products of 4.5 us.
+// Why three stages of two slabs, one producer, at the first case's 241 us of the time: six
+// stages of one slab 257, stages as small as the tile 250, a second producer thread 242.
 //
 // Every wait is bounded, as in tc_kernel.cu.
 #include "expert.h"

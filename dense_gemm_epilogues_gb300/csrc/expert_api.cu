@@ -190,7 +190,7 @@ gemm_status_t gemm_run_grouped(gemm_plan_t plan, gemm_layout_t lb, int64_t group
     const size_t xb = repitch_bytes(x, M, K, 1), wb = repitch_bytes(w, wrows, wcols, nw);
     if (xb + wb > 0) {
       s = ensure_ws(plan, xb + wb, stream);
-      char* ws = static_cast<char*>(plan->ws);
+      char* ws = static_cast<char*>(plan->ws.p);
       if (s == GEMM_OK) s = repitch(&x, M, K, 1, nullptr, ws, stream);
       if (s == GEMM_OK) s = repitch(&w, wrows, wcols, nw, nw > 1 ? offsets : nullptr, ws + xb, stream);
       if (s != GEMM_OK) return s;
@@ -241,7 +241,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
   const size_t xb = K > 0 ? repitch_bytes(x, K, M, 1) : 0, yb = K > 0 ? repitch_bytes(y, K, N, 1) : 0;
   gemm_status_t s = ensure_ws(plan, mb + xb + yb, stream);
   if (s != GEMM_OK) return s;
-  char* ws = static_cast<char*>(plan->ws);
+  char* ws = static_cast<char*>(plan->ws.p);
   CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(ws);
   if (K > 0) {
     s = repitch(&x, K, M, 1, nullptr, ws + mb, stream);
@@ -338,7 +338,7 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
     s = ensure_ws(plan, qb + xb + wb, stream);
     if (s != GEMM_OK) return s;
   }
-  char* ws = static_cast<char*>(plan->ws);
+  char* ws = static_cast<char*>(plan->ws.p);
   if (qb > 0) {   // packed weights that TMA cannot address are copied to a pitch it can
     if (launch_repitch(p.q, p.ldq, p.stride_q, ws, ldq, N * ldq, N, (K + 1) / 2, groups, offsets, 1, stream) != cudaSuccess)
       return GEMM_ERR_CUDA;
@@ -417,7 +417,7 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   const size_t sb = align_up((size_t)batch * ortho_slots(m, n) * sizeof(float), 256);
   gemm_status_t s = ensure_ws(plan, 2 * xb + 2 * eb + sb + (size_t)num_counters * sizeof(int32_t), stream);
   if (s != GEMM_OK) return s;
-  char* ws = static_cast<char*>(plan->ws);
+  char* ws = static_cast<char*>(plan->ws.p);
   __half* X[2] = {reinterpret_cast<__half*>(ws), reinterpret_cast<__half*>(ws + xb)};
   __half* E = reinterpret_cast<__half*>(ws + 2 * xb);
   __half* F = reinterpret_cast<__half*>(ws + 2 * xb + eb);

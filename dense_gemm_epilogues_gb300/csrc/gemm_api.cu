@@ -52,17 +52,67 @@ void log_config(const char* entry, int64_t M, int64_t N, int64_t K, int64_t batc
                c.xf_staged);
 }
 
-gemm_status_t ensure_ws(gemm_plan* plan, size_t bytes, cudaStream_t stream) {
-  if (plan->ws_bytes >= bytes) return GEMM_OK;
-  if (plan->ws) {
-    cudaFreeAsync(plan->ws, stream);
-    plan->ws = nullptr;
-    plan->ws_bytes = 0;
+namespace {
+// Allocations while a stream is being captured: allowed, and not part of the graph.
+struct CaptureRelaxed {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  CaptureRelaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~CaptureRelaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  CaptureRelaxed(const CaptureRelaxed&) = delete;
+  CaptureRelaxed& operator=(const CaptureRelaxed&) = delete;
+};
+
+// Device memory of zeros, at once, whatever is being captured (the zeros are written on a
+// stream of their own).
+cudaError_t malloc_zeroed(void** p, size_t bytes) {
+  CaptureRelaxed relaxed;
+  cudaStream_t s = nullptr;
+  cudaError_t e = cudaMalloc(p, bytes);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e == cudaSuccess) {
+    e = cudaMemsetAsync(*p, 0, bytes, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    cudaStreamDestroy(s);
   }
-  void* p = nullptr;
-  if (cudaMallocAsync(&p, bytes, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-  plan->ws = p;
-  plan->ws_bytes = bytes;
+  if (e != cudaSuccess) {
+    cudaFree(*p);
+    *p = nullptr;
+  }
+  return e;
+}
+}  // namespace
+
+gemm_status_t ensure_buffer(gemm_plan* plan, PlanBuffer& b, size_t bytes, bool zero,
+                            std::vector<PlanBuffer>& kept, cudaStream_t stream) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) return GEMM_ERR_CUDA;
+  const bool capturing = cs != cudaStreamCaptureStatusNone;
+  if (b.bytes < bytes) {
+    if (b.p) {
+      if (b.captured || capturing) kept.push_back(b);
+      else cudaFreeAsync(b.p, stream);
+      b = PlanBuffer{};
+    }
+    cudaError_t e;
+    void* p = nullptr;
+    if (!capturing) {
+      e = cudaMallocAsync(&p, bytes, stream);
+      if (e == cudaSuccess && zero) e = cudaMemsetAsync(p, 0, bytes, stream);
+    } else if (zero) {
+      e = malloc_zeroed(&p, bytes);
+    } else {
+      CaptureRelaxed relaxed;
+      e = cudaMalloc(&p, bytes);
+    }
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return GEMM_ERR_CUDA;
+    }
+    b.p = p;
+    b.bytes = bytes;
+  }
+  b.captured = b.captured || capturing;
   return GEMM_OK;
 }
 
@@ -588,17 +638,11 @@ gemm_status_t launch_tc_problem(gemm_plan* plan, const gemm_config_t& cfg, gemm_
     // CTA, then one arrival counter per tile.
     const size_t part_bytes = (size_t)cfg.grid * 2 * TC_BM * (size_t)bn * sizeof(float);
     const size_t need = part_bytes + (size_t)tp.num_tiles * sizeof(int32_t);
-    if (plan->sk1_ws_bytes < need) {
-      if (plan->sk1_ws) cudaFreeAsync(plan->sk1_ws, stream);
-      plan->sk1_ws = nullptr;
-      plan->sk1_ws_bytes = 0;
-      if (cudaMallocAsync(&plan->sk1_ws, need, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-      if (cudaMemsetAsync(plan->sk1_ws, 0, need, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-      plan->sk1_ws_bytes = need;
-    }
+    const gemm_status_t s = ensure_buffer(plan, plan->sk1_ws, need, true, plan->kept_counters, stream);
+    if (s != GEMM_OK) return s;
     tp.sk_first_tile = tp.num_tiles - std::min<int32_t>(cfg.sk_tiles, tp.num_tiles);
-    tp.sk_partials = static_cast<float*>(plan->sk1_ws);
-    tp.sk_flags = reinterpret_cast<int32_t*>(static_cast<char*>(plan->sk1_ws) + part_bytes);
+    tp.sk_partials = static_cast<float*>(plan->sk1_ws.p);
+    tp.sk_flags = reinterpret_cast<int32_t*>(static_cast<char*>(plan->sk1_ws.p) + part_bytes);
   }
   // K rotation for a single tile column (whole floating tiles only; GEMM_TC_KROT=0 off).
   tp.k_rotate = (tp.tiles_n == 1 && tp.tiles_m > 1 && chunk_kb == 0 && tp.sk_first_tile == tp.num_tiles) ? 1 : 0;
@@ -844,10 +888,12 @@ gemm_status_t gemm_plan_destroy(gemm_plan_t plan) {
   if (!plan) return GEMM_OK;
   DeviceGuard g(plan->device);
   cudaDeviceSynchronize();
-  if (plan->ws) cudaFree(plan->ws);
+  if (plan->ws.p) cudaFree(plan->ws.p);
   if (plan->stage) cudaFree(plan->stage);
   if (plan->sk_ws) cudaFree(plan->sk_ws);
-  if (plan->sk1_ws) cudaFree(plan->sk1_ws);
+  if (plan->sk1_ws.p) cudaFree(plan->sk1_ws.p);
+  for (const PlanBuffer& b : plan->kept) cudaFree(b.p);
+  for (const PlanBuffer& b : plan->kept_counters) cudaFree(b.p);
   if (plan->d_err) cudaFree(plan->d_err);
   if (plan->host_pipe) {
     for (cudaEvent_t e : plan->host_ev) cudaEventDestroy(e);
@@ -889,7 +935,10 @@ gemm_status_t gemm_plan_device_status(gemm_plan_t plan, gemm_stream_t stream, in
   if (cudaMemcpy(&v, plan->d_err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
   if (cudaMemset(plan->d_err, 0, sizeof(int32_t)) != cudaSuccess) return GEMM_ERR_CUDA;
   // A launch that gave up may have left stream-K arrival counters counted in.
-  if (v != 0 && plan->sk1_ws && cudaMemset(plan->sk1_ws, 0, plan->sk1_ws_bytes) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (v != 0 && plan->sk1_ws.p && cudaMemset(plan->sk1_ws.p, 0, plan->sk1_ws.bytes) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (v != 0)
+    for (const PlanBuffer& b : plan->kept_counters)
+      if (cudaMemset(b.p, 0, b.bytes) != cudaSuccess) return GEMM_ERR_CUDA;
   *code = v;
   return GEMM_OK;
 }
@@ -946,7 +995,7 @@ gemm_status_t run_impl(gemm_plan_t plan, gemm_layout_t la, gemm_layout_t lb, int
     if (s != GEMM_OK) return s;
     cudaError_t ce = cudaSuccess;
     if (cfg.xf_staged & GEMM_XF_A) {
-      uint16_t* As = static_cast<uint16_t*>(plan->ws);
+      uint16_t* As = static_cast<uint16_t*>(plan->ws.p);
       const uint16_t* Ao = static_cast<const uint16_t*>(A);
       for (int64_t z = 0; z < na && ce == cudaSuccess; ++z)
         ce = la == GEMM_OP_T ? launch_xf_stage(Ao + z * bt.sa, As + z * bt.sa, M, K, lda, xf_req, 0, stream)
@@ -954,7 +1003,7 @@ gemm_status_t run_impl(gemm_plan_t plan, gemm_layout_t la, gemm_layout_t lb, int
       A = As;
     }
     if (cfg.xf_staged & GEMM_XF_B) {
-      uint16_t* Bs = reinterpret_cast<uint16_t*>(static_cast<char*>(plan->ws) + a_bytes);
+      uint16_t* Bs = reinterpret_cast<uint16_t*>(static_cast<char*>(plan->ws.p) + a_bytes);
       const uint16_t* Bo = static_cast<const uint16_t*>(B);
       for (int64_t z = 0; z < nb && ce == cudaSuccess; ++z)
         ce = lb == GEMM_OP_N ? launch_xf_stage(Bo + z * bt.sb, Bs + z * bt.sb, N, K, ldb, xf_req, 1, stream)
@@ -986,8 +1035,8 @@ gemm_status_t run_impl(gemm_plan_t plan, gemm_layout_t la, gemm_layout_t lb, int
       const size_t a_bytes = align_up((size_t)a_el * 2, 256);
       s = ensure_ws(plan, a_bytes + (size_t)b_el * 2, stream);
       if (s != GEMM_OK) break;
-      __half* A16 = static_cast<__half*>(plan->ws);
-      __half* B16 = reinterpret_cast<__half*>(static_cast<char*>(plan->ws) + a_bytes);
+      __half* A16 = static_cast<__half*>(plan->ws.p);
+      __half* B16 = reinterpret_cast<__half*>(static_cast<char*>(plan->ws.p) + a_bytes);
       const int8_t* A8 = static_cast<const int8_t*>(A);
       const int8_t* B8 = static_cast<const int8_t*>(B);
       cudaError_t ce = cudaSuccess;
@@ -1028,7 +1077,7 @@ gemm_status_t run_impl(gemm_plan_t plan, gemm_layout_t la, gemm_layout_t lb, int
         fp.kb_per_part = (int32_t)((nkt + cfg.split_k - 1) / cfg.split_k);
         s = ensure_ws(plan, (size_t)cfg.sk_tiles * cfg.split_k * FFMA_BM * FFMA_BN * sizeof(float), stream);
         if (s != GEMM_OK) break;
-        fp.ws = static_cast<float*>(plan->ws);
+        fp.ws = static_cast<float*>(plan->ws.p);
       }
       fp.xf = xf;
       fp.epi = e;
@@ -1256,7 +1305,7 @@ gemm_status_t gemm_run_complex(gemm_plan_t plan, gemm_unit_t unit, gemm_layout_t
     const size_t b_bytes = (size_t)ldb_r * (lb == GEMM_OP_N ? 2 * N : 2 * K) * es;
     s = ensure_ws(plan, a_bytes + b_bytes, stream);
     if (s != GEMM_OK) return s;
-    char* ws = static_cast<char*>(plan->ws);
+    char* ws = static_cast<char*>(plan->ws.p);
     cudaError_t ce = cudaSuccess;
     if (stage_a) {
       ce = launch_pair_stage_a(A, lda, la == GEMM_OP_T, M, K, es, ws, lds, stream);

@@ -2,10 +2,20 @@
 #pragma once
 
 #include <cstdint>
+#include <vector>
 
 #include <nvtx3/nvToolsExt.h>
 
 #include "kernels.h"
+
+namespace gemmlib {
+// Device scratch that grows on demand (ensure_buffer).
+struct PlanBuffer {
+  void* p = nullptr;
+  size_t bytes = 0;
+  bool captured = false;   // a captured call holds its address
+};
+}  // namespace gemmlib
 
 struct gemm_plan {
   int device = 0;
@@ -13,8 +23,10 @@ struct gemm_plan {
   gemm_dtype_t c = GEMM_F32;
   int sm_count = 0;
   int32_t* d_err = nullptr;          // device error word
-  void* ws = nullptr;                // int8 staging: fp16 copies of A and B
-  size_t ws_bytes = 0;
+  gemmlib::PlanBuffer ws;            // staged operands, partial sums, the expert layers' intermediates
+  // Blocks that a larger one has replaced but captured graphs still use (of sk1_ws: apart,
+  // since a launch that gave up leaves its arrival counters other than zero).
+  std::vector<gemmlib::PlanBuffer> kept, kept_counters;
   void* stage = nullptr;             // gemm_run_host device buffers
   size_t stage_bytes = 0;
   gemm_kernel_t forced = GEMM_KERNEL_AUTO;
@@ -25,8 +37,7 @@ struct gemm_plan {
   // Stream-K of the single-CTA kernel: two fp32 partial slots per CTA, then one
   // arrival counter per tile (zero between launches; each tile's last arriver
   // resets its counter).
-  void* sk1_ws = nullptr;
-  size_t sk1_ws_bytes = 0;
+  gemmlib::PlanBuffer sk1_ws;
   gemm_config_t last{};
   uint64_t timeout_ns = 4000000000ull;
   // gemm_run_host's row-panel pipeline: copy-in and copy-out streams and the
@@ -86,8 +97,15 @@ struct DeviceGuard {
 // GEMM_LOG=1: print the configuration of a launch to stderr.
 void log_config(const char* entry, int64_t M, int64_t N, int64_t K, int64_t batch, const gemm_config_t& c);
 
-// Grow the plan's scratch (ws) to at least `bytes`, in stream order.
-gemm_status_t ensure_ws(gemm_plan* plan, size_t bytes, cudaStream_t stream);
+// Grow plan scratch to at least `bytes`, in stream order.  A captured graph keeps the
+// addresses of its calls: a block that a captured call uses is never freed before the
+// plan, and what a capture has to allocate is ordinary memory, not the graph's.
+// zero: a new block starts as zeros.
+gemm_status_t ensure_buffer(gemm_plan* plan, PlanBuffer& b, size_t bytes, bool zero,
+                            std::vector<PlanBuffer>& kept, cudaStream_t stream);
+inline gemm_status_t ensure_ws(gemm_plan* plan, size_t bytes, cudaStream_t stream) {
+  return ensure_buffer(plan, plan->ws, bytes, false, plan->kept, stream);
+}
 
 // A row-pitched tensor of 16-bit elements (inner elements contiguous, `ld`
 // elements between rows of the outer dimension) with a third, outermost

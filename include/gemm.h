@@ -217,6 +217,11 @@ gemm_status_t gemm_plan_destroy(gemm_plan_t plan);
  * split-tail partials, host staging) is
  * reused by every call: calls that use one plan from several streams or host
  * threads at once race on it; use one plan per concurrent stream.
+ * Stream capture: any call may be captured, its first use of the plan or not.  The
+ * graph holds the plan's scratch: the plan must live as long as the graph, and keeps
+ * the blocks that captured calls use until it is destroyed, also when a later call
+ * needs a larger one.  Graphs that run at the same time (or beside a call on the plan)
+ * need plans of their own, as concurrent streams do.
  * Stream-K (environment GEMM_STREAM_K=1, off by default) lets CTA pairs of one
  * launch wait for each other's partial results; it assumes the launch's CTA
  * pairs are all resident, so kernels running concurrently on other streams can
@@ -487,7 +492,7 @@ gemm_status_t gemm_noalloc_set_timeout(uint64_t timeout_ns);
  * quantize_q4) and orthogonalize of the Python package.  Operands at any alignment and
  * pitch are taken; one that TMA cannot address (a base off 16 bytes, or rows that are not
  * a multiple of 16 bytes apart) costs a copy into the plan's scratch.  As for gemm_run,
- * calls that overlap on the GPU need a plan each.
+ * calls that overlap on the GPU need a plan each, and captured calls keep their scratch.
  * gemm_plan_last_config describes the tensor-core launch; gemm_run_q4 with few rows
  * reports GEMM_KERNEL_SIMT. */
 
@@ -537,9 +542,8 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
  * Any number of rows: one token (each weight is read once) up to a prompt.
  * Up to 32 rows per expert on average every term is exact up to the fp32 sum: q - zero is
  * an integer and the scale multiplies the sum of its group.  Beyond, where that is
- * faster, each w is rounded once to A's type, into scratch of 2 bytes per weight (so such
- * a call's first use in a stream capture needs an earlier one of its size), and multiplied
- * on the tensor cores.
+ * faster, each w is rounded once to A's type, into scratch of 2 bytes per weight, and
+ * multiplied on the tensor cores.
  * With `offsets`, row r uses the weights, scales, zeros and bias of its group
  * (experts); NULL with groups == 1 is a dense layer.
  * ld_scales and ld_zeros below 2^23 (else GEMM_ERR_UNSUPPORTED).

@@ -1,0 +1,124 @@
+"""Plans of the expert-layer operators: the scratch that captured graphs keep, and
+use on other streams."""
+import pytest
+import torch
+
+import dense_gemm_epilogues_gb300 as G
+from expert_helpers import DT, offsets_of, random_q4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    G.load_library()
+
+
+def _gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def _layer(E=4, counts=(30, 70, 0, 50), K=192, N=256, seed=3):
+    gen = _gen(seed)
+    off, R = offsets_of(counts), sum(counts)
+    x = torch.randn((R, K), device="cuda", generator=gen).bfloat16()
+    dy = torch.randn((R, N), device="cuda", generator=gen).bfloat16()
+    w = torch.randn((E, K, N), device="cuda", generator=gen).bfloat16()
+    return off, x, dy, w, random_q4(N, K, 64, DT["bf16"], True, gen, E)
+
+
+def _calls(off, x, dy, w, q4, **kw):
+    """One call of each operator; kw: plan of bf16 operands, if any."""
+    q, s, z = q4
+    return [lambda: G.grouped_matmul(x, w, off, **kw), lambda: G.grouped_weight_grad(x, dy, off, **kw),
+            lambda: G.q4_matmul(x, q, s, 64, zeros=z, offsets=off, **kw), lambda: G.orthogonalize(w, **kw)]
+
+
+def _grow(plan, seed):
+    """Calls on the plan that need more scratch than _layer's, with values of their own."""
+    gen = _gen(seed)
+    x = torch.randn((300, 1024), device="cuda", generator=gen).bfloat16()
+    q, s, z = random_q4(2048, 1024, 64, DT["bf16"], True, gen)
+    G.q4_matmul(x, q, s, 64, zeros=z, plan=plan)
+    G.orthogonalize(torch.randn((1200, 2048), device="cuda", generator=gen).bfloat16(), plan=plan)
+
+
+def _odd_layer():
+    """Operands that TMA cannot address: every operator needs scratch."""
+    return _layer(K=190, N=251)
+
+
+def _layer_of(kind):
+    return {"even": _layer, "odd": _odd_layer}[kind]()
+
+
+@pytest.mark.parametrize("kind", ["even", "odd"])
+def test_graphs_survive_a_larger_call_on_their_plan(kind):
+    """The scratch of captured calls stays when the plan grows: replays after larger calls on
+    the plan, and on another one that would be given what it freed, agree with eager calls."""
+    a = _layer_of(kind)
+    plan, other = G.Plan(G.GEMM_BF16, G.GEMM_F32), G.Plan(G.GEMM_BF16, G.GEMM_F32)
+    want = [c() for c in _calls(*a, plan=plan)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [c() for c in _calls(*a, plan=plan)]
+    for turn in range(3):
+        _grow(plan, 10 + turn)
+        for c in _calls(*_layer(seed=20 + turn), plan=other):
+            c()
+        for t in got:
+            t.zero_()
+        graph.replay()
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
+    for u, v in zip([c() for c in _calls(*a, plan=plan)], want):
+        assert torch.equal(u, v)
+    assert plan.device_status() == 0 and other.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["even", "odd"])
+def test_a_plan_first_used_inside_a_capture(kind):
+    """Its scratch is ordinary memory: eager calls before the first replay may use it, and it
+    may grow within the capture."""
+    a = _layer_of(kind)
+    _grow(G.Plan(G.GEMM_BF16, G.GEMM_F32), 1)
+    want = [c() for c in _calls(*a, plan=G.Plan(G.GEMM_BF16, G.GEMM_F32))]
+    torch.cuda.synchronize()
+    plan, graph = G.Plan(G.GEMM_BF16, G.GEMM_F32), torch.cuda.CUDAGraph()
+    big = torch.randn((700, 900), device="cuda", generator=_gen(2)).bfloat16()
+    with torch.cuda.graph(graph):
+        got = [c() for c in _calls(*a, plan=plan)]
+        up = G.orthogonalize(big, plan=plan)
+    for u, v in zip([c() for c in _calls(*a, plan=plan)], want):
+        assert torch.equal(u, v)
+    for _ in range(2):
+        graph.replay()
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
+        assert torch.equal(up, G.orthogonalize(big, plan=plan))
+        _grow(plan, 3)
+    assert plan.device_status() == 0
+
+
+def test_a_kept_plan_follows_its_stream():
+    """Inputs that are written behind queued work on a side stream, with a kept plan (no call
+    in between waits for the device)."""
+    off, x, dy, w, q4 = _layer()
+    plan = G.Plan(G.GEMM_BF16, G.GEMM_F32)
+    want = [c() for c in _calls(off, x, dy, w, q4, plan=plan)]
+    x2, dy2, w2 = torch.zeros_like(x), torch.zeros_like(dy), torch.zeros_like(w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(500_000_000)
+        for to, src in ((x2, x), (dy2, dy), (w2, w)):
+            to.copy_(src)
+        got, done = [c() for c in _calls(off, x2, dy2, w2, q4, plan=plan)], torch.cuda.Event()
+        done.record()
+    assert not done.query()
+    side.synchronize()
+    for u, v in zip(got, want):
+        assert torch.equal(u, v)
+    assert plan.device_status() == 0

@@ -408,7 +408,8 @@ def matmul(a, b, *, c=None, alpha: float = 1.0, beta: float = 0.0, bias=None,
 
 # ---- expert layers (expert.py): loaded on first use, since they need torch ----
 
-_EXPERT = ("grouped_matmul", "grouped_weight_grad", "quantize_q4", "q4_matmul", "orthogonalize")
+_EXPERT = ("grouped_matmul", "grouped_weight_grad", "quantize_q4", "q4_matmul", "orthogonalize",
+           "default_plan_status")
 
 
 def __getattr__(name):

@@ -867,15 +867,14 @@ gemm_status_t gemm_plan_create(gemm_plan_t* plan, gemm_dtype_t ab, gemm_dtype_t 
   }
   DeviceGuard g(device);
   if (!g.ok) return GEMM_ERR_CUDA;
+  CaptureRelaxed relaxed;   // a plan may be made while a stream is being captured
   gemm_plan* p = new (std::nothrow) gemm_plan();
   if (!p) return GEMM_ERR_CUDA;
   p->device = device;
   p->ab = ab;
   p->c = c;
   if (cudaDeviceGetAttribute(&p->sm_count, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-      cudaMalloc(&p->d_err, sizeof(int32_t)) != cudaSuccess ||
-      cudaMemset(p->d_err, 0, sizeof(int32_t)) != cudaSuccess) {
-    if (p->d_err) cudaFree(p->d_err);
+      malloc_zeroed(reinterpret_cast<void**>(&p->d_err), sizeof(int32_t)) != cudaSuccess) {
     delete p;
     return GEMM_ERR_CUDA;
   }

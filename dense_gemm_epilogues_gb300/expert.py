@@ -4,10 +4,17 @@ gradient, products with 4-bit weights, orthogonalised updates.
 The functions check their arguments, read pointers, strides and the current
 stream and call the C entry points of include/gemm.h; a decoding step calls them
 once per layer and matrix, so they are written to take little host time.
+
+A call without `plan` uses one that is kept for its thread, stream and operand type,
+so it waits for nothing; default_plan_status() reports errors found on the device.  Such
+plans keep their scratch: a program that wants it back, that runs captured graphs at the
+same time (a capture's stream gives its graphs one plan), or that reads the status of
+single calls makes its own.  Nothing is recorded for autograd.
 """
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Optional
 
 import torch
@@ -44,15 +51,38 @@ def _device(x, *others) -> int:
     return d
 
 
-def _plan_for(plan, ab_code: int, c_code: int, device: int) -> Plan:
-    """The caller's plan, which has to be for these operands, or a new one."""
+# The plans of calls that are given none, by (thread, device, stream, operand type, c_dtype):
+# calls that can overlap never share scratch.  Kept for the life of the process.
+_DEFAULTS = {}
+
+
+def _plan_for(plan, ab_code: int, c_code: int, device: int, stream: int) -> Plan:
+    """The caller's plan, which has to be for these operands, or this stream's default one."""
     if plan is None:
-        return Plan(ab_code, c_code, device)
+        key = (threading.get_ident(), device, stream, ab_code, c_code)
+        plan = _DEFAULTS.get(key)
+        if plan is None:
+            plan = _DEFAULTS[key] = Plan(ab_code, c_code, device)
+        return plan
     if plan.ab_dtype != ab_code:
         raise GemmError(GEMM_ERR_UNSUPPORTED, "a plan of another operand type")
     if plan.device != device:
         raise ValueError("the plan is on another device")
     return plan
+
+
+def default_plan_status(device=None) -> int:
+    """What gemm_plan_device_status reports of calls that were given no plan: the first error
+    (GEMM_ERR_INVALID_ARG for bad offsets, GEMM_ERR_TIMEOUT for an expired wait) of all
+    threads and streams since the last time, or 0.  Waits for the device (the current one, or
+    `device`) and clears what it reports; not during a stream capture."""
+    index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    torch.cuda.synchronize(index)
+    code = 0
+    for key, plan in list(_DEFAULTS.items()):
+        if key[1] == index:
+            code = plan.device_status() or code
+    return code
 
 
 def _pitch(shape, stride, name: str) -> int:
@@ -115,11 +145,12 @@ def grouped_matmul(x, w, offsets, *, alpha: float = 1.0, bias=None, relu: bool =
     else:
         raise ValueError("w must have unit stride along K or N and no overlapping rows")
     out, ldd, code = _output(out, M, N, out_dtype or dtype, x)
-    plan = _plan_for(plan, _code(dtype), GEMM_F32, device)
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(dtype), GEMM_F32, device, stream)
     epi, stride_bias = _epilogue(bias, groups, N, relu, code)
     status = _LIB.gemm_run_grouped(plan.handle, lb, groups, M, N, K, alpha, x.data_ptr(), lda, w.data_ptr(), ldb,
                                    ws if groups > 1 else 0, out.data_ptr(), ldd, offsets.data_ptr(), epi, stride_bias,
-                                   _raw_stream(device) if stream is None else stream)
+                                   stream)
     if status:
         raise GemmError(status, "gemm_run_grouped")
     return out
@@ -150,7 +181,8 @@ def grouped_weight_grad(x, dy, offsets, *, alpha: float = 1.0, accumulate: bool 
     elif out.shape != (groups, M, N) or (out.stride(2) != 1 and N > 1) or (out.stride(1) < N and M > 1):
         raise ValueError("out must be [groups, K, N] with contiguous rows")
     code = _code(out.dtype)
-    plan = _plan_for(plan, _code(dtype), code, device)
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(dtype), code if accumulate else GEMM_F32, device, stream)
     if accumulate and plan.c_dtype != code:
         raise ValueError("accumulate needs a plan whose c_dtype is out's type")
     ldd = max(out.stride(1), N, 1)
@@ -160,7 +192,7 @@ def grouped_weight_grad(x, dy, offsets, *, alpha: float = 1.0, accumulate: bool 
                                          _pitch((rows, M), x.stride(), "x"), dy.data_ptr(),
                                          _pitch((rows, N), dy.stride(), "dy"), 1.0 if accumulate else 0.0,
                                          p if accumulate else None, ldd, stride_d, p, ldd, stride_d,
-                                         offsets.data_ptr(), code, _raw_stream(device) if stream is None else stream)
+                                         offsets.data_ptr(), code, stream)
     if status:
         raise GemmError(status, "gemm_run_grouped_wgrad")
     return out
@@ -220,7 +252,8 @@ def q4_matmul(x, q, scales, group_size: int, *, zeros=None, offsets=None, alpha:
             (N > 1 and (qs[-2] < shape[-1] or ss[-2] < kg or (zs is not None and zs[-2] < kg))):
         raise ValueError("q, scales and zeros need contiguous rows that do not overlap")
     out, ldd, code = _output(out, M, N, out_dtype or dtype, x)
-    plan = _plan_for(plan, _code(dtype), GEMM_F32, device)
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(dtype), GEMM_F32, device, stream)
     epi, stride_bias = _epilogue(bias, groups, N, relu, code)
     ex = groups > 1
     weights = gemm_q4_t(q.data_ptr(), max(qs[-2], shape[-1]), qs[0] if ex else 0, scales.data_ptr(),
@@ -229,7 +262,7 @@ def q4_matmul(x, q, scales, group_size: int, *, zeros=None, offsets=None, alpha:
                         zs[0] if ex and zs is not None else 0, group_size)
     status = _LIB.gemm_run_q4(plan.handle, groups, M, N, K, alpha, x.data_ptr(), _pitch((M, K), x.stride(), "x"),
                               weights, out.data_ptr(), ldd, offsets.data_ptr() if offsets is not None else None, epi,
-                              stride_bias, _raw_stream(device) if stream is None else stream)
+                              stride_bias, stream)
     if status:
         raise GemmError(status, "gemm_run_q4")
     return out
@@ -261,11 +294,12 @@ def orthogonalize(g, *, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: f
         if (t.stride(2) != 1 and n > 1) or (m > 1 and t.stride(1) < n):
             raise ValueError(f"{name} must have contiguous rows (or columns) like the other")
     ldd = max(ov.stride(1), n, 1)
-    plan = _plan_for(plan, _code(g.dtype), GEMM_F32, device)
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(g.dtype), GEMM_F32, device, stream)
     status = _LIB.gemm_orthogonalize(plan.handle, batch, m, n, steps, (ctypes.c_double * 3)(*coeffs), eps,
                                      gv.data_ptr(), max(gv.stride(1), n, 1), gv.stride(0) if batch > 1 else 0,
                                      ov.data_ptr(), ldd, ov.stride(0) if batch > 1 else m * ldd, _code(out.dtype),
-                                     _raw_stream(device) if stream is None else stream)
+                                     stream)
     if status:
         raise GemmError(status, "gemm_orthogonalize")
     return out

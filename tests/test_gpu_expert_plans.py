@@ -1,5 +1,7 @@
-"""Plans of the expert-layer operators: the scratch that captured graphs keep, and
-use on other streams."""
+"""Plans of the expert-layer operators: the scratch that captured graphs keep, use on
+other streams, and calls without a plan."""
+import threading
+
 import pytest
 import torch
 
@@ -122,3 +124,89 @@ def test_a_kept_plan_follows_its_stream():
     for u, v in zip(got, want):
         assert torch.equal(u, v)
     assert plan.device_status() == 0
+
+
+def test_calls_without_a_plan_do_not_wait_for_the_device():
+    """Work queued ahead on the stream is still running when such a call returns."""
+    for call in _calls(*_layer()):
+        want = call()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(1_000_000_000)
+        got, done = call(), torch.cuda.Event()
+        done.record()
+        assert not done.query()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+def test_calls_without_a_plan_report_their_errors():
+    off, x, dy, w, q4 = _layer()
+    assert G.default_plan_status() == 0
+    bad = torch.tensor([0, 30, 20, 100, 150], dtype=torch.int32, device="cuda")
+    for call in _calls(bad, x, dy, w, q4)[:3]:
+        call()
+        assert G.default_plan_status() == G.GEMM_ERR_INVALID_ARG
+        assert G.default_plan_status() == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        G.grouped_matmul(x, w, bad)
+    assert G.default_plan_status() == G.GEMM_ERR_INVALID_ARG
+
+
+def test_calls_without_a_plan_on_several_streams_and_threads():
+    """Every stream and thread has scratch of its own: calls that run together agree with
+    calls one after the other."""
+    layers = [_layer(seed=s) for s in range(4)]
+    want = [[c() for c in _calls(*a)] for a in layers]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got[i] = [c() for c in _calls(*layers[i])]
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(want, got):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
+    assert G.default_plan_status() == 0
+
+
+def test_calls_without_a_plan_inside_a_capture():
+    """The first such call of a stream, too: its plan is made during the capture."""
+    a = _layer()
+    want = [c() for c in _calls(*a)]
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        got = [c() for c in _calls(*a)]
+    for _ in range(2):
+        graph.replay()
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
+    with torch.cuda.stream(side):
+        again = [c() for c in _calls(*a)]
+    torch.cuda.synchronize()
+    for u, v in zip(again, want):
+        assert torch.equal(u, v)
+    assert G.default_plan_status() == 0
+
+
+def test_calls_without_a_plan_keep_one():
+    from dense_gemm_epilogues_gb300 import expert
+    a = _layer()
+    for c in _calls(*a):
+        c()
+    made = len(expert._DEFAULTS)
+    for c in _calls(*a):
+        c()
+    G.grouped_weight_grad(a[1], a[2], a[0], out_dtype=DT["f32"])
+    assert len(expert._DEFAULTS) == made

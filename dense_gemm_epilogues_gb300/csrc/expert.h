@@ -61,6 +61,13 @@ __device__ __forceinline__ void with_type(int dtype, F&& f) {
   else f(TypeTag<GEMM_BF16>{});
 }
 
+// ReLU that keeps NaN (fmaxf would make it 0 and hide it from the layers that follow).
+__device__ __forceinline__ float relu_keep_nan(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Order this thread's use of a tensor map after its making by another kernel.
 __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* tm) {
   asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(tm) : "memory");

@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(32 * WARPS, Q4Cfg<MT, NT>::CTAS) q4_kernel(con
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) v += red[(w * 8 * NT + tok) * Cfg::PITCH + row];
         v = fmaf(v, p.epi.alpha, b);
-        if (p.epi.relu) v = fmaxf(v, 0.0f);
+        if (p.epi.relu) v = relu_keep_nan(v);
         store_float_as(p.epi.D, p.epi.d_dtype, (int64_t)(tok0 + tok) * p.epi.ldd + n0 + row, v);
       }
     }

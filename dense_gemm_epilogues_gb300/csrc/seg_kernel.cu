@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               x[j] += bias;
-              if (p.epi.relu) x[j] = fmaxf(x[j], 0.0f);
+              if (p.epi.relu) x[j] = relu_keep_nan(x[j]);
             }
             store_chunk_t<decltype(dt)::value>(p.epi.D, p.epi.ldd, (int64_t)t.n0 + c * 32, m, t.n_valid - c * 32, m_left,
                                                x, turn, p.epi.vec_d);

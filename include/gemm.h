@@ -510,6 +510,7 @@ gemm_status_t gemm_noalloc_set_timeout(uint64_t timeout_ns);
  *   epi         bias: N entries per group (GEMM_BIAS_COL; group g's at
  *               g * stride_bias elements), act, out_dtype.  NULL: none, out_dtype
  *               c_dtype.  GEMM_BIAS_ROW and load_xf are GEMM_ERR_UNSUPPORTED.
+ *               The ReLU of the expert-layer operators keeps NaN.
  * K == 0 gives D = act(bias).  D must not overlap A.
  * ------------------------------------------------------------------------- */
 gemm_status_t gemm_run_grouped(gemm_plan_t plan, gemm_layout_t layoutB, int64_t groups, int64_t M, int64_t N,

@@ -96,12 +96,17 @@ struct SegParams {
   // each), tiles_m x tiles_n of X (bn columns each) per matrix; num_tiles over all steps.
   int32_t batch, steps, bns, bn;
   int32_t store_t;              // the result (epi.D) is stored transposed
+  // Matrices as pairs of fp16 halves (the second one is what the first rounds away): X
+  // always for a X; with `pairs`, X, E and F in the products too, as the sum of three,
+  // hi hi + hi lo + lo hi (the second halves then lie `batch` slices behind the first).
+  int32_t pairs;
   int32_t* counters;            // 3 * steps * batch * tiles_m, zero at the start
   struct {
     __half *x[2], *e, *f;       // step s reads x[s % 2]
+    __half* xlo[2];             // second halves of X (without `pairs` one buffer: read in place)
     int64_t ldx, stride_x, lde, stride_e;
     float a[2], b[2], c;        // early steps, the last two (see gemm_orthogonalize)
-    float inv_scale;            // X is held times 1 / inv_scale
+    float inv_x, scale_e, inv_e;   // X is held times 1 / inv_x, E and F times scale_e = 1 / inv_e
   } chain;
   EpiParams epi;
   int32_t* err;
@@ -158,13 +163,14 @@ struct OrthoInput {
   int32_t vec;              // G's rows can be read 16 bytes at a time
 };
 int ortho_slots(int64_t m, int64_t n);   // partial sums per matrix
-// X = G / (||G|| + eps) times `scale`, in fp16; partials: batch * ortho_slots(m, n) floats.
+// X = G / (||G|| + eps) times `scale`, as pairs of fp16 halves x + xlo; partials: batch *
+// ortho_slots(m, n) floats.
 // counters[0 .. num_counters) are set to zero.
 cudaError_t launch_ortho_input(const OrthoInput& in, int dtype, int64_t batch, float* partials, float eps, float scale,
-                               __half* x, int64_t ldx, int64_t stride_x, int32_t* counters, int64_t num_counters,
-                               cudaStream_t stream);
-// D (M x N) = scale * X (or its transpose), cast.
-cudaError_t launch_unscale(const __half* x, int64_t batch, int64_t M, int64_t N, int64_t ldx, int64_t stride_x,
+                               __half* x, __half* xlo, int64_t ldx, int64_t stride_x, int32_t* counters,
+                               int64_t num_counters, cudaStream_t stream);
+// D (M x N) = scale * (x + xlo) (or its transpose), cast.
+cudaError_t launch_unscale(const __half* x, const __half* xlo, int64_t batch, int64_t M, int64_t N, int64_t ldx, int64_t stride_x,
                            int transpose, float scale, void* D, int dtype, int64_t ldd, int64_t stride_d,
                            cudaStream_t stream);
 

@@ -395,7 +395,6 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   const int64_t m = tall ? N : M, n = tall ? M : N;
   const int64_t ldx = (n + 15) / 16 * 16, lde = (m + 15) / 16 * 16;   // rows on 32 bytes
   const int64_t sx = m * ldx, se = m * lde;
-  const size_t xb = align_up((size_t)(batch * sx) * 2, 256), eb = align_up((size_t)(batch * se) * 2, 256);
   // Tiles: CTA pairs with 256 columns cost the least per product; with too few of them
   // for all pairs, narrower ones on E and F fill the chip, and small problems (whose time
   // is the chain of tile latencies) run narrow tiles on single CTAs.  Measured, us, single
@@ -415,38 +414,50 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   if (per_step > kMaxTiles / std::max(1, steps)) return GEMM_ERR_UNSUPPORTED;
   const int64_t num_counters = 3 * (int64_t)steps * batch * tm;
   const size_t sb = align_up((size_t)batch * ortho_slots(m, n) * sizeof(float), 256);
-  gemm_status_t s = ensure_ws(plan, 2 * xb + 2 * eb + sb + (size_t)num_counters * sizeof(int32_t), stream);
+  // X is held as a pair of fp16 halves for a X, and X, E and F as one half each in the
+  // products: that leaves 0.7 to 1.4e-3 of the result's norm for a full-rank matrix and up to
+  // 3.1e-3 for one of low rank, beside the 1.7e-3 of a rounding to bf16.  A finer result
+  // takes products of pairs, three for one, whose error is that of fp32 arithmetic.
+  const bool pairs = out_dtype != GEMM_BF16;
+  const int64_t halves = pairs ? 2 : 1;   // second halves behind the first ones, as further slices
+  const size_t xs = align_up((size_t)(halves * batch * sx) * 2, 256), es_b = align_up((size_t)(halves * batch * se) * 2, 256);
+  const size_t ls = pairs ? 0 : xs;   // without pairs one buffer of second halves: a tile reads and writes only its own part
+  gemm_status_t s = ensure_ws(plan, 2 * xs + ls + 2 * es_b + sb + (size_t)num_counters * sizeof(int32_t), stream);
   if (s != GEMM_OK) return s;
   char* ws = static_cast<char*>(plan->ws.p);
-  __half* X[2] = {reinterpret_cast<__half*>(ws), reinterpret_cast<__half*>(ws + xb)};
-  __half* E = reinterpret_cast<__half*>(ws + 2 * xb);
-  __half* F = reinterpret_cast<__half*>(ws + 2 * xb + eb);
-  float* sums = reinterpret_cast<float*>(ws + 2 * xb + 2 * eb);
-  int32_t* counters = reinterpret_cast<int32_t*>(ws + 2 * xb + 2 * eb + sb);
-  // fp16 keeps 11 bits; entries of X are at most ~1 and as small as 1 / sqrt(m n), so
-  // they are held times 256, which keeps the small ones out of fp16's subnormals.
-  const float scale = 256.0f;
+  __half* X[2] = {reinterpret_cast<__half*>(ws), reinterpret_cast<__half*>(ws + xs)};
+  __half* one_lo = reinterpret_cast<__half*>(ws + 2 * xs);
+  __half* Xlo[2] = {pairs ? X[0] + batch * sx : one_lo, pairs ? X[1] + batch * sx : one_lo};
+  __half* E = reinterpret_cast<__half*>(ws + 2 * xs + ls);
+  __half* F = reinterpret_cast<__half*>(ws + 2 * xs + ls + es_b);
+  float* sums = reinterpret_cast<float*>(ws + 2 * xs + ls + 2 * es_b);
+  int32_t* counters = reinterpret_cast<int32_t*>(ws + 2 * xs + ls + 2 * es_b + sb);
+  // Entries of X are at most ~1 and as small as 1 / sqrt(m n), so they are held times 1024,
+  // which keeps the second halves' units (2^-24) below 2^-20 of an entry up to m n = 2^26.
+  // In pairs E and F are held times 256 for the same reason (entries of 1 / m).
+  const float scale = 1024.0f, scale_e = pairs ? 256.0f : 1.0f;
   const int es = dtype_bytes(plan->ab);
   const OrthoInput in{G, m, n, ldg, stride_g, tall ? 1 : 0,
                       aligned16(G) && (ldg * es) % 16 == 0 && (batch == 1 || (stride_g * es) % 16 == 0) ? 1 : 0};
-  if (launch_ortho_input(in, plan->ab, batch, sums, (float)eps, scale, X[0], ldx, sx, counters, num_counters, stream) !=
-      cudaSuccess)
+  if (launch_ortho_input(in, plan->ab, batch, sums, (float)eps, scale, X[0], Xlo[0], ldx, sx, counters, num_counters,
+                         stream) != cudaSuccess)
     return GEMM_ERR_CUDA;
   if (steps == 0)
-    return launch_unscale(X[0], batch, M, N, ldx, sx, tall, 1.0f / scale, D, out_dtype, ldd, stride_d, stream) ==
+    return launch_unscale(X[0], Xlo[0], batch, M, N, ldx, sx, tall, 1.0f / scale, D, out_dtype, ldd, stride_d, stream) ==
                    cudaSuccess
                ? GEMM_OK
                : GEMM_ERR_CUDA;
   SegParams p;
   std::memset(&p, 0, sizeof(p));
   const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  bool ok = encode_3d(&p.tmA, dt, E, m, m, lde, batch, se, TC_BK, 128) &&
-            encode_3d(&p.tmB[CHAIN_F], dt, F, m, m, lde, batch, se, TC_BK, 128);
-  ok = ok && encode_3d(&p.tmB[CHAIN_EB], dt, E, m, m, lde, batch, se, TC_BK, (uint32_t)(bns / cg));
+  const int64_t slices = halves * batch;
+  bool ok = encode_3d(&p.tmA, dt, E, m, m, lde, slices, se, TC_BK, 128) &&
+            encode_3d(&p.tmB[CHAIN_F], dt, F, m, m, lde, slices, se, TC_BK, 128);
+  ok = ok && encode_3d(&p.tmB[CHAIN_EB], dt, E, m, m, lde, slices, se, TC_BK, (uint32_t)(bns / cg));
   for (int i = 0; i < 2; ++i)
-    ok = ok && encode_3d(&p.tmB[CHAIN_XK + i], dt, X[i], n, m, ldx, batch, sx, TC_BK, 128) &&
-         encode_3d(&p.tmB[CHAIN_XB + i], dt, X[i], n, m, ldx, batch, sx, TC_BK, (uint32_t)(bns / cg)) &&
-         encode_3d(&p.tmB[CHAIN_XN + i], dt, X[i], n, m, ldx, batch, sx, 64, 2 * TC_BK);
+    ok = ok && encode_3d(&p.tmB[CHAIN_XK + i], dt, X[i], n, m, ldx, slices, sx, TC_BK, 128) &&
+         encode_3d(&p.tmB[CHAIN_XB + i], dt, X[i], n, m, ldx, slices, sx, TC_BK, (uint32_t)(bns / cg)) &&
+         encode_3d(&p.tmB[CHAIN_XN + i], dt, X[i], n, m, ldx, slices, sx, 64, 2 * TC_BK);
   if (!ok) return GEMM_ERR_CUDA;
   p.M = m;
   p.N = (int32_t)n;
@@ -461,7 +472,11 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   p.bn = bn;
   p.store_t = tall ? 1 : 0;
   p.counters = counters;
-  for (int i = 0; i < 2; ++i) p.chain.x[i] = X[i];
+  p.pairs = pairs ? 1 : 0;
+  for (int i = 0; i < 2; ++i) {
+    p.chain.x[i] = X[i];
+    p.chain.xlo[i] = Xlo[i];
+  }
   p.chain.e = E;
   p.chain.f = F;
   p.chain.ldx = ldx;
@@ -476,7 +491,9 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
     p.chain.b[h] = (float)(coeffs[1] + 2 * coeffs[2] * h);
   }
   p.chain.c = (float)coeffs[2];
-  p.chain.inv_scale = 1.0f / scale;
+  p.chain.inv_x = 1.0f / scale;
+  p.chain.scale_e = scale_e;
+  p.chain.inv_e = 1.0f / scale_e;
   p.epi = epilogue_of(nullptr, out_dtype, 1.0, D, ldd);
   if (batch > 1 && (stride_d * dtype_bytes(out_dtype)) % 16 != 0) p.epi.vec_d = 0;
   p.epi.stride_d = stride_d;

@@ -1,6 +1,6 @@
 // ortho_kernels.cu -- what the Newton-Schulz steps need around their products: the
-// norm of each matrix, the normalised fp16 copy that the products read, and the
-// cast of a result that no product writes itself.
+// norm of each matrix, the normalised copy that the products read (pairs of fp16 halves),
+// and the cast of a result that no product writes itself.
 #include "expert.h"
 
 namespace gemmlib {
@@ -171,10 +171,11 @@ __global__ void __launch_bounds__(256) sumsq_kernel(const OrthoInput in, float* 
   if (threadIdx.x == 0) partials[blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
-// X = G * (scale / (norm + eps)) in fp16, rows pitched to ldx with zeros past n.
+// X = G * (scale / (norm + eps)) as x + xlo, both fp16, xlo what x rounds away; rows
+// pitched to ldx with zeros past n.
 template <typename T>
 __global__ void __launch_bounds__(256) normalize_kernel(const OrthoInput in, const float* partials, int slots,
-                                                        float eps, float scale, __half* x, int64_t ldx,
+                                                        float eps, float scale, __half* x, __half* xlo, int64_t ldx,
                                                         int64_t stride_x) {
   __shared__ float tile[TILE][TILE + 1];
   pdl_wait();
@@ -186,12 +187,19 @@ __global__ void __launch_bounds__(256) normalize_kernel(const OrthoInput in, con
   for (int i = threadIdx.x; i < slots; i += 256) s += partials[blockIdx.y * slots + i];
   const float f = scale / (sqrtf(block_sum(s)) + eps);
   x += blockIdx.y * stride_x;
+  xlo += blockIdx.y * stride_x;
   auto store = [&](int64_t r, int64_t c, const float (&e)[8]) {
     if (r >= in.m || c >= ldx) return;
-    __half2 h[4];
+    __align__(16) __half2 h[4], l[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = __floats2half2_rn(e[2 * k] * f, e[2 * k + 1] * f);
+    for (int k = 0; k < 4; ++k) {
+      const float v0 = __fmul_rn(e[2 * k], f), v1 = __fmul_rn(e[2 * k + 1], f);
+      h[k] = __floats2half2_rn(v0, v1);
+      const float2 w = __half22float2(h[k]);
+      l[k] = __floats2half2_rn(v0 - w.x, v1 - w.y);
+    }
     *reinterpret_cast<uint4*>(x + r * ldx + c) = *reinterpret_cast<uint4*>(h);
+    *reinterpret_cast<uint4*>(xlo + r * ldx + c) = *reinterpret_cast<uint4*>(l);
   };
   float e[2][8];
   for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -216,20 +224,22 @@ __global__ void __launch_bounds__(256) normalize_kernel(const OrthoInput in, con
   }
 }
 
-__global__ void __launch_bounds__(256) unscale_kernel(const __half* x, int64_t M, int64_t N, int64_t ldx,
+__global__ void __launch_bounds__(256) unscale_kernel(const __half* x, const __half* xlo, int64_t M, int64_t N, int64_t ldx,
                                                       int64_t stride_x, int transpose, float scale, void* D, int dtype,
                                                       int64_t ldd, int64_t stride_d) {
   x += blockIdx.y * stride_x;
+  xlo += blockIdx.y * stride_x;
   char* d = static_cast<char*>(D) + blockIdx.y * stride_d * dtype_bytes(dtype);
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < M * N; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t r = i / N, c = i % N;
-    store_float_as(d, dtype, r * ldd + c, __half2float(x[transpose ? c * ldx + r : r * ldx + c]) * scale);
+    const int64_t at = transpose ? c * ldx + r : r * ldx + c;
+    store_float_as(d, dtype, r * ldd + c, (__half2float(x[at]) + __half2float(xlo[at])) * scale);
   }
 }
 
 template <typename T>
 cudaError_t launch_ortho_input(const OrthoInput& in, int64_t batch, float* partials, float eps, float scale, __half* x,
-                               int64_t ldx, int64_t stride_x, int32_t* counters, int64_t num_counters,
+                               __half* xlo, int64_t ldx, int64_t stride_x, int32_t* counters, int64_t num_counters,
                                cudaStream_t stream) {
   const int64_t tiles = ((in.m + TILE - 1) / TILE) * ((ldx + TILE - 1) / TILE);
   const int slots = ortho_slots(in.m, in.n);
@@ -237,7 +247,7 @@ cudaError_t launch_ortho_input(const OrthoInput& in, int64_t batch, float* parti
                                    counters, num_counters);
   if (e != cudaSuccess) return e;
   return launch_dependent(normalize_kernel<T>, dim3((unsigned)std::min<int64_t>(tiles, std::max<int64_t>(1216 / batch, 76)), (unsigned)batch), 256, stream,
-                          in, (const float*)partials, slots, eps, scale, x, ldx, stride_x);
+                          in, (const float*)partials, slots, eps, scale, x, xlo, ldx, stride_x);
 }
 
 }  // namespace
@@ -249,19 +259,19 @@ int ortho_slots(int64_t m, int64_t n) {
 }
 
 cudaError_t launch_ortho_input(const OrthoInput& in, int dtype, int64_t batch, float* partials, float eps, float scale,
-                               __half* x, int64_t ldx, int64_t stride_x, int32_t* counters, int64_t num_counters,
-                               cudaStream_t stream) {
-  if (dtype == GEMM_F32) return launch_ortho_input<float>(in, batch, partials, eps, scale, x, ldx, stride_x, counters, num_counters, stream);
-  if (dtype == GEMM_F16) return launch_ortho_input<__half>(in, batch, partials, eps, scale, x, ldx, stride_x, counters, num_counters, stream);
-  return launch_ortho_input<__nv_bfloat16>(in, batch, partials, eps, scale, x, ldx, stride_x, counters, num_counters, stream);
+                               __half* x, __half* xlo, int64_t ldx, int64_t stride_x, int32_t* counters,
+                               int64_t num_counters, cudaStream_t stream) {
+  if (dtype == GEMM_F32) return launch_ortho_input<float>(in, batch, partials, eps, scale, x, xlo, ldx, stride_x, counters, num_counters, stream);
+  if (dtype == GEMM_F16) return launch_ortho_input<__half>(in, batch, partials, eps, scale, x, xlo, ldx, stride_x, counters, num_counters, stream);
+  return launch_ortho_input<__nv_bfloat16>(in, batch, partials, eps, scale, x, xlo, ldx, stride_x, counters, num_counters, stream);
 }
 
-cudaError_t launch_unscale(const __half* x, int64_t batch, int64_t M, int64_t N, int64_t ldx, int64_t stride_x,
+cudaError_t launch_unscale(const __half* x, const __half* xlo, int64_t batch, int64_t M, int64_t N, int64_t ldx, int64_t stride_x,
                            int transpose, float scale, void* D, int dtype, int64_t ldd, int64_t stride_d,
                            cudaStream_t stream) {
   const int64_t per = (M * N + 255) / 256;
   unscale_kernel<<<dim3((unsigned)std::min<int64_t>(per, 2048), (unsigned)batch), 256, 0, stream>>>(
-      x, M, N, ldx, stride_x, transpose, scale, D, dtype, ldd, stride_d);
+      x, xlo, M, N, ldx, stride_x, transpose, scale, D, dtype, ldd, stride_d);
   return cudaGetLastError();
 }
 

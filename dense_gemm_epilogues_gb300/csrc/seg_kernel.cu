@@ -4,7 +4,8 @@
 //   WGRAD   D_g = alpha * A_g' * B_g + beta * C_g, the sum over the rows of group g;
 //   CHAIN   the products of the Newton-Schulz steps, all of them in one launch:
 //           E = X X' - h I,  F = c E E' + b E,  X <- F X + a X  for every matrix of a batch
-//           (in the last two steps F = c E E' + b E + a I,  X <- F X).
+//           (in the last two steps F = c E E' + b E + a I,  X <- F X), X as a pair of fp16
+//           halves, E and F as one half or, for results finer than bf16, as pairs too.
 //
 // One structure serves them all, on single CTAs (CG = 1, tiles of 128 x 128) and on
 // CTA pairs (CG = 2, 256 x 256): a producer thread streams 64-deep slabs of both
@@ -667,13 +668,20 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
         b_slab = t.product == 2 ? (uint32_t)SLAB_BYTES : (uint32_t)(p.bns / CG * TC_BK * 2);
         if (!__all_sync(0xffffffffu, chain_seen(ready_seq, tile_no++, wc))) { ok = false; break; }
       }
+      // CHAIN with pairs: three products into one accumulator, hi hi, hi lo, lo hi.
+      const int parts = MODE == SEG_CHAIN && p.pairs ? 3 : 1;
       // N side contiguous along N (weights' gradients, X) rather than along K.
       const bool b_mn = MODE == SEG_CHAIN ? t.product == 2 : B_MN;
       const bool b_two = !(MODE == SEG_CHAIN && t.n_mma <= 64 * CG);   // MN-major: two boxes of 64 columns
       const uint32_t a_one = (uint32_t)(A_MN ? SLABS : 1) * (uint32_t)SLAB_BYTES;
       const uint32_t b_one = (uint32_t)(b_mn ? SLABS : 1) * (b_mn && !b_two ? b_slab / 2 : b_slab);
       const int num_kb = (t.k + TC_BK - 1) / TC_BK;
-      for (int kb = 0; kb < num_kb; kb += SLABS) {
+      for (int part = 0, kb = 0; part < parts; kb + SLABS < num_kb ? kb += SLABS : (kb = 0, ++part)) {
+        if (num_kb == 0) break;
+        if constexpr (MODE == SEG_CHAIN) {
+          za = t.e + (part == 2 ? p.batch : 0);
+          zb = t.e + (part == 1 ? p.batch : 0);
+        }
         const bool two = kb + 1 < num_kb;   // K-major: two slabs
         if (!warp_wait(empty_bar(stage), phase ^ 1u, wc)) { ok = false; break; }
         if (one) {
@@ -740,7 +748,8 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
         const uint32_t idesc = p.idesc | ((uint32_t)(t.n_mma >> 3) << 17) |
                                ((MODE == SEG_CHAIN && b_mn ? 1u : 0u) << 16);   // bit 16: N side MN-major
         const int num_kb = (t.k + TC_BK - 1) / TC_BK, num_k16 = (t.k + 15) / 16;
-        for (int kb = 0; kb < num_kb; kb += SLABS) {
+        const int parts = MODE == SEG_CHAIN && p.pairs ? 3 : 1;
+        for (int part = 0, kb = 0; part < parts; kb + SLABS < num_kb ? kb += SLABS : (kb = 0, ++part)) {
           if (!warp_wait(full_bar(stage), phase, wc)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sa = base + (uint32_t)(stage * STAGE_BYTES), sb = sa + (uint32_t)OPERAND_BYTES;
@@ -752,7 +761,7 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
               // Steps of 16 k: 2048 bytes of an MN-major operand; 32 bytes of a K-major slab's rows.
               const uint32_t km = (uint32_t)(q / (TC_BK / 16) * SLAB_BYTES + q % (TC_BK / 16) * 32) >> 4;
               const uint32_t mm = (uint32_t)q * 2048u >> 4;
-              const uint32_t acc = q > 0 || kb > 0 ? 1u : 0u;
+              const uint32_t acc = q > 0 || kb > 0 || part > 0 ? 1u : 0u;
               if constexpr (CG == 2) tc_mma_f16_pair(d_tmem, ad + (A_MN ? mm : km), bd + (MN ? mm : km), idesc, acc);
               else tc_mma_f16(d_tmem, ad + (A_MN ? mm : km), bd + (MN ? mm : km), idesc, acc);
             };
@@ -838,58 +847,74 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
       float shift = 0.0f;
       bool store_n = true, store_t = false;   // as it is, transposed
       bool scratch_d = MODE == SEG_CHAIN;     // D is scratch
+      const __half* c_lo = nullptr;           // CHAIN: second halves of C and D, if any
+      __half* d_lo = nullptr;
       auto ext = [](int cols) { return MODE == SEG_CHAIN ? min(32, (cols + 7) & ~7) : cols; };
       if constexpr (MODE == SEG_CHAIN) {
         const bool late = t.step >= p.steps - 2, last = t.step == p.steps - 1;
-        __half* Y = p.chain.x[(t.step + 1) & 1];
+        const int64_t second = (int64_t)p.batch * p.chain.stride_e, at_e = t.e * p.chain.stride_e;
+        const int64_t at_x = t.e * p.chain.stride_x;
         ep.ldc = p.chain.lde;
         ep.ldd = p.chain.lde;
         ep.d_dtype = GEMM_F16;
         ep.vec_d = 1;
-        ptr.C = p.chain.e + t.e * p.chain.stride_e;
+        ptr.C = p.chain.e + at_e;
         if (t.product == 0) {
-          ep.alpha = p.chain.inv_scale * p.chain.inv_scale;
+          ep.alpha = p.chain.inv_x * p.chain.inv_x * p.chain.scale_e;
           ep.read_c = 0;
-          shift = late ? 1.0f : 0.0f;
-          ptr.D = p.chain.e + t.e * p.chain.stride_e;
+          shift = late ? p.chain.scale_e : 0.0f;
+          ptr.D = p.chain.e + at_e;
+          if (p.pairs) d_lo = p.chain.e + at_e + second;
           store_t = t.n0 < t.m0;
         } else if (t.product == 1) {
-          ep.alpha = p.chain.c;
+          ep.alpha = p.chain.c * p.chain.inv_e;
           ep.beta = late ? p.chain.b[1] : p.chain.b[0];
-          shift = late ? -p.chain.a[1] : 0.0f;
-          ptr.D = p.chain.f + t.e * p.chain.stride_e;
+          shift = late ? -p.chain.a[1] * p.chain.scale_e : 0.0f;
+          ptr.D = p.chain.f + at_e;
+          if (p.pairs) {
+            c_lo = p.chain.e + at_e + second;
+            d_lo = p.chain.f + at_e + second;
+          }
           store_t = t.n0 < t.m0;
         } else {
-          ep.alpha = last ? p.chain.inv_scale : 1.0f;
-          // a X: in the last two steps by F's diagonal, which holds a (X is then not read
-          // again: 13 per cent of these tiles' L2 traffic).  Earlier the rounding of a sum
-          // near 3.4 to fp16 would grow with the small singular values (272 x 5632: relative
-          // error of the result 2.6e-3 instead of 2.1e-3).
+          ep.alpha = p.chain.inv_e * (last ? p.chain.inv_x : 1.0f);
+          // a X: early from both halves of X.  A direction that G lacks is in no other term, and
+          // what is rounded there grows by a in every later step (a single fp16 X leaves 15 per
+          // cent of the result's norm for a matrix of rank 1, the pair 0.3).  In the last two
+          // steps it comes by F's diagonal, which holds a, and X is not read again (a fifth of the
+          // L2 traffic of tiles 768 deep); from the start the rounding of a sum near 3.4 to fp16
+          // would grow with the small singular values (272 x 5632: relative error of the
+          // result 2.6e-3 instead of 2.2e-3).
           if (late) {
             ep.read_c = 0;
           } else {
-            ep.beta = p.chain.a[0] * ep.alpha;
-            ptr.C = p.chain.x[t.step & 1] + t.e * p.chain.stride_x;
+            ep.beta = p.chain.a[0];
+            ptr.C = p.chain.x[t.step & 1] + at_x;
+            c_lo = p.chain.xlo[t.step & 1] + at_x;
             ep.ldc = p.chain.ldx;
           }
           ep.ldd = p.chain.ldx;
-          ptr.D = Y + t.e * p.chain.stride_x;
+          ptr.D = p.chain.x[(t.step + 1) & 1] + at_x;
+          if (p.pairs || t.step + 3 < p.steps) d_lo = p.chain.xlo[(t.step + 1) & 1] + at_x;
           if (last) {
             ep.ldd = p.epi.ldd;
             ep.d_dtype = p.epi.d_dtype;
             ep.vec_d = p.epi.vec_d;
             ptr.D = static_cast<char*>(p.epi.D) + t.e * p.epi.stride_d * dtype_bytes(p.epi.d_dtype);
+            d_lo = nullptr;
             store_t = p.store_t != 0;
             store_n = !store_t;
             scratch_d = false;
           }
         }
       }
-      CChunk cc;
-      cc.held = false;
+      CChunk cc, cl;
+      cc.held = cl.held = false;
       if (MODE == SEG_CHAIN && !chain_seen(ready_seq, tile_no++, wc)) break;
       if (MODE != SEG_TOKENS && ep.read_c)   // the first C chunk comes in during the MMAs
         load_c(ep, ptr.C, m, (int64_t)t.n0 + c_first * 32, m_left, ext(t.n_valid - c_first * 32), cc);
+      if (MODE == SEG_CHAIN && c_lo != nullptr)
+        load_c(ep, c_lo, m, (int64_t)t.n0 + c_first * 32, m_left, ext(t.n_valid - c_first * 32), cl);
       if (t.k > 0) {
         if (!warp_wait(tfull_bar(buf), (acc_it >> 1) & 1u, wc)) break;
         tc_fence_after();
@@ -955,11 +980,17 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
             const int n_left = t.n_valid - c * 32, n_ext = scratch_d ? ext(n_left) : n_left;
             float x[32];
             take(x);
-            if (c + 2 < chunks) fetch(c + 2);   // the next chunk while this one is stored
-            else release();
+            // The next chunk while this one is stored.  (CHAIN fetches it afterwards: with both
+            // halves of C in registers the compiler would spill, which waits for the loads.)
+            if (c + 2 >= chunks) release();
+            else if (MODE != SEG_CHAIN) fetch(c + 2);
             if (ep.read_c) {
               add_c(ep, ptr.C, m, n, m_left, ext(n_left), cc, x, turn);
               if (c + 2 < chunks) load_c(ep, ptr.C, m, n + 64, m_left, ext(n_left - 64), cc);
+            }
+            if (MODE == SEG_CHAIN && c_lo != nullptr) {
+              fma_c16(ep, x, cl.w, 0, 16);   // (scratch: always held)
+              if (c + 2 < chunks) load_c(ep, c_lo, m, n + 64, m_left, ext(n_left - 64), cl);
             }
             if (MODE == SEG_CHAIN && shift != 0.0f) {
               const int64_t d = m + lane - n;   // the diagonal crosses this row of the chunk at column d
@@ -970,6 +1001,13 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
             if (store_n) store_chunk<DT>(ptr.D, ep.ldd, m, n, m_left, n_ext, x, turn, ep.vec_d);
             if (MODE == SEG_CHAIN && store_t)
               store_chunk_t<DT>(ptr.D, ep.ldd, n, m, n_left, scratch_d ? ext(m_left) : m_left, x, turn, ep.vec_d);
+            if (MODE == SEG_CHAIN && DT == GEMM_F16 && d_lo != nullptr) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] -= __half2float(__float2half_rn(x[j]));
+              store_chunk<DT>(d_lo, ep.ldd, m, n, m_left, n_ext, x, turn, ep.vec_d);
+              if (store_t) store_chunk_t<DT>(d_lo, ep.ldd, n, m, n_left, ext(m_left), x, turn, ep.vec_d);
+            }
+            if (MODE == SEG_CHAIN && c + 2 < chunks) fetch(c + 2);
           }
         };
         with_type(ep.d_dtype, run);

@@ -581,11 +581,15 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
  *   G, ldg      row-major M x N (M > N runs on the transpose), stride_g elements
  *               from matrix to matrix (0: one matrix for all).
  *   D, ldd      row-major, out_dtype F32, F16 or BF16.
- * At most 65535 matrices and 64 steps.  X is held in fp16 between the products (times a
- * power of two that keeps it out of the subnormals); sums are fp32.  Directions that
- * a matrix lacks (the gradient of fewer rows than its sizes) collect that rounding, which
- * every step multiplies by a: with the usual coefficients and 5 steps a noise of a few
- * per cent of the result's norm.  The sum of squares has
+ * At most 65535 matrices and 64 steps; sums are fp32.  Between the products X is a pair of
+ * fp16 halves (times 1024; entries of 64 or more become infinite).  For a bf16 result the
+ * products take X's first half, and E = X X' and F = b E + c E E' as one half each: with the
+ * usual coefficients and 5 steps the result is then 1.7e-3 to 2.2e-3 of its norm from the
+ * exact one (1.66e-3 is the rounding to bf16), and up to 3.5e-3 where the matrix lacks
+ * directions (the gradient of fewer rows than its sizes: what is rounded there grows by a
+ * in every later step).  For F32 and F16 results the products take pairs, three for one,
+ * at the precision of fp32 arithmetic and about three times the time.
+ * The sum of squares has
  * one order, so a matrix gives the same bits alone, in a batch, and transposed.
  * All products of all steps are one cooperative launch whose CTAs wait for one another's
  * tiles; as everywhere each wait ends after the plan's bound, and

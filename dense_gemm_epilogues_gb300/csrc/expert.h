@@ -92,6 +92,7 @@ struct SegParams {
   int32_t tiles_per_group, num_tiles;
   int32_t a_batched;            // TOKENS: the M side has one slice per group
   uint32_t idesc;               // instruction descriptor without N
+  const float* m_scale;         // TOKENS: factors of the M side's rows, M per group; null: 1
   // CHAIN: X is M x N, E and F are M x M; tiles_per_group tiles of E or F (bns columns
   // each), tiles_m x tiles_n of X (bn columns each) per matrix; num_tiles over all steps.
   int32_t batch, steps, bns, bn;
@@ -140,6 +141,7 @@ struct Q4Params {
   int32_t ab_dtype;
   int32_t q_batched;             // tm_q has one slice per group
   int32_t cta_rows;              // columns of weights per CTA
+  const float* col_scale;        // decoded weights are s (q - z) / col_scale, N per group; null: 1
   int32_t group_units, group_shift, vec_s, scale_cols;   // set by launch_q4
   EpiParams epi;
   uint64_t timeout_ns;
@@ -152,6 +154,8 @@ struct Q4Shape {
 };
 Q4Shape q4_shape(int64_t N, int64_t rows_per_group, int64_t groups_used, int sm_count);
 cudaError_t launch_q4(const Q4Params& p, int nt, cudaStream_t stream);
+// out[group][n]: the power of two near 2^-11 times the largest scale of column n.
+cudaError_t launch_q4_range(const Q4Params& p, float* out, cudaStream_t stream);
 cudaError_t launch_q4_dequant(const Q4Params& p, void* out, int64_t ldw, int64_t stride_w, cudaStream_t stream);
 
 // Newton-Schulz: the wide matrix X (m <= n) of each input matrix G.

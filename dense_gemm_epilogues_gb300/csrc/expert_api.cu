@@ -111,9 +111,11 @@ gemm_config_t seg_config(int cg, int64_t tiles, int workers) {
 }
 
 // D[r, :] = epilogue(x[r, :] * W_g) on seg_kernel: x M x K row-major, W_g K x N (w_mn: N
-// contiguous, else K); TMA can address both.
+// contiguous, else K); TMA can address both.  w_scale: factors of W_g's columns, N per group,
+// or null.
 gemm_status_t tokens_product(gemm_plan* plan, const Groups& groups, int64_t M, int64_t N, int64_t K, const Operand& x,
-                             const Operand& w, bool w_mn, const EpiParams& epi, const char* entry, cudaStream_t stream) {
+                             const Operand& w, bool w_mn, const float* w_scale, const EpiParams& epi, const char* entry,
+                             cudaStream_t stream) {
   const int64_t nw = w.stride != 0 ? groups.count : 1;   // matrices of weights
   SegParams p;
   std::memset(&p, 0, sizeof(p));
@@ -138,6 +140,7 @@ gemm_status_t tokens_product(gemm_plan* plan, const Groups& groups, int64_t M, i
     if (!ok) return GEMM_ERR_CUDA;
   }
   p.a_batched = nw > 1 ? 1 : 0;
+  p.m_scale = w_scale;
   p.M = N;
   p.K = (int32_t)K;
   p.tiles_m = (int32_t)((N + 128 * cg - 1) / (128 * cg));
@@ -196,8 +199,8 @@ gemm_status_t gemm_run_grouped(gemm_plan_t plan, gemm_layout_t lb, int64_t group
       if (s != GEMM_OK) return s;
     }
   }
-  return tokens_product(plan, Groups{offsets, (int32_t)groups, (int32_t)M, plan->d_err}, M, N, K, x, w, w_mn, e, "grouped",
-                        stream);
+  return tokens_product(plan, Groups{offsets, (int32_t)groups, (int32_t)M, plan->d_err}, M, N, K, x, w, w_mn, nullptr, e,
+                        "grouped", stream);
 }
 
 gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N, int64_t K, double alpha,
@@ -334,8 +337,13 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   const bool prompt = q4_decode_once(N, K, per_group, std::min(groups, M), plan->sm_count);
   const int64_t ldw = (K + 15) / 16 * 16;
   const size_t wb = prompt ? align_up((size_t)(groups * N * ldw) * 2, 256) : 0;
-  if (qb + xb + wb > 0) {
-    s = ensure_ws(plan, qb + xb + wb, stream);
+  // Weights with scales of a wider type are decoded into fp16 relative to their column's
+  // largest scale (2000 rows of 4096 to 11008, fp32 scales: 140 us, with bf16 x 135); bf16 has the
+  // range of every scale.
+  const bool ranged = prompt && plan->ab == GEMM_F16 && B->scale_dtype != GEMM_F16;
+  const size_t fb = ranged ? (size_t)(groups * N) * sizeof(float) : 0;
+  if (qb + xb + wb + fb > 0) {
+    s = ensure_ws(plan, qb + xb + wb + fb, stream);
     if (s != GEMM_OK) return s;
   }
   char* ws = static_cast<char*>(plan->ws.p);
@@ -349,9 +357,14 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   s = K == 0 ? GEMM_OK : repitch(&x, M, K, 1, nullptr, ws + qb, stream);
   if (s != GEMM_OK) return s;
   if (prompt) {
+    if (ranged) {
+      float* range = reinterpret_cast<float*>(ws + qb + xb + wb);
+      if (launch_q4_range(p, range, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+      p.col_scale = range;
+    }
     if (launch_q4_dequant(p, ws + qb + xb, ldw, N * ldw, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-    return tokens_product(plan, p.g, M, N, K, x, Operand{ws + qb + xb, ldw, groups > 1 ? N * ldw : 0}, false, p.epi,
-                          "q4", stream);
+    return tokens_product(plan, p.g, M, N, K, x, Operand{ws + qb + xb, ldw, groups > 1 ? N * ldw : 0}, false,
+                          p.col_scale, p.epi, "q4", stream);
   }
   const Q4Shape shape = q4_shape(N, per_group, std::min(groups, M), plan->sm_count);
   p.cta_rows = shape.cta_rows;

@@ -406,6 +406,32 @@ __device__ __forceinline__ void unpack_pairs(uint32_t w, uint32_t zero, uint32_t
   }
 }
 
+// Per column the power of two 2^(e - 11), 2^e <= its largest scale < 2^(e + 1): scales of a
+// wider type than fp16 divided by it give weights below 15 * 2^12 < 65504 that are normal
+// fp16 numbers down to 2^-25 of the column's largest, so decoding them into fp16 rounds each
+// once, whatever the scales' size.  One warp per column; infinite and NaN scales are passed
+// over (their weights are infinite or NaN in any case).
+__global__ void __launch_bounds__(256) q4_range_kernel(const __grid_constant__ Q4Params p, float* out) {
+  pdl_wait();
+  const int e = (int)blockIdx.y, n = (int)(blockIdx.x * 8 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  int lo, hi;
+  group_range(p.g, e, lo, hi);
+  if (lo == hi || n >= p.N) return;
+  const char* scales = static_cast<const char*>(p.scales) + e * p.stride_s * dtype_bytes(p.scale_dtype);
+  float most = 0.0f;
+  const int cols = (p.K + p.group - 1) / p.group;
+  for (int c = lane; c < cols; c += 32) {
+    const float s = fabsf(load_as_float(scales, p.scale_dtype, n * p.lds + c));
+    if (s <= 3.402823466e38f) most = fmaxf(most, s);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (lane == 0) {
+    const int biased = (int)(__float_as_uint(most) >> 23) - 11;
+    out[(int64_t)e * p.N + n] = most > 0.0f ? __uint_as_float((uint32_t)max(biased, 1) << 23) : 1.0f;
+  }
+}
+
 // Weights as 16-bit values s * (q - z), K-major with pitch ldw (a multiple of 16; zeros
 // past K); groups without rows are skipped.  Bound by memory (the store is four times the
 // load): a thread takes 16 k of DQ_COLS columns, all of its loads before the first use and
@@ -458,7 +484,9 @@ __global__ void __launch_bounds__(256) q4_dequant_kernel(const __grid_constant__
       }
     } else {
       for (int64_t n = n0; n < min(n0 + DQ_COLS, (int64_t)p.N); ++n) {
-        const float s = load_as_float(scales, p.scale_dtype, n * p.lds + gk);
+        float s = load_as_float(scales, p.scale_dtype, n * p.lds + gk);
+        // (a power of two: its reciprocal has the mirrored exponent)
+        if (p.col_scale != nullptr) s *= __uint_as_float((254u << 23) - __float_as_uint(p.col_scale[(int64_t)e * p.N + n]));
         const int z = zeros ? zeros[n * p.ldz + gk] & 15 : 8;
         uint32_t o[8];
 #pragma unroll
@@ -552,6 +580,10 @@ Q4Shape q4_shape(int64_t N, int64_t rows_per_group, int64_t groups_used, int sm_
 
 cudaError_t launch_q4(const Q4Params& p, int nt, cudaStream_t stream) {
   return p.ab_dtype == GEMM_BF16 ? launch_q4_rows<true>(p, nt, stream) : launch_q4_rows<false>(p, nt, stream);
+}
+
+cudaError_t launch_q4_range(const Q4Params& p, float* out, cudaStream_t stream) {
+  return launch_dependent(q4_range_kernel, dim3((unsigned)((p.N + 7) / 8), (unsigned)p.g.count), 256, stream, p, out);
 }
 
 cudaError_t launch_q4_dequant(const Q4Params& p, void* out, int64_t ldw, int64_t stride_w, cudaStream_t stream) {

@@ -929,6 +929,7 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
           for (int j = 0; j < 32; ++j) r[j] = 0u;
         }
       };
+      if (MODE == SEG_TOKENS && p.m_scale != nullptr && lane < m_left) ep.alpha *= p.m_scale[t.e * p.M + m + lane];
       auto take = [&](float (&x)[32]) {
         tmem_wait_ld();
 #pragma unroll

@@ -544,7 +544,9 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
  * Up to 32 rows per expert on average every term is exact up to the fp32 sum: q - zero is
  * an integer and the scale multiplies the sum of its group.  Beyond, where that is
  * faster, each w is rounded once to A's type, into scratch of 2 bytes per weight, and
- * multiplied on the tensor cores.
+ * multiplied on the tensor cores.  (With F16 A and scales of a wider type it is rounded
+ * relative to its column's largest scale, so their size does not matter; with F16 scales a
+ * w beyond 65504, which F16 does not hold, becomes infinite.)
  * With `offsets`, row r uses the weights, scales, zeros and bias of its group
  * (experts); NULL with groups == 1 is a dense layer.
  * ld_scales and ld_zeros below 2^23 (else GEMM_ERR_UNSUPPORTED).

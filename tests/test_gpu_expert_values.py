@@ -1,4 +1,5 @@
-"""Values at the edges of the expert-layer operators' types: NaN under the fused ReLU."""
+"""Values at the edges of the expert-layer operators' types: NaN under the fused ReLU, and
+4-bit weights whose scales lie outside fp16."""
 import pytest
 import torch
 
@@ -56,3 +57,28 @@ def test_relu_of_4_bit_products_keeps_nan(rows, N):
     ref, mag = grouped_ref(x, w.mT[None], offsets_of([rows]), b, True)
     assert ref[3].isnan().all() and ref[:, 20].isnan().all() and ref[:, 33].isnan().all()
     _same_with_nan(y, ref, mag, K, "f32", U["bf16"] if rows > 32 else 0.0)
+
+
+# fp16 activations with scales of a wider type: weights below fp16's normal numbers, above its
+# largest one, and of sizes that differ from column to column.  A weight is rounded once,
+# relative to its column's largest scale (the groups of a column differ by at most 2^4 here),
+# so the bound is that of a rounding to fp16.  Rows: inside the product; once, on single CTAs
+# and on pairs.
+@pytest.mark.parametrize("rows,N,experts", [(5, 300, 1), (300, 4096, 1), (600, 12000, 1), (300, 1000, 3)])
+@pytest.mark.parametrize("sdt", ["f32", "bf16"])
+@pytest.mark.parametrize("size", ["small", "large", "mixed"])
+def test_4_bit_scales_outside_fp16(rows, N, experts, sdt, size):
+    gen, K = _gen(3), 256
+    x = torch.randn((rows, K), device="cuda", generator=gen).half()
+    q, s, z = random_q4(N, K, 64, torch.float32, True, gen, experts)
+    e = {"small": torch.full((N, 1), -28.0), "large": torch.full((N, 1), 24.0),
+         "mixed": (torch.arange(N) * 7 % 80 - 40).float()[:, None]}[size].cuda()
+    s = (s * torch.exp2(e)).to(DT[sdt])
+    s[:, 4] = 0
+    counts = [rows] if experts == 1 else [rows - 120, 0, 120]
+    off = offsets_of(counts)
+    plan = G.Plan(G.GEMM_F16, G.GEMM_F32)
+    y = G.q4_matmul(x, q, s, 64, zeros=z, offsets=off, out_dtype=DT["f32"], plan=plan)
+    assert plan.device_status() == 0
+    w = q4_weights(q, s, z, K, 64)
+    check(y, *grouped_ref(x, w.mT, off), K, "f32", U["f16"] if rows > 32 else 0.0)

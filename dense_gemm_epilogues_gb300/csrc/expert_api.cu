@@ -334,16 +334,20 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   const int64_t ldq = align_up((size_t)(K + 1) / 2, 16);
   const size_t qb = K == 0 || q_ok ? 0 : align_up((size_t)(groups * N * ldq), 256);
   const size_t xb = K == 0 ? 0 : repitch_bytes(x, M, K, 1);
-  const bool prompt = q4_decode_once(N, K, per_group, std::min(groups, M), plan->sm_count);
+  bool prompt = q4_decode_once(N, K, per_group, std::min(groups, M), plan->sm_count);
   const int64_t ldw = (K + 15) / 16 * 16;
-  const size_t wb = prompt ? align_up((size_t)(groups * N * ldw) * 2, 256) : 0;
+  size_t wb = prompt ? align_up((size_t)(groups * N * ldw) * 2, 256) : 0;
   // Weights with scales of a wider type are decoded into fp16 relative to their column's
   // largest scale (2000 rows of 4096 to 11008, fp32 scales: 140 us, with bf16 x 135); bf16 has the
   // range of every scale.
-  const bool ranged = prompt && plan->ab == GEMM_F16 && B->scale_dtype != GEMM_F16;
-  const size_t fb = ranged ? (size_t)(groups * N) * sizeof(float) : 0;
-  if (qb + xb + wb + fb > 0) {
-    s = ensure_ws(plan, qb + xb + wb + fb, stream);
+  bool ranged = prompt && plan->ab == GEMM_F16 && B->scale_dtype != GEMM_F16;
+  size_t fb = ranged ? (size_t)(groups * N) * sizeof(float) : 0;
+  if (prompt && ensure_ws(plan, qb + xb + wb + fb, stream) != GEMM_OK) {
+    prompt = ranged = false;   // no memory for the decoded weights of all experts: decode inside the product
+    wb = fb = 0;
+  }
+  if (!prompt && qb + xb > 0) {
+    s = ensure_ws(plan, qb + xb, stream);
     if (s != GEMM_OK) return s;
   }
   char* ws = static_cast<char*>(plan->ws.p);

@@ -546,7 +546,8 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
  * faster, each w is rounded once to A's type, into scratch of 2 bytes per weight, and
  * multiplied on the tensor cores.  (With F16 A and scales of a wider type it is rounded
  * relative to its column's largest scale, so their size does not matter; with F16 scales a
- * w beyond 65504, which F16 does not hold, becomes infinite.)
+ * w beyond 65504, which F16 does not hold, becomes infinite.)  Where that scratch cannot be
+ * had, the product decodes inside as for few rows.
  * With `offsets`, row r uses the weights, scales, zeros and bias of its group
  * (experts); NULL with groups == 1 is a dense layer.
  * ld_scales and ld_zeros below 2^23 (else GEMM_ERR_UNSUPPORTED).

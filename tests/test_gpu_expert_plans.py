@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import dense_gemm_epilogues_gb300 as G
-from expert_helpers import DT, offsets_of, random_q4
+from expert_helpers import DT, check, offsets_of, q4_weights, random_q4
 
 pytestmark = pytest.mark.gpu
 
@@ -210,3 +210,24 @@ def test_calls_without_a_plan_keep_one():
         c()
     G.grouped_weight_grad(a[1], a[2], a[0], out_dtype=DT["f32"])
     assert len(expert._DEFAULTS) == made
+
+
+def test_4_bit_products_without_memory_for_decoded_weights():
+    """1024 experts that share 8192 x 20480 weights would decode into 343 GB: more than the
+    device has, so the product decodes inside."""
+    gen, E, N, K, R = _gen(5), 1024, 8192, 20480, 34 * 1024
+    assert 2 * E * N * K > torch.cuda.get_device_properties(0).total_memory
+    q, s, _ = random_q4(N, K, 128, DT["bf16"], False, gen)
+    x = torch.zeros((R, K), device="cuda", dtype=DT["bf16"])
+    x[:40] = torch.randn((40, K), device="cuda", generator=gen).bfloat16()
+    off = torch.full((E + 1,), 40, dtype=torch.int32, device="cuda")
+    off[:6] = 0
+    plan = G.Plan(G.GEMM_BF16, G.GEMM_F32)
+    y = G.q4_matmul(x, q.expand(E, -1, -1), s.expand(E, -1, -1), 128, offsets=off, out_dtype=DT["f32"], plan=plan)
+    assert plan.device_status() == 0
+    w = q4_weights(q[:500], s[:500], None, K, 128)
+    v = x[:40].double()
+    check(y[:40, :500], v @ w.mT, v.abs() @ w.abs().mT, K, "f32")
+    for c in _calls(*_layer(), plan=plan):   # the plan is as good as before
+        c()
+    assert plan.device_status() == 0

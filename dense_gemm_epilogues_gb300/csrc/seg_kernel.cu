@@ -910,7 +910,8 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
       }
       CChunk cc, cl;
       cc.held = cl.held = false;
-      if (MODE == SEG_CHAIN && !chain_seen(ready_seq, tile_no++, wc)) break;
+      // (one answer for the warp: lanes that saw the flag and lanes that saw an abort must not part)
+      if (MODE == SEG_CHAIN && !__all_sync(0xffffffffu, chain_seen(ready_seq, tile_no++, wc))) break;
       if (MODE != SEG_TOKENS && ep.read_c)   // the first C chunk comes in during the MMAs
         load_c(ep, ptr.C, m, (int64_t)t.n0 + c_first * 32, m_left, ext(t.n_valid - c_first * 32), cc);
       if (MODE == SEG_CHAIN && c_lo != nullptr)

@@ -598,16 +598,21 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
     }
     if (MODE == SEG_TOKENS) __syncthreads();
     if (MODE == SEG_TOKENS && warp == 0) {
+      // First tiles, saturated at MOST: offsets that decrease can give the same rows to many
+      // groups, and a sum past 2^31 would wrap to tiles outside the buffers.  (What good
+      // offsets give stays below 2^28, and a group's own tiles do in any case.)
+      constexpr int MOST = 1 << 29;
       int sum = 0;
       for (int e0 = 0; e0 < E; e0 += 32) {
         int v = e0 + lane < E ? (groups.cnt[e0 + lane] + BN - 1) / BN * p.tiles_m : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int u = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += u;
+          if (lane >= o) v = min(v + u, MOST);
         }
-        if (e0 + lane < E) groups.cum[e0 + lane + 1] = sum + v;
-        sum += __shfl_sync(0xffffffffu, v, 31);
+        v = min(v + sum, MOST);
+        if (e0 + lane < E) groups.cum[e0 + lane + 1] = v;
+        sum = __shfl_sync(0xffffffffu, v, 31);
       }
       if (lane == 0) groups.cum[0] = 0;
     }

@@ -110,6 +110,13 @@ gemm_config_t seg_config(int cg, int64_t tiles, int workers) {
   return c;
 }
 
+// A call that launches nothing.
+gemm_status_t nothing(gemm_plan* plan) {
+  plan->last = gemm_config_t{};
+  plan->last.kernel = GEMM_KERNEL_NONE;
+  return GEMM_OK;
+}
+
 // D[r, :] = epilogue(x[r, :] * W_g) on seg_kernel: x M x K row-major, W_g K x N (w_mn: N
 // contiguous, else K); TMA can address both.  w_scale: factors of W_g's columns, N per group,
 // or null.
@@ -178,7 +185,7 @@ gemm_status_t gemm_run_grouped(gemm_plan_t plan, gemm_layout_t lb, int64_t group
   const gemm_dtype_t out = epi ? epi->out_dtype : plan->c;
   gemm_status_t s = check_epilogue(epi, out);
   if (s != GEMM_OK) return s;
-  if (groups == 0 || M == 0 || N == 0) return GEMM_OK;
+  if (groups == 0 || M == 0 || N == 0) return nothing(plan);
   if (!offsets || !D || ldd < N) return GEMM_ERR_INVALID_ARG;
   if (K > 0 && (!A || !B || lda < K || ldb < (lb == GEMM_OP_N ? K : N))) return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
@@ -214,7 +221,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_plan_t plan, int64_t groups, int64_t M
   if (groups < 0 || M < 0 || N < 0 || K < 0 || stride_c < 0 || stride_d < 0) return GEMM_ERR_INVALID_ARG;
   if (groups > kMaxGroups || too_large({M, N, K})) return GEMM_ERR_UNSUPPORTED;
   if (!is_float_out(out_dtype)) return GEMM_ERR_INVALID_ARG;
-  if (groups == 0 || M == 0 || N == 0) return GEMM_OK;
+  if (groups == 0 || M == 0 || N == 0) return nothing(plan);
   if (!offsets || !D || ldd < N) return GEMM_ERR_INVALID_ARG;
   if (groups > 1 && stride_d < (M - 1) * ldd + N) return GEMM_ERR_INVALID_ARG;
   if (K > 0 && (!A || !B || lda < M || ldb < N)) return GEMM_ERR_INVALID_ARG;
@@ -299,7 +306,7 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   const gemm_dtype_t out = epi ? epi->out_dtype : plan->c;
   gemm_status_t s = check_epilogue(epi, out);
   if (s != GEMM_OK) return s;
-  if (groups == 0 || M == 0 || N == 0) return GEMM_OK;
+  if (groups == 0 || M == 0 || N == 0) return nothing(plan);
   if (!D || ldd < N || (groups > 1 && !offsets)) return GEMM_ERR_INVALID_ARG;
   const int64_t kg = (K + B->group_size - 1) / B->group_size;
   if (K > 0 && (!A || lda < K || !B->values || B->ld_values < (K + 1) / 2 || !B->scales || B->ld_scales < kg ||
@@ -382,7 +389,13 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
   if (launch_q4(p, shape.nt, stream) != cudaSuccess) return GEMM_ERR_CUDA;
   gemm_config_t cfg{};
   cfg.kernel = GEMM_KERNEL_SIMT;
+  cfg.bm = 8 * shape.nt;
+  cfg.bn = shape.cta_rows;
+  cfg.bk = 128;
+  cfg.cta_group = cfg.cluster = cfg.split_k = 1;
+  cfg.grid = cfg.tiles = (int32_t)((N + shape.cta_rows - 1) / shape.cta_rows * groups);
   plan->last = cfg;
+  log_config("q4", M, N, K, groups, cfg);
   return GEMM_OK;
 }
 
@@ -400,7 +413,7 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
     return GEMM_ERR_INVALID_ARG;
   if (out_dtype != GEMM_F16 && out_dtype != GEMM_BF16 && out_dtype != GEMM_F32) return GEMM_ERR_INVALID_ARG;
   if (batch > 65535 || too_large({M, N})) return GEMM_ERR_UNSUPPORTED;
-  if (batch == 0 || M == 0 || N == 0) return GEMM_OK;
+  if (batch == 0 || M == 0 || N == 0) return nothing(plan);
   if (!G || !D || ldg < N || ldd < N) return GEMM_ERR_INVALID_ARG;
   if (batch > 1 && stride_d < (M - 1) * ldd + N) return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
@@ -459,11 +472,12 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   if (launch_ortho_input(in, plan->ab, batch, sums, (float)eps, scale, X[0], Xlo[0], ldx, sx, counters, num_counters,
                          stream) != cudaSuccess)
     return GEMM_ERR_CUDA;
-  if (steps == 0)
-    return launch_unscale(X[0], Xlo[0], batch, M, N, ldx, sx, tall, 1.0f / scale, D, out_dtype, ldd, stride_d, stream) ==
-                   cudaSuccess
-               ? GEMM_OK
-               : GEMM_ERR_CUDA;
+  if (steps == 0) {
+    if (launch_unscale(X[0], Xlo[0], batch, M, N, ldx, sx, tall, 1.0f / scale, D, out_dtype, ldd, stride_d, stream) !=
+        cudaSuccess)
+      return GEMM_ERR_CUDA;
+    return nothing(plan);   // (no product)
+  }
   SegParams p;
   std::memset(&p, 0, sizeof(p));
   const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -522,6 +536,7 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   const int workers = workers_of(plan, cg, batch * std::max(per_sym, tm * tn));
   if (launch_seg(p, SEG_CHAIN, cg, false, workers, stream) != cudaSuccess) return GEMM_ERR_CUDA;
   plan->last = seg_config(cg, p.num_tiles, workers);
+  plan->last.bn = bns;
   log_config("orthogonalize", m, n, steps, batch, plan->last);
   return GEMM_OK;
 }

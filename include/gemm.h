@@ -493,8 +493,11 @@ gemm_status_t gemm_noalloc_set_timeout(uint64_t timeout_ns);
  * pitch are taken; one that TMA cannot address (a base off 16 bytes, or rows that are not
  * a multiple of 16 bytes apart) costs a copy into the plan's scratch.  As for gemm_run,
  * calls that overlap on the GPU need a plan each, and captured calls keep their scratch.
- * gemm_plan_last_config describes the tensor-core launch; gemm_run_q4 with few rows
- * reports GEMM_KERNEL_SIMT. */
+ * gemm_plan_last_config describes the launch of the products: GEMM_KERNEL_TC or
+ * GEMM_KERNEL_TC_PAIR on the tcgen05 kernel (of gemm_orthogonalize bn is the width of the
+ * tiles of the symmetric products; X's are 64 wide on single CTAs and 256 on pairs), and
+ * GEMM_KERNEL_SIMT where gemm_run_q4 decodes inside the product (on mma.sync: bm rows per
+ * pass over the weights, bn columns per CTA). */
 
 /* ---------------------------------------------------------------------------
  * gemm_run_grouped -- every row times its group's matrix:

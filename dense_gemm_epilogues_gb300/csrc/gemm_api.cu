@@ -635,14 +635,15 @@ gemm_status_t launch_tc_problem(gemm_plan* plan, const gemm_config_t& cfg, gemm_
   tp.sk_first_tile = tp.num_tiles;
   if (cfg.sk_tiles > 0 && chunk_kb == 0) {
     // Stream-K over the last sk_tiles tiles: two 128 x bn fp32 partial slots per
-    // CTA, then one arrival counter per tile.
+    // CTA, and one arrival counter per tile.
     const size_t part_bytes = (size_t)cfg.grid * 2 * TC_BM * (size_t)bn * sizeof(float);
-    const size_t need = part_bytes + (size_t)tp.num_tiles * sizeof(int32_t);
-    const gemm_status_t s = ensure_buffer(plan, plan->sk1_ws, need, true, plan->kept_counters, stream);
+    gemm_status_t s = ensure_buffer(plan, plan->sk1_ws, part_bytes, false, plan->kept, stream);
+    if (s == GEMM_OK)
+      s = ensure_buffer(plan, plan->sk1_flags, (size_t)tp.num_tiles * sizeof(int32_t), true, plan->kept_counters, stream);
     if (s != GEMM_OK) return s;
     tp.sk_first_tile = tp.num_tiles - std::min<int32_t>(cfg.sk_tiles, tp.num_tiles);
     tp.sk_partials = static_cast<float*>(plan->sk1_ws.p);
-    tp.sk_flags = reinterpret_cast<int32_t*>(static_cast<char*>(plan->sk1_ws.p) + part_bytes);
+    tp.sk_flags = static_cast<int32_t*>(plan->sk1_flags.p);
   }
   // K rotation for a single tile column (whole floating tiles only; GEMM_TC_KROT=0 off).
   tp.k_rotate = (tp.tiles_n == 1 && tp.tiles_m > 1 && chunk_kb == 0 && tp.sk_first_tile == tp.num_tiles) ? 1 : 0;
@@ -891,6 +892,7 @@ gemm_status_t gemm_plan_destroy(gemm_plan_t plan) {
   if (plan->stage) cudaFree(plan->stage);
   if (plan->sk_ws) cudaFree(plan->sk_ws);
   if (plan->sk1_ws.p) cudaFree(plan->sk1_ws.p);
+  if (plan->sk1_flags.p) cudaFree(plan->sk1_flags.p);
   for (const PlanBuffer& b : plan->kept) cudaFree(b.p);
   for (const PlanBuffer& b : plan->kept_counters) cudaFree(b.p);
   if (plan->d_err) cudaFree(plan->d_err);
@@ -934,7 +936,8 @@ gemm_status_t gemm_plan_device_status(gemm_plan_t plan, gemm_stream_t stream, in
   if (cudaMemcpy(&v, plan->d_err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
   if (cudaMemset(plan->d_err, 0, sizeof(int32_t)) != cudaSuccess) return GEMM_ERR_CUDA;
   // A launch that gave up may have left stream-K arrival counters counted in.
-  if (v != 0 && plan->sk1_ws.p && cudaMemset(plan->sk1_ws.p, 0, plan->sk1_ws.bytes) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (v != 0 && plan->sk1_flags.p && cudaMemset(plan->sk1_flags.p, 0, plan->sk1_flags.bytes) != cudaSuccess)
+    return GEMM_ERR_CUDA;
   if (v != 0)
     for (const PlanBuffer& b : plan->kept_counters)
       if (cudaMemset(b.p, 0, b.bytes) != cudaSuccess) return GEMM_ERR_CUDA;

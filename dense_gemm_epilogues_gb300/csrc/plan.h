@@ -24,7 +24,7 @@ struct gemm_plan {
   int sm_count = 0;
   int32_t* d_err = nullptr;          // device error word
   gemmlib::PlanBuffer ws;            // staged operands, partial sums, the expert layers' intermediates
-  // Blocks that a larger one has replaced but captured graphs still use (of sk1_ws: apart,
+  // Blocks that a larger one has replaced but captured graphs still use (of sk1_flags: apart,
   // since a launch that gave up leaves its arrival counters other than zero).
   std::vector<gemmlib::PlanBuffer> kept, kept_counters;
   void* stage = nullptr;             // gemm_run_host device buffers
@@ -34,10 +34,11 @@ struct gemm_plan {
   void* sk_ws = nullptr;             // stream-K partial accumulators and flags (per cluster and CTA)
   size_t sk_ws_bytes = 0;
   int32_t sk_epoch = 0;
-  // Stream-K of the single-CTA kernel: two fp32 partial slots per CTA, then one
-  // arrival counter per tile (zero between launches; each tile's last arriver
-  // resets its counter).
-  gemmlib::PlanBuffer sk1_ws;
+  // Stream-K of the single-CTA kernel: two fp32 partial slots per CTA, and one arrival
+  // counter per tile (zero between launches; each tile's last arriver resets its
+  // counter).  The counters have a buffer of their own: the slots' size goes with the
+  // tile width, and counters behind them would lie in an earlier launch's partial sums.
+  gemmlib::PlanBuffer sk1_ws, sk1_flags;
   gemm_config_t last{};
   uint64_t timeout_ns = 4000000000ull;
   // gemm_run_host's row-panel pipeline: copy-in and copy-out streams and the

@@ -99,7 +99,7 @@ struct SegParams {
   int32_t store_t;              // the result (epi.D) is stored transposed
   // Matrices as pairs of fp16 halves (the second one is what the first rounds away): X
   // always for a X; with `pairs`, X, E and F in the products too, as the sum of three,
-  // hi hi + hi lo + lo hi (the second halves then lie `batch` slices behind the first).
+  // hi lo + lo hi + hi hi (the second halves then lie `batch` slices behind the first).
   int32_t pairs;
   int32_t* counters;            // 3 * steps * batch * tiles_m, zero at the start
   struct {

@@ -427,11 +427,14 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   const int64_t sx = m * ldx, se = m * lde;
   // Tiles: CTA pairs with 256 columns cost the least per product; with too few of them
   // for all pairs, narrower ones on E and F fill the chip, and small problems (whose time
-  // is the chain of tile latencies) run narrow tiles on single CTAs.  Measured, us, single
-  // CTAs / pairs with E and F tiles of 64 / 128 / 256 columns:
-  //   256 x 384 74 / 94 / 106 / 128;  1024^2 108 / 138 / 156 / 197;  700 x 2800 141 / 150 / 170 / 217;
-  //   1024 x 4096 193 / 179 / 204 / 270;  2048^2 282 / 249 / 223 / 274;  32 of 300 x 500
-  //   186 / 228 / 169 / 178;  16 of 768 x 2001 548 / 470 / 387 / 386;  4096 x 11008 - / - / 2650 / 2160.
+  // is the chain of tile latencies) run narrow tiles on single CTAs.  Measured, us, bf16
+  // result, single CTAs / pairs with E and F tiles of 64 / 128 / 256 columns:
+  //   256 x 384 80 / 105 / 116 / 138;  1024^2 116 / 151 / 169 / 213;  700 x 2800 153 / 162 / 184 / 234;
+  //   1024 x 4096 211 / 194 / 220 / 288;  2048^2 299 / 267 / 241 / 294;  32 of 300 x 500
+  //   238 / 274 / 209 / 205;  16 of 768 x 2001 642 / 566 / 480 / 476;  4096 x 11008 - / - / 2331 / 2103.
+  // fp32 result (three products for one): 256 x 384 113 / 140 / 159 / 202;  700 x 2800 290 / 287 /
+  // 335 / 452;  1024 x 4096 434 / 358 / 416 / 593;  2048^2 680 / 548 / 458 / 588;  16 of 768 x 2001
+  // 1397 / 1077 / 907 / 889;  4096 x 11008 - / - / 6730 / 6291.
   const int64_t m256 = (m + 255) / 256, sym256 = batch * m256 * (m256 + 1) / 2, dense256 = batch * m256 * ((n + 255) / 256);
   int cg = 1, bns = 64, bn = 64;   // columns of a tile of E and F, and of X
   if (plan->pair_clusters > 0 && (sym256 >= 24 || dense256 >= 48)) {
@@ -447,7 +450,7 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   // X is held as a pair of fp16 halves for a X, and X, E and F as one half each in the
   // products: that leaves 0.7 to 1.4e-3 of the result's norm for a full-rank matrix and up to
   // 3.1e-3 for one of low rank, beside the 1.7e-3 of a rounding to bf16.  A finer result
-  // takes products of pairs, three for one, whose error is that of fp32 arithmetic.
+  // takes products of pairs, three for one: 2e-6 to 4e-5.
   const bool pairs = out_dtype != GEMM_BF16;
   const int64_t halves = pairs ? 2 : 1;   // second halves behind the first ones, as further slices
   const size_t xs = align_up((size_t)(halves * batch * sx) * 2, 256), es_b = align_up((size_t)(halves * batch * se) * 2, 256);

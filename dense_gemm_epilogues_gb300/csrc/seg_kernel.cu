@@ -673,7 +673,8 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
         b_slab = t.product == 2 ? (uint32_t)SLAB_BYTES : (uint32_t)(p.bns / CG * TC_BK * 2);
         if (!__all_sync(0xffffffffu, chain_seen(ready_seq, tile_no++, wc))) { ok = false; break; }
       }
-      // CHAIN with pairs: three products into one accumulator, hi hi, hi lo, lo hi.
+      // CHAIN with pairs: three products into one accumulator, hi lo, lo hi, hi hi: the small
+      // ones first, since every addition truncates at the running sum's size.
       const int parts = MODE == SEG_CHAIN && p.pairs ? 3 : 1;
       // N side contiguous along N (weights' gradients, X) rather than along K.
       const bool b_mn = MODE == SEG_CHAIN ? t.product == 2 : B_MN;
@@ -684,8 +685,8 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
       for (int part = 0, kb = 0; part < parts; kb + SLABS < num_kb ? kb += SLABS : (kb = 0, ++part)) {
         if (num_kb == 0) break;
         if constexpr (MODE == SEG_CHAIN) {
-          za = t.e + (part == 2 ? p.batch : 0);
-          zb = t.e + (part == 1 ? p.batch : 0);
+          za = t.e + (parts == 3 && part == 1 ? p.batch : 0);
+          zb = t.e + (parts == 3 && part == 0 ? p.batch : 0);
         }
         const bool two = kb + 1 < num_kb;   // K-major: two slabs
         if (!warp_wait(empty_bar(stage), phase ^ 1u, wc)) { ok = false; break; }

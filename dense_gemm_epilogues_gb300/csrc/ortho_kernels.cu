@@ -13,10 +13,10 @@ namespace {
 // in shared memory.  Either way every thread meets the
 // same units in the same order, so the sum of squares has one order, fixed by X's shape
 // alone: a matrix, its transpose, and any batch around it give the same bits.
-// Bound by memory: G is read twice (the second time from L2 when it fits) and X
-// written once.  Many light threads; the next tile's units are under way while one tile
-// is worked on, and the first of the second pass while the norm is added up: 22 and 30 us
-// for 4096 x 11008 in bf16 (4.1 and 6.0 TB/s), 20 and 24 for 16 x 768 x 2001, whose rows
+// Bound by memory: G is read twice (the second time from L2 when it fits) and both halves
+// of X written once.  Many light threads; the next tile's units are under way while one
+// tile is worked on, and the first of the second pass while the norm is added up: 25 and 42
+// us for 4096 x 11008 in bf16 (3.6 and 6.4 TB/s), 20 and 28 for 16 x 768 x 2001, whose rows
 // lie at every alignment.
 constexpr int TILE = 64;
 

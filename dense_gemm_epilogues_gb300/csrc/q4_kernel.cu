@@ -23,7 +23,9 @@
 // the end, in a fixed order.
 // Measured (graph replays): one row of 4096 to 4096 7.2 us, of 4096 to 11008 11.9 us (2 TB/s
 // of packed weights); 16 rows 18.5, 32 rows 25 us; 24 rows over 16 experts, 2048 to 1408,
-// 12.4 us.  Bound by instructions (half of the issue slots, the rest latency), not by HBM.
+// 12.4 us.  Not bound by HBM (one row of 4096 to 11008 reads 1.5 TB/s): half of the issue
+// slots are empty, so most of it is latency (launch, barriers, a warp's few chunks, the
+// reduction), and the busy half is 5 to 7 lane instructions per weight.
 //
 // Many rows (a prompt): the weights are written once as 16-bit values s * (q - z)
 // into scratch and the products run on the tensor cores (seg_kernel.cu).

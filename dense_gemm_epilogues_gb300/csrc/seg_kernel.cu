@@ -47,9 +47,10 @@
 // of the operands' bytes, 85 % of a copy; over 32 experts, 4096 x 2048, input and weight
 // gradient together: 399 us, 1.38 PFLOP/s, held by operand supply; 16 rows over 8 experts,
 // 1024 to 2048: 9.0 us, the latency of a launch and eight stages.  Newton-Schulz, five
-// steps: 4096 x 11008 2.14 ms with its input passes, 1.45 PFLOP/s (the symmetric products
-// counted half), at the power cap; 16 x 768 x 2001 384 us (a tile of 768 k takes about 6 us
-// for 3.9 us of MMAs: L2 traffic); 384 x 256 75 us, 15 dependent products of 4.5 us.
+// steps, bf16 result: 4096 x 11008 2.19 ms with its input passes, 1.42 PFLOP/s (the symmetric
+// products counted half), at the power cap; 16 x 768 x 2001 477 us (a tile of 768 k takes 6 us
+// and more for 3.9 us of MMAs: L2 traffic; without X's second halves 384); 384 x 256 81 us,
+// 15 dependent products of 5 us.  fp32 result, products of pairs: 5.95 ms, 885 and 114 us.
 // Why three stages of two slabs, one producer, at the first case's 241 us of the time: six
 // stages of one slab 257, stages as small as the tile 250, a second producer thread 242.
 //

@@ -452,8 +452,10 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
   // X is held as a pair of fp16 halves for a X, and X, E and F as one half each in the
   // products: that leaves 0.7 to 1.4e-3 of the result's norm for a full-rank matrix and up to
   // 3.1e-3 for one of low rank, beside the 1.7e-3 of a rounding to bf16.  A finer result
-  // takes products of pairs, three for one: 2e-6 to 4e-5.
-  const bool pairs = out_dtype != GEMM_BF16;
+  // takes products of pairs, three for one: 2e-6 to 4e-5.  So does one of at most 16 singular
+  // values, over which the roundings do not average out (1 x 2: up to 1e-2 from one half).
+  // Times of one half / pairs, us: 16 x 64 68 / 78, 16 x 2048 90 / 143, 64 of 16 x 2048 309 / 410.
+  const bool pairs = out_dtype != GEMM_BF16 || m <= 16;
   const int64_t halves = pairs ? 2 : 1;   // second halves behind the first ones, as further slices
   const size_t xs = align_up((size_t)(halves * batch * sx) * 2, 256), es_b = align_up((size_t)(halves * batch * se) * 2, 256);
   const size_t ls = pairs ? 0 : xs;   // without pairs one buffer of second halves: a tile reads and writes only its own part

@@ -593,9 +593,10 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
  * usual coefficients and 5 steps the result is then 1.7e-3 to 2.2e-3 of its norm from the
  * exact one (1.66e-3 is the rounding to bf16), and up to 3.5e-3 where the matrix lacks
  * directions (the gradient of fewer rows than its sizes: what is rounded there grows by a
- * in every later step).  For F32 and F16 results the products take pairs, three for one, in
- * up to three times the time: 2e-6 (384 x 256) to 4e-5 (4096 x 11008) from the exact result,
- * where steps in fp32 are 2e-6 to 8e-6 from it (the tensor cores' sums truncate).
+ * in every later step).  For F32 and F16 results, and where the smaller size is at most
+ * 16, the products take pairs, three for one, in up to three times the time: 2e-6
+ * (384 x 256) to 4e-5 (4096 x 11008) from the exact result, where steps in fp32 are 2e-6
+ * to 8e-6 from it (the tensor cores' sums truncate).
  * The sum of squares has
  * one order, so a matrix gives the same bits alone, in a batch, and transposed.
  * All products of all steps are one cooperative launch whose CTAs wait for one another's

@@ -89,6 +89,23 @@ def test_few_rows(batch, m, n, rank, tall):
             assert _rel(d[z], ref) <= bound, (out, z, _rel(d[z], ref), bound)
 
 
+@pytest.mark.parametrize("m,n", [(1, 2), (1, 300), (2, 5), (3, 8), (5, 21), (16, 64), (16, 17)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_matrices_of_a_few_rows(m, n, tall):
+    """300 matrices of a few singular values, where no rounding averages out: a bf16 result
+    is as near as its own rounding and fp32 steps allow."""
+    gen = torch.Generator("cuda").manual_seed(3)
+    g = torch.randn((300, m, n), device="cuda", generator=gen)
+    plan = G.Plan(G.GEMM_F32, G.GEMM_F32)
+    d = G.orthogonalize(g.mT.contiguous() if tall else g, plan=plan)
+    assert plan.device_status() == 0
+    d = d.mT if tall else d
+    for z in range(300):
+        ref = newton_schulz_ref(g[z])
+        bound = U["bf16"] + 4 * _rel(_plain(g[z]), ref) + 12 * -(-n // 16) * 2.0 ** -23
+        assert _rel(d[z], ref) <= bound, (z, _rel(d[z], ref), bound)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,n", [(1, 1), (40, 1), (7, 9), (333, 1001), (257, 255), (1536, 520)])
 def test_wide_results_are_as_precise_as_their_type(m, n, dtype):

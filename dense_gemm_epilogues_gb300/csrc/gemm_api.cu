@@ -131,6 +131,21 @@ static bool encode_fn() {
   return g_encode != nullptr;
 }
 
+// g_encode, which needs a current context: a thread that has made no runtime call of its own
+// (it uses a plan that another one made) has none yet, and gets the device's.
+static bool encode(CUtensorMap* tm, CUtensorMapDataType dt, int rank, const void* ptr, const cuuint64_t* dims,
+                   const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
+                   CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+  const cuuint32_t estr[3] = {1, 1, 1};
+  for (int attempt = 0;; ++attempt) {
+    if (g_encode(tm, dt, rank, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                 promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+      return true;
+    int dev = 0;
+    if (attempt > 0 || cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+  }
+}
+
 bool encode_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
                uint64_t ld, uint64_t nbatch, uint64_t bstride, uint32_t box_inner, uint32_t box_outer) {
   if (!encode_fn()) return false;
@@ -141,11 +156,7 @@ bool encode_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_
   cuuint64_t dims[3] = {inner, outer, nbatch};
   cuuint64_t strides[2] = {ld * 2, bstride * 2};
   cuuint32_t box[3] = {box_inner, box_outer, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = g_encode(tm, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return encode(tm, dt, 3, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool encode_tiled(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
@@ -156,9 +167,7 @@ bool encode_tiled(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint
   cuuint64_t dims[3] = {inner, outer, nbatch};
   cuuint64_t strides[2] = {pitch_bytes, bstride_bytes};
   cuuint32_t box[3] = {box_inner, box_outer, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return g_encode(tm, dt, flat ? 2 : 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode(tm, dt, flat ? 2 : 3, ptr, dims, strides, box, swizzle);
 }
 
 }  // namespace gemmlib
@@ -660,11 +669,7 @@ bool encode_2d(CUtensorMap* tm, CUtensorMapDataType dt, int es, const void* ptr,
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {ld * (uint64_t)es};
   cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(tm, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return encode(tm, dt, 2, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // A 1-D tensor map over a vector of n elements, boxes of `box` elements.
@@ -673,11 +678,7 @@ bool encode_1d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_
   cuuint64_t dims[1] = {n};
   cuuint64_t strides[1] = {0};   // unused for rank 1
   cuuint32_t boxd[1] = {box};
-  cuuint32_t estr[1] = {1};
-  CUresult r = g_encode(tm, dt, 1, const_cast<void*>(ptr), dims, strides, boxd, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return encode(tm, dt, 1, ptr, dims, strides, boxd, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 CUtensorMapDataType tma_dtype(gemm_dtype_t t) {

@@ -231,3 +231,28 @@ def test_4_bit_products_without_memory_for_decoded_weights():
     for c in _calls(*_layer(), plan=plan):   # the plan is as good as before
         c()
     assert plan.device_status() == 0
+
+
+def test_a_plan_in_threads_that_use_cuda_for_the_first_time():
+    """A plan and memory that the main thread made: the call is the new thread's first."""
+    a = _layer()
+    plan, b = G.Plan(G.GEMM_BF16, G.GEMM_F32), a[3][0]
+    big = torch.randn((4096, 4096), device="cuda", generator=_gen(1)).bfloat16()
+
+    def diagonal():
+        d = torch.empty((4096, 4096), device="cuda")
+        G.gemm_run_diag(plan.handle, G.GEMM_SIDE_LEFT, G.GEMM_OP_T, 4096, 4096, 1.0, big.data_ptr(), big.data_ptr(), 4096,
+                        0.0, None, 0, d.data_ptr(), 4096)
+        return d
+
+    calls = _calls(*a, plan=plan) + [lambda: G.matmul(a[1], b, plan=plan), diagonal]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    for call, out in zip(calls, want):
+        got = []
+        t = threading.Thread(target=lambda: got.append(call()))
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert len(got) == 1 and torch.equal(got[0], out)
+    assert plan.device_status() == 0

@@ -51,19 +51,43 @@ def _device(x, *others) -> int:
     return d
 
 
-# The plans of calls that are given none, by (thread, device, stream, operand type, c_dtype):
-# calls that can overlap never share scratch.  Kept for the life of the process.
-_DEFAULTS = {}
+# The plans of calls that are given none: per thread by (device, stream, operand type,
+# c_dtype), so calls that can overlap never share scratch.  A thread that ends leaves its
+# plans to later ones on the same streams; none is destroyed (a captured graph may use it).
+_DEFAULTS = []   # all of them
+_FREE = {}       # lists of those whose thread has ended
+
+
+class _Lease(dict):
+    def __del__(self, free=_FREE):   # (bound here: at exit the module's names may be gone)
+        for key, plan in self.items():
+            free.setdefault(key, []).append(plan)
+
+
+class _Thread(threading.local):
+    def __init__(self):
+        self.plans = _Lease()
+
+
+_THREAD = _Thread()
+
+
+def _default_plan(key) -> Plan:
+    try:
+        plan = _FREE[key].pop()
+    except (KeyError, IndexError):
+        device, _, ab_code, c_code = key
+        plan = Plan(ab_code, c_code, device)
+        _DEFAULTS.append(plan)
+    _THREAD.plans[key] = plan
+    return plan
 
 
 def _plan_for(plan, ab_code: int, c_code: int, device: int, stream: int) -> Plan:
     """The caller's plan, which has to be for these operands, or this stream's default one."""
     if plan is None:
-        key = (threading.get_ident(), device, stream, ab_code, c_code)
-        plan = _DEFAULTS.get(key)
-        if plan is None:
-            plan = _DEFAULTS[key] = Plan(ab_code, c_code, device)
-        return plan
+        key = (device, stream, ab_code, c_code)
+        return _THREAD.plans.get(key) or _default_plan(key)
     if plan.ab_dtype != ab_code:
         raise GemmError(GEMM_ERR_UNSUPPORTED, "a plan of another operand type")
     if plan.device != device:
@@ -79,8 +103,8 @@ def default_plan_status(device=None) -> int:
     index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
     torch.cuda.synchronize(index)
     code = 0
-    for key, plan in list(_DEFAULTS.items()):
-        if key[1] == index:
+    for plan in list(_DEFAULTS):
+        if plan.device == index:
             code = plan.device_status() or code
     return code
 

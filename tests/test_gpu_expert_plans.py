@@ -256,3 +256,27 @@ def test_a_plan_in_threads_that_use_cuda_for_the_first_time():
         torch.cuda.synchronize()
         assert len(got) == 1 and torch.equal(got[0], out)
     assert plan.device_status() == 0
+
+
+def test_threads_that_end_leave_their_plans_to_others():
+    from dense_gemm_epilogues_gb300 import expert
+    a = _layer()
+    want = [c() for c in _calls(*a)]
+    got = []
+
+    def work():
+        got.append([c() for c in _calls(*a)])
+
+    def one():
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+
+    one()
+    made = len(expert._DEFAULTS)
+    for _ in range(5):
+        one()
+    assert len(expert._DEFAULTS) == made and len(got) == 6
+    for out in got:
+        for u, v in zip(out, want):
+            assert torch.equal(u, v)

@@ -596,7 +596,8 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
  * in every later step).  For F32 and F16 results, and where the smaller size is at most
  * 16, the products take pairs, three for one, in up to three times the time: 2e-6
  * (384 x 256) to 4e-5 (4096 x 11008) from the exact result, where steps in fp32 are 2e-6
- * to 8e-6 from it (the tensor cores' sums truncate).
+ * to 8e-6 from it.  The tensor cores' sums truncate, so this grows with the longer size
+ * (2000 x 1200000: 3e-3, with a bf16 result 3.8e-3).
  * The sum of squares has
  * one order, so a matrix gives the same bits alone, in a batch, and transposed.
  * All products of all steps are one cooperative launch whose CTAs wait for one another's

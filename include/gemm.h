@@ -588,7 +588,8 @@ gemm_status_t gemm_run_q4(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N
  *               from matrix to matrix (0: one matrix for all).
  *   D, ldd      row-major, out_dtype F32, F16 or BF16.
  * At most 65535 matrices and 64 steps; sums are fp32.  Between the products X is a pair of
- * fp16 halves (times 1024; entries of 64 or more become infinite).  For a bf16 result the
+ * fp16 halves (times 1024; entries of 64 or more become infinite, as do those of F of 256
+ * or more where the products take pairs).  For a bf16 result the
  * products take X's first half, and E = X X' and F = b E + c E E' as one half each: with the
  * usual coefficients and 5 steps the result is then 1.7e-3 to 2.2e-3 of its norm from the
  * exact one (1.66e-3 is the rounding to bf16), and up to 3.5e-3 where the matrix lacks

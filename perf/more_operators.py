@@ -151,12 +151,14 @@ def _top(logits, top, mask, experts):
 
 
 def _rows(index, experts):
-    """(slots, counts, offsets): the place of every (token, expert) among the rows sorted by expert."""
+    """(slots, counts, offsets, routed): the place of every (token, expert) among the rows sorted by expert, the
+    rows of every expert, where they begin, and how many tokens have any."""
     flat = torch.where(index < 0, experts, index).flatten().long()
     place = torch.argsort(torch.argsort(flat, stable=True), stable=True)
     counts = (flat[:, None] == torch.arange(experts, device=flat.device)).sum(0).int()
     offsets = torch.cat((counts.new_zeros(1), counts.cumsum(0).int()))
-    return torch.where(index < 0, -1, place.view(index.shape)).int(), counts, offsets
+    routed = (index[:, 0] >= 0).sum().int()
+    return torch.where(index < 0, -1, place.view(index.shape)).int(), counts, offsets, routed
 
 
 def _shapes(case):
@@ -202,20 +204,19 @@ def prepare(case, seed):
         st["mask"] = _mask(T) if case["padded"] else None
         if op == "route_grad":   # what the forward pass left
             st["experts"], _ = _top(st["logits"].float(), k, st["mask"], E)
-            st["slots"], st["counts"], st["offsets"] = _rows(st["experts"], E)
+            st["slots"], st["counts"], st["offsets"], st["routed"] = _rows(st["experts"], E)
             z = st["logits"].double()
             s = torch.where(st["experts"] < 0, 0.0, z.softmax(1).gather(1, st["experts"].long().clamp(min=0)))
             if case["renormalize"]:
                 s = s / s.sum(1, keepdim=True).clamp(min=1e-300)
             st["weights"] = s.float()
-            st["loss"] = torch.zeros((), device="cuda")
             st["dweights"] = _randn((T, k), gen)
             st["dloss"] = torch.full((), 0.01 * T, device="cuda")
         st["keep"] = T <= 64   # a decoding loop keeps the buffers of its router
     elif op in ("exchange", "exchange_grad"):
         T, k, d, E = case["tokens"], case["top"], case["d"], case["experts"]
         st["experts"], value = _top(_logits(T, E, gen), k, _mask(T) if case["padded"] else None, E)
-        st["slots"], st["counts"], st["offsets"] = _rows(st["experts"], E)
+        st["slots"], st["counts"], st["offsets"], st["routed"] = _rows(st["experts"], E)
         st["weights"] = torch.where(st["experts"] < 0, 0.0, value.softmax(1))
         st["y"] = _randn((T * k, d), gen, 1.0, dt)
         if op == "exchange":
@@ -298,20 +299,21 @@ def _plain(st):
         E, k = c["experts"], c["top"]
         z = st["logits"].float()
         index, value = _top(z, k, st["mask"], E)
-        slots, counts, offsets = _rows(index, E)
+        slots, counts, offsets, routed = _rows(index, E)
         used = index[:, :1] >= 0
         p = _probabilities(z, used)
         w = torch.where(index >= 0, p.gather(1, index.long().clamp(min=0)), 0.0)
         if c["renormalize"]:
             e = torch.where(index >= 0, torch.exp(value - torch.where(used, value[:, :1], 0.0)), 0.0)
             w = torch.where(used, e / e.sum(1, keepdim=True), 0.0)
-        loss = (_balance(counts, E) * p.sum(0)).sum() / used.sum().clamp(min=1)
-        return {"weights": w, "experts": index, "slots": slots, "counts": counts, "offsets": offsets, "loss": loss}
+        loss = (_balance(counts, E) * p.sum(0)).sum() / routed.clamp(min=1)
+        return {"weights": w, "experts": index, "slots": slots, "counts": counts, "offsets": offsets,
+                "routed": routed, "loss": loss}
     if op == "route_grad":
         E = c["experts"]
         used = st["experts"][:, :1] >= 0
         p = _probabilities(st["logits"].float(), used)
-        g = (st["dloss"] / used.sum().clamp(min=1)) * _balance(st["counts"], E).expand_as(p)
+        g = (st["dloss"] / st["routed"].clamp(min=1)) * _balance(st["counts"], E).expand_as(p)
         chosen = st["experts"] >= 0
         dw = torch.where(chosen, st["dweights"], 0.0)
         at = st["experts"].long().clamp(min=0)
@@ -358,8 +360,8 @@ def _plan(G, dtype):
 
 def _routing(G, st):
     c = st["case"]
-    return G.Routing(st["weights"], st["experts"], st["slots"], st["counts"], st["offsets"], st.get("loss"),
-                     c.get("renormalize", True))
+    return G.Routing(st["weights"], st["experts"], st["slots"], st["counts"], st["offsets"], st["routed"],
+                     renormalize=c.get("renormalize", True))
 
 
 def _package(st):
@@ -380,7 +382,7 @@ def _package(st):
         if st["keep"]:
             st["out"] = r
         return {"weights": r.weights, "experts": r.experts, "slots": r.slots, "counts": r.counts,
-                "offsets": r.offsets, "loss": r.loss}
+                "offsets": r.offsets, "routed": r.routed, "loss": r.loss}
     if op == "route_grad":
         return G.route_grad(st["logits"], _routing(G, st), dweights=st["dweights"], dloss=st["dloss"], plan=plan)
     if op == "exchange":
@@ -462,7 +464,7 @@ def exact(case, seed):
         tokens, rows = (index[:, 0] >= 0).sum().clamp(min=1), counts.sum().clamp(min=1)
         if op == "route":
             return {"weights": w, "experts": None, "slots": None, "counts": None, "offsets": None,
-                    "loss": E / (rows * tokens) * (counts * p.sum(0)).sum()}
+                    "routed": None, "loss": E / (rows * tokens) * (counts * p.sum(0)).sum()}
         out = torch.zeros_like(p)
         dw = st["dweights"].double()
         for j in range(case["top"]):   # each chosen weight's Jacobian in turn

@@ -43,7 +43,8 @@ EXPORTED = ["gemm_plan_create", "gemm_plan_destroy", "gemm_run", "gemm_run_host"
             "gemm_plan_set_timeout", "gemm_status_string", "gemm_abi_version",
             "gemm_run_s8_noalloc", "gemm_noalloc_device_status", "gemm_noalloc_set_timeout",
             "gemm_run_strided_batched", "gemm_run_diag", "gemm_run_complex",
-            "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_run_q4", "gemm_orthogonalize"]
+            "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_run_q4", "gemm_orthogonalize",
+            "gemm_route", "gemm_route_grad", "gemm_dispatch", "gemm_combine", "gemm_combine_grad", "gemm_clip_norm"]
 
 
 GEMM_XF_A, GEMM_XF_B = 1, 2
@@ -62,6 +63,16 @@ class gemm_q4_t(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("scale_dtype", ctypes.c_int), ("ld_scales", ctypes.c_int64),
                 ("stride_scales", ctypes.c_int64), ("zeros", ctypes.c_void_p), ("ld_zeros", ctypes.c_int64),
                 ("stride_zeros", ctypes.c_int64), ("group_size", ctypes.c_int64)]
+
+
+class gemm_routing_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("weights", "experts", "slots", "counts", "offsets", "routed", "loss")] + \
+               [("top", ctypes.c_int32), ("renormalize", ctypes.c_int32)]
+
+
+class gemm_tensor_t(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("src_type", ctypes.c_int), ("dst_type", ctypes.c_int)]
 
 
 class gemm_config_t(ctypes.Structure):
@@ -132,6 +143,13 @@ def load_library(path: str = LIB_PATH):
                                 epi_p, i64, vp]
     lib.gemm_orthogonalize.argtypes = [vp, i64, i64, i64, ci, ctypes.POINTER(dbl), dbl, vp, i64, i64, vp, i64,
                                        i64, ci, vp]
+    route_p = ctypes.POINTER(gemm_routing_t)
+    lib.gemm_route.argtypes = [vp, i64, i64, vp, i64, vp, route_p, vp]
+    lib.gemm_route_grad.argtypes = [vp, i64, i64, vp, i64, route_p, vp, dbl, vp, vp, i64, vp]
+    lib.gemm_dispatch.argtypes = [vp, i64, i64, i64, i64, vp, i64, vp, vp, vp, i64, vp]
+    lib.gemm_combine.argtypes = [vp, i64, i64, i64, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp]
+    lib.gemm_combine_grad.argtypes = [vp, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp]
+    lib.gemm_clip_norm.argtypes = [vp, i64, ctypes.POINTER(gemm_tensor_t), dbl, dbl, vp, vp]
     for name in EXPORTED:
         if name not in ("gemm_status_string", "gemm_abi_version"):
             getattr(lib, name).restype = ci
@@ -406,15 +424,18 @@ def matmul(a, b, *, c=None, alpha: float = 1.0, beta: float = 0.0, bias=None,
     return out
 
 
-# ---- expert layers (expert.py): loaded on first use, since they need torch ----
+# ---- expert layers (expert.py) and what stands around them (layers.py): loaded on first
+# use, since they need torch ----
 
-_EXPERT = ("grouped_matmul", "grouped_weight_grad", "quantize_q4", "q4_matmul", "orthogonalize",
-           "default_plan_status")
+_LAZY = {n: "expert" for n in ("grouped_matmul", "grouped_weight_grad", "quantize_q4", "q4_matmul", "orthogonalize",
+                               "default_plan_status")}
+_LAZY.update({n: "layers" for n in ("Routing", "route", "route_grad", "dispatch", "dispatch_grad", "combine",
+                                    "combine_grad", "TensorList", "clip_grad_norm", "grad_norm")})
 
 
 def __getattr__(name):
-    if name in _EXPERT:
-        from . import expert
-        globals().update({n: getattr(expert, n) for n in _EXPERT})
+    if name in _LAZY:
+        import importlib
+        globals()[name] = getattr(importlib.import_module("." + _LAZY[name], __name__), name)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,6 +1,6 @@
 """Build libgemm.so (in-tree) with nvcc for sm_103a.
 
-Eleven translation units are compiled in parallel and linked into
+The translation units are compiled in parallel and linked into
 ``dense_gemm_epilogues_gb300/libgemm.so``; objects go to ``_build/``.  The
 CUDA runtime is linked statically, the driver API (TMA descriptor encoding) is
 reached through the runtime's driver entry-point query, so the library has no
@@ -18,8 +18,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemm.so")
 SOURCES = ["gemm_api.cu", "tc_kernel.cu", "tc2_kernel.cu", "simt_kernels.cu", "diag_kernel.cu",
-           "pair_kernel.cu", "expert_api.cu", "q4_kernel.cu", "repitch_kernel.cu", "ortho_kernels.cu", "seg_kernel.cu"]
-HEADERS = ["common.cuh", "kernels.h", "plan.h", "expert.h"]
+           "pair_kernel.cu", "expert_api.cu", "q4_kernel.cu", "repitch_kernel.cu", "ortho_kernels.cu", "seg_kernel.cu",
+           "layer_api.cu", "route_kernels.cu", "exchange_kernels.cu", "clip_kernels.cu"]
+HEADERS = ["common.cuh", "kernels.h", "plan.h", "expert.h", "layer.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,320 @@
+"""What stands around the products of a layer, on torch tensors: the routing of tokens to
+experts with its balance loss, rows between tokens and experts, gradients clipped by their
+global norm.
+
+Like the expert-layer functions these check their arguments, read pointers, strides and the
+current stream and call the C entry points of include/gemm.h.  A call without `plan` uses the
+default plan of its thread, stream and operand type; nothing is recorded for autograd: each
+function's gradient is a function beside it.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import GEMM_F32, GemmError, Plan, gemm_routing_t, gemm_tensor_t
+from .expert import _LIB, _code, _device, _pitch, _plan_for, _raw_stream
+
+_I32, _F32 = torch.int32, torch.float32
+
+
+class Routing(NamedTuple):
+    """Tokens routed to experts (route); the gradients and the exchange of rows read it."""
+    weights: torch.Tensor    # [tokens, top] float32: what each chosen expert's row is added with
+    experts: torch.Tensor    # [tokens, top] int32, best first; -1 behind the last
+    slots: torch.Tensor      # [tokens, top] int32: places among the rows sorted by expert; -1
+    counts: torch.Tensor     # [experts] int32: rows of each expert
+    offsets: torch.Tensor    # [experts + 1] int32, as grouped_matmul takes them
+    routed: torch.Tensor     # int32 scalar: tokens that have any expert
+    loss: Optional[torch.Tensor] = None   # float32 scalar: the balance loss
+    renormalize: bool = True
+
+
+def _flat(t, dtype, shape, name: str):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor of shape {tuple(shape)}")
+
+
+def _check_routing(r, tokens: int, experts: int):
+    shape = r.experts.shape
+    if len(shape) != 2 or shape[0] != tokens:
+        raise ValueError("the routing is of another number of tokens")
+    _flat(r.experts, _I32, shape, "experts")
+    _flat(r.slots, _I32, shape, "slots")
+    _flat(r.weights, _F32, shape, "weights")
+    _flat(r.counts, _I32, (experts,), "counts")
+    _flat(r.offsets, _I32, (experts + 1,), "offsets")
+    if r.routed.dtype is not _I32 or r.routed.numel() != 1:
+        raise ValueError("routed must be an int32 scalar")
+    if r.loss is not None and (r.loss.dtype is not _F32 or r.loss.numel() != 1):
+        raise ValueError("loss must be a float32 scalar")
+    return shape[1]
+
+
+def _c_routing(r, top: int):
+    return gemm_routing_t(r.weights.data_ptr(), r.experts.data_ptr(), r.slots.data_ptr(), r.counts.data_ptr(),
+                          r.offsets.data_ptr(), r.routed.data_ptr(), r.loss.data_ptr() if r.loss is not None else None,
+                          top, 1 if r.renormalize else 0)
+
+
+def route(logits, top: int, *, renormalize: bool = True, mask=None, out: Optional[Routing] = None,
+          plan: Optional[Plan] = None, stream=None) -> Routing:
+    """Routes every token to its `top` largest logits (gemm_route): a Routing with the weights
+    (softmax at the chosen experts, adding up to 1 if renormalize), the experts, every row's
+    place among the rows sorted by expert, the experts' row counts and offsets, and the balance
+    loss  E * sum_e (rows of e / rows) * (mean over tokens of p_e),  1 for an even routing.
+
+    logits: [tokens, experts] float32, float16 or bfloat16 with contiguous rows.  Equal logits
+    go to the lower index; an expert at -inf is not taken (its weight is 0, its expert and slot
+    -1).  mask: [tokens] bool or uint8, the tokens that count.  out: a Routing to write into."""
+    tokens, experts = logits.shape
+    if not 0 < top <= experts:
+        raise ValueError("top must be between 1 and the number of experts")
+    ld = _pitch((tokens, experts), logits.stride(), "logits")
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (tokens,)
+                             or not mask.is_contiguous()):
+        raise ValueError("mask must be a contiguous bool or uint8 tensor of one entry per token")
+    device = _device(logits, mask)
+    if out is None:
+        d = logits.device
+        r = Routing(torch.empty((tokens, top), dtype=_F32, device=d), torch.empty((tokens, top), dtype=_I32, device=d),
+                    torch.empty((tokens, top), dtype=_I32, device=d), torch.empty((experts,), dtype=_I32, device=d),
+                    torch.empty((experts + 1,), dtype=_I32, device=d), torch.empty((), dtype=_I32, device=d),
+                    torch.empty((), dtype=_F32, device=d), renormalize)
+    else:
+        if _check_routing(out, tokens, experts) != top:
+            raise ValueError("out is of another top")
+        _device(logits, out.weights, out.experts, out.slots, out.counts, out.offsets, out.routed, out.loss)
+        r = out if out.renormalize == renormalize else out._replace(renormalize=renormalize)
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(logits.dtype), GEMM_F32, device, stream)
+    status = _LIB.gemm_route(plan.handle, tokens, experts, logits.data_ptr(), ld,
+                             mask.data_ptr() if mask is not None else None, _c_routing(r, top), stream)
+    if status:
+        raise GemmError(status, "gemm_route")
+    return r
+
+
+def route_grad(logits, routing: Routing, *, dweights=None, dloss=None, out=None, plan: Optional[Plan] = None,
+               stream=None):
+    """The gradient of a routing's weights and balance loss by its logits (gemm_route_grad), in
+    their type and shape; the choice and the counts are constants.
+
+    dweights: [tokens, top] float32, or None.  dloss: a float32 scalar on the device, a number,
+    or None (the loss is not used)."""
+    tokens, experts = logits.shape
+    top = _check_routing(routing, tokens, experts)
+    if dweights is not None:
+        _flat(dweights, _F32, (tokens, top), "dweights")
+    scale, p = 1.0, None
+    if dloss is None:
+        scale = 0.0
+    elif isinstance(dloss, torch.Tensor):
+        if dloss.dtype is not _F32 or dloss.numel() != 1:
+            raise ValueError("dloss must be a float32 scalar")
+        p = dloss.data_ptr()
+    else:
+        scale = float(dloss)
+    if out is None:
+        out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape or out.dtype is not logits.dtype:
+        raise ValueError("out must have the shape and type of logits")
+    device = _device(logits, out, dweights, dloss if p is not None else None, routing.weights, routing.experts,
+                     routing.counts, routing.offsets, routing.routed)
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(logits.dtype), GEMM_F32, device, stream)
+    status = _LIB.gemm_route_grad(plan.handle, tokens, experts, logits.data_ptr(),
+                                  _pitch((tokens, experts), logits.stride(), "logits"), _c_routing(routing, top),
+                                  dweights.data_ptr() if dweights is not None else None, scale, p, out.data_ptr(),
+                                  _pitch((tokens, experts), out.stride(), "out"), stream)
+    if status:
+        raise GemmError(status, "gemm_route_grad")
+    return out
+
+
+def _exchange(routing, x, out, rows: int, *others):
+    """(tokens, top, width, device, out) of an exchange: x [.., width], out [rows, width] of x's type."""
+    shape = routing.slots.shape
+    if len(shape) != 2 or x.dim() != 2:
+        raise ValueError("rows must be [rows, width] and slots [tokens, top]")
+    _flat(routing.slots, _I32, shape, "slots")
+    width = x.shape[1]
+    if out is None:
+        out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+    elif out.shape != (rows, width) or out.dtype is not x.dtype:
+        raise ValueError("out must be [rows, width] of the rows' type")
+    return shape[0], shape[1], width, _device(x, out, routing.slots, *others), out
+
+
+def _used(routing):
+    e = routing.offsets
+    if e.dtype is not _I32 or e.dim() != 1 or e.stride(0) != 1 or e.shape[0] < 1:
+        raise ValueError("offsets must be a contiguous int32 tensor")
+    return e.data_ptr() + 4 * (e.shape[0] - 1)
+
+
+def dispatch(x, routing: Routing, *, out=None, plan: Optional[Plan] = None, stream=None):
+    """Every token's row to the places of its experts' rows (gemm_dispatch): [tokens * top, width]
+    rows sorted by expert, those behind the last used one zero.  x: [tokens, width] float32,
+    float16 or bfloat16 with contiguous rows."""
+    rows = out.shape[0] if out is not None else routing.slots.numel()
+    tokens, top, width, device, out = _exchange(routing, x, out, rows, routing.offsets)
+    if x.shape[0] != tokens:
+        raise ValueError("x must have one row per token")
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(x.dtype), GEMM_F32, device, stream)
+    status = _LIB.gemm_dispatch(plan.handle, tokens, top, rows, width, x.data_ptr(), _pitch(x.shape, x.stride(), "x"),
+                                routing.slots.data_ptr(), _used(routing), out.data_ptr(),
+                                _pitch(out.shape, out.stride(), "out"), stream)
+    if status:
+        raise GemmError(status, "gemm_dispatch")
+    return out
+
+
+def _combine(y, routing, weights, residual, out, plan, stream):
+    tokens, top, width, device, out = _exchange(routing, y, out, routing.slots.shape[0], weights, residual)
+    if weights is not None:
+        _flat(weights, _F32, (tokens, top), "weights")
+    ldr = 0
+    if residual is not None:
+        if residual.shape != (tokens, width) or residual.dtype is not y.dtype:
+            raise ValueError("residual must be [tokens, width] of y's type")
+        ldr = _pitch(residual.shape, residual.stride(), "residual")
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(y.dtype), GEMM_F32, device, stream)
+    status = _LIB.gemm_combine(plan.handle, tokens, top, y.shape[0], width, y.data_ptr(),
+                               _pitch(y.shape, y.stride(), "y"), routing.slots.data_ptr(),
+                               weights.data_ptr() if weights is not None else None,
+                               residual.data_ptr() if residual is not None else None, ldr, out.data_ptr(),
+                               _pitch(out.shape, out.stride(), "out"), stream)
+    if status:
+        raise GemmError(status, "gemm_combine")
+    return out
+
+
+def combine(y, routing: Routing, *, residual=None, out=None, plan: Optional[Plan] = None, stream=None):
+    """The experts' rows back to their tokens (gemm_combine):
+    out[t] = residual[t] + sum_j weights[t, j] * y[slots[t, j]], [tokens, width] of y's type.
+
+    y: [rows, width] sorted rows; residual: [tokens, width] of y's type (it may be `out`)."""
+    return _combine(y, routing, routing.weights, residual, out, plan, stream)
+
+
+def dispatch_grad(drows, routing: Routing, *, out=None, plan: Optional[Plan] = None, stream=None):
+    """The gradient of dispatch: the sum of every token's rows of drows (gemm_combine with
+    weights of one)."""
+    return _combine(drows, routing, None, None, out, plan, stream)
+
+
+def combine_grad(dout, y, routing: Routing, *, out=None, plan: Optional[Plan] = None, stream=None):
+    """(dy, dweights) of combine (gemm_combine_grad): dy like y, rows behind the last used one
+    zero; dweights [tokens, top] float32, 0 where there is no row.  The residual's gradient is
+    dout itself.  out: where dy goes."""
+    rows = y.shape[0]
+    tokens, top, width, device, out = _exchange(routing, y, out, rows, dout, routing.weights, routing.offsets)
+    if dout.shape != (tokens, width) or dout.dtype is not y.dtype:
+        raise ValueError("dout must be [tokens, width] of y's type")
+    _flat(routing.weights, _F32, (tokens, top), "weights")
+    dweights = torch.empty((tokens, top), dtype=_F32, device=y.device)
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(y.dtype), GEMM_F32, device, stream)
+    status = _LIB.gemm_combine_grad(plan.handle, tokens, top, rows, width, dout.data_ptr(),
+                                    _pitch(dout.shape, dout.stride(), "dout"), y.data_ptr(),
+                                    _pitch(y.shape, y.stride(), "y"), routing.slots.data_ptr(), _used(routing),
+                                    routing.weights.data_ptr(), out.data_ptr(),
+                                    _pitch(out.shape, out.stride(), "out"), dweights.data_ptr(), stream)
+    if status:
+        raise GemmError(status, "gemm_combine_grad")
+    return out, dweights
+
+
+# ------------------------------ clipping ------------------------------------
+
+def _fills(t) -> bool:
+    """Do the tensor's entries fill a stretch of memory, in any order of its dimensions?"""
+    if t.is_contiguous():
+        return True
+    need = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size == 1:
+            continue
+        if stride != need:
+            return False
+        need *= size
+    return True
+
+
+class TensorList:
+    """Tensors whose global norm is taken and that are scaled together, laid out once: the
+    gradients that a program keeps from step to step.  out: where the scaled values go, tensors
+    of the same shapes and strides and any of the types (None: in place)."""
+
+    def __init__(self, tensors, out=None):
+        self.tensors, self.out = list(tensors), list(out) if out is not None else None
+        to = self.tensors if self.out is None else self.out
+        if len(to) != len(self.tensors):
+            raise ValueError("out must have a tensor for each")
+        self.table = (gemm_tensor_t * max(1, len(to)))()
+        spans = []
+        for i, (t, o) in enumerate(zip(self.tensors, to)):
+            if not _fills(t):
+                raise ValueError("tensors must fill their memory (no gaps between their entries)")
+            if o is not t and (o.shape != t.shape or o.stride() != t.stride()):
+                raise ValueError("out must have the tensors' shapes and strides")
+            n = t.numel()
+            self.table[i] = gemm_tensor_t(t.data_ptr(), o.data_ptr(), n, _code(t.dtype), _code(o.dtype))
+            if n:
+                spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(), i, self.out is None))
+                if o is not t:
+                    spans.append((o.data_ptr(), o.data_ptr() + n * o.element_size(), i, True))
+        spans.sort()
+        end, written_end = 0, 0   # of all spans so far, and of those that are written
+        for lo, hi, i, written in spans:
+            if lo < (end if written else written_end):
+                raise ValueError("tensors overlap")
+            end = max(end, hi)
+            written_end = max(written_end, hi) if written else written_end
+        self.device = _device(*self.tensors, *(self.out or ())) if self.tensors else None
+
+
+def _norm_of(tensors, max_norm: float, eps: float, scales: bool, plan, stream):
+    if not isinstance(tensors, TensorList):
+        tensors = TensorList(tensors)
+    if not max_norm >= 0 or not 0 <= eps < math.inf:
+        raise ValueError("max_norm and eps must not be negative, and eps finite")
+    device = tensors.device
+    if device is None:
+        device = plan.device if plan is not None else torch.cuda.current_device()
+    norm = torch.empty((), dtype=_F32, device=f"cuda:{device}")
+    stream = _raw_stream(device) if stream is None else stream
+    if plan is None:
+        plan = _plan_for(None, GEMM_F32, GEMM_F32, device, stream)
+    elif plan.device != device:
+        raise ValueError("the plan is on another device")
+    table, n = tensors.table, len(tensors.tensors)
+    if not scales:
+        table = (gemm_tensor_t * max(1, n))(*[gemm_tensor_t(e.src, None, e.count, e.src_type, e.src_type)
+                                              for e in table[:n]])
+    status = _LIB.gemm_clip_norm(plan.handle, n, table, max_norm, eps, norm.data_ptr(), stream)
+    if status:
+        raise GemmError(status, "gemm_clip_norm")
+    return norm
+
+
+def clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, plan: Optional[Plan] = None, stream=None):
+    """Scales tensors by min(1, max_norm / (norm + eps)) of their global norm (gemm_clip_norm) and
+    returns the norm, a float32 scalar on the device.  A norm that is not finite leaves the
+    values as they are, so that the step can be skipped.
+
+    tensors: a list of float32, float16 and bfloat16 tensors (scaled in place) or a TensorList,
+    which may send the scaled values elsewhere and in another type.  None may overlap another.
+    The plan may be of any type."""
+    return _norm_of(tensors, max_norm, eps, True, plan, stream)
+
+
+def grad_norm(tensors, *, plan: Optional[Plan] = None, stream=None):
+    """The global norm of a list of tensors or a TensorList, a float32 scalar on the device."""
+    return _norm_of(tensors, math.inf, 0.0, False, plan, stream)

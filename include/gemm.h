@@ -611,6 +611,113 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
                                  void* D, int64_t ldd, int64_t stride_d, gemm_dtype_t out_dtype,
                                  gemm_stream_t stream);
 
+/* ===========================================================================
+ * Around the products: routing of tokens to experts, the exchange of rows between
+ * tokens and experts, and gradients clipped by their global norm.  No page has a
+ * counterpart; they are what an expert layer needs beside its products.  They use
+ * the plan's device, error word and scratch as the others do and are asynchronous
+ * on `stream`.  No atomics decide an order: equal inputs give equal bits.
+ * ======================================================================== */
+
+/* In PyTorch terms: route, route_grad, dispatch, dispatch_grad, combine, combine_grad and
+ * clip_grad_norm of the Python package. */
+
+/* A routing of `tokens` tokens.  All pointers are device memory. */
+typedef struct {
+    float* weights;     /* tokens x top: what each chosen expert's row is added with */
+    int32_t* experts;   /* tokens x top: the chosen experts, best first; -1 behind the last one */
+    int32_t* slots;     /* tokens x top: the place of each (token, expert) among the sorted rows; -1 */
+    int32_t* counts;    /* experts: rows of each */
+    int32_t* offsets;   /* experts + 1: where each one's rows begin, as gemm_run_grouped takes it */
+    int32_t* routed;    /* 1: tokens that have any expert */
+    float* loss;        /* 1: the balance loss; NULL: not wanted */
+    int32_t top;        /* experts per token, 1 .. 32 */
+    int32_t renormalize;/* nonzero: a token's weights add up to 1 */
+} gemm_routing_t;
+
+/* ---------------------------------------------------------------------------
+ * gemm_route -- from a router's logits z (tokens x experts, row-major, the plan's
+ * ab_dtype) to rows sorted by expert:
+ *     p = softmax(z);  the experts of a token are its `top` largest z, the lower index
+ *     first where they are equal (NaN counts as the largest);  an expert whose z is
+ *     -infinity is not taken, so a token may get fewer, or none;
+ *     weights = p at them, or (renormalize) p at them over their sum; 0 behind the last;
+ *     rows are numbered by expert, then by token, then by choice;
+ *     loss = experts / (rows * routed) * sum_e counts[e] * sum_t p[t, e]  (0 without rows),
+ *     which is 1 for an even routing; the sum runs over the tokens that have any expert.
+ *   mask        tokens bytes, 0: the token gets no expert and counts nowhere; NULL: all do.
+ *   experts     1 .. 1024, tokens * top < 2^31 (else GEMM_ERR_UNSUPPORTED).
+ * Softmax and sums are fp32, the loss's last sums fp64.
+ * ------------------------------------------------------------------------- */
+gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ld,
+                         const uint8_t* mask, const gemm_routing_t* routing, gemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gemm_route_grad -- the gradient of a routing's weights and loss by its logits:
+ *     dlogits = sum_j dweights[t, j] dweights_j/dz + dloss_scale * (*dloss) * dloss/dz
+ * in the logits' type; the choice and the counts are constants.  Reads the routing's
+ * weights, experts, counts, offsets and routed (not its slots and loss).
+ *   dweights    tokens x top fp32 (entries of no expert are not read); NULL: none.
+ *   dloss       device fp32 scalar; NULL: 1.
+ * A token without experts has the gradient 0.  dlogits may be the logits themselves.
+ * ------------------------------------------------------------------------- */
+gemm_status_t gemm_route_grad(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ld,
+                              const gemm_routing_t* routing, const float* dweights, double dloss_scale,
+                              const float* dloss, void* dlogits, int64_t ldd, gemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gemm_dispatch, gemm_combine, gemm_combine_grad -- rows of `width` entries of the plan's
+ * ab_dtype (F32, F16 or BF16) between tokens and the buffer of `rows` sorted rows:
+ *     dispatch       D[slots[t, j], :] = X[t, :]
+ *     combine        D[t, :] = residual[t, :] + sum_j weights[t, j] * Y[slots[t, j], :]
+ *     combine_grad   dY[slots[t, j], :] = weights[t, j] * dout[t, :],
+ *                    dweights[t, j] = sum_c dout[t, c] * Y[slots[t, j], c]   (fp32)
+ * The gradient of dispatch is combine without weights and residual.  Sums are fp32 and
+ * rounded once.  weights NULL: 1; residual NULL: 0.
+ *   slots       tokens x top (top 1 .. 32), no row twice; outside 0 .. rows - 1 there is no row
+ *               (dweights 0), and where it is not -1 either gemm_plan_device_status reports
+ *               GEMM_ERR_INVALID_ARG.
+ *   used        device: rows in use (offsets + experts of a routing); rows from there on are
+ *               written as zeros by dispatch and combine_grad.  NULL: all are in use; a row
+ *               that no slot names is then left as it is.
+ * D must not overlap the inputs, but combine's D may be its residual.
+ * ------------------------------------------------------------------------- */
+gemm_status_t gemm_dispatch(gemm_plan_t plan, int64_t tokens, int64_t top, int64_t rows, int64_t width, const void* X,
+                            int64_t ldx, const int32_t* slots, const int32_t* used, void* D, int64_t ldd,
+                            gemm_stream_t stream);
+gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top, int64_t rows, int64_t width, const void* Y,
+                           int64_t ldy, const int32_t* slots, const float* weights, const void* residual, int64_t ldr,
+                           void* D, int64_t ldd, gemm_stream_t stream);
+gemm_status_t gemm_combine_grad(gemm_plan_t plan, int64_t tokens, int64_t top, int64_t rows, int64_t width,
+                                const void* dout, int64_t ldo, const void* Y, int64_t ldy, const int32_t* slots,
+                                const int32_t* used, const float* weights, void* dY, int64_t lddy, float* dweights,
+                                gemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gemm_clip_norm -- the global norm of a list of tensors, and the tensors scaled by it:
+ *     *norm = sqrt(sum over all entries of src^2),
+ *     dst = src * min(1, max_norm / (*norm + eps)).
+ *   tensors     host array, read during the call; each entry `count` consecutive entries of
+ *               src_type F32, F16 or BF16 at any address that suits the type.  dst NULL: the
+ *               tensor only counts; dst == src (of the same type): in place, and not touched
+ *               when the factor is 1; else a cast copy.  No dst may overlap another entry's
+ *               src or dst.  At most 2^20 tensors (else GEMM_ERR_UNSUPPORTED).
+ *   max_norm    >= 0; infinity: the factor is 1.      eps   >= 0, finite.
+ *   norm        device fp32 scalar.
+ * Any plan on the device serves (its types are not used).  Squares are added in fp32 over 32
+ * entries and in fp64 beyond; entries of any finite size count.  A norm that is not finite in
+ * fp32 (NaN or infinity among the entries, or a norm past 2^128) gives the factor 1, so that the caller can skip the step.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const void* src;
+    void* dst;
+    int64_t count;
+    gemm_dtype_t src_type, dst_type;
+} gemm_tensor_t;
+
+gemm_status_t gemm_clip_norm(gemm_plan_t plan, int64_t count, const gemm_tensor_t* tensors, double max_norm, double eps,
+                             float* norm, gemm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,80 @@
+"""Plain 64-bit forms of the operators around the products, and the bounds their tests use.
+
+A result rounded once to its type is off by at most U[type] of its value (half a step).  A
+sum of n fp32 terms in any order loses at most n 2^-24 of the sum of their absolute values.
+expf is within 2 steps (2^-22), and the rounding of its argument x adds |x| 2^-24.
+"""
+import math
+
+import torch
+
+from expert_helpers import DT, TINY, U  # noqa: F401  (shared with the tests)
+
+EPS = 2.0 ** -23
+
+
+def within(got, ref, tol, what=""):
+    """|got - ref| <= tol, entry by entry; NaN and infinities have to be the same."""
+    got, ref = got.double(), ref.double()
+    same = (got.isnan() & ref.isnan()) | (got == ref)
+    bad = ~(same | ((got - ref).abs() <= tol))
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} outside the bound, first at "
+                           f"{bad.nonzero()[0].tolist()}: {got[bad][0]} for {ref[bad][0]}")
+
+
+def route_ref(logits, top, renormalize=True, mask=None):
+    """The routing in 64 bits, choice by choice: (weights, experts, slots, counts, offsets, routed, loss, p, spread)."""
+    z = logits.double().cpu()
+    T, E = z.shape
+    order = torch.where(z.isnan(), math.inf, z)
+    nan = z.isnan()
+    experts = torch.full((T, top), -1, dtype=torch.long)
+    for t in range(T):
+        if mask is not None and not bool(mask[t]):
+            continue
+        ranked = sorted((e for e in range(E) if order[t, e] != -math.inf),
+                        key=lambda e: (not bool(nan[t, e]), -float(order[t, e]), e))[:top]
+        experts[t, :len(ranked)] = torch.tensor(ranked, dtype=torch.long)
+    chosen = experts >= 0
+    any_ = chosen[:, :1]
+    p = torch.where(any_, torch.softmax(torch.where(any_, z, 0.0), 1), 0.0)
+    w = torch.where(chosen, p.gather(1, experts.clamp(min=0)), 0.0)
+    if renormalize:
+        w = torch.where(chosen, w / w.sum(1, keepdim=True), 0.0)
+    counts = torch.bincount(experts[chosen], minlength=E)
+    offsets = torch.cat((torch.zeros(1, dtype=torch.long), counts.cumsum(0)))
+    slots = torch.full((T, top), -1, dtype=torch.long)
+    flat = experts.flatten()
+    at = offsets[:-1].clone()
+    for i in range(flat.numel()):
+        e = int(flat[i])
+        if e >= 0:
+            slots.view(-1)[i] = at[e]
+            at[e] += 1
+    rows, routed = int(counts.sum()), int(any_.sum())
+    loss = E * (counts * p.sum(0)).sum() / max(1, rows * routed) if rows else torch.tensor(0.0, dtype=torch.float64)
+    finite = torch.where(torch.isfinite(z), z, 0.0)
+    spread = (finite.amax(1) - finite.amin(1)).max() if T else 0.0
+    return w, experts, slots, counts, offsets, routed, loss, p, float(spread)
+
+
+def route_grad_ref(logits, top, dweights, dloss, renormalize=True, mask=None):
+    """(the gradient in 64 bits, the sum of the absolute values of its terms)."""
+    w, experts, _, counts, _, routed, _, p, spread = route_ref(logits, top, renormalize, mask)
+    T, E = p.shape
+    rows = int(counts.sum())
+    chosen = experts >= 0
+    dw = torch.where(chosen, dweights.double().cpu(), 0.0) if dweights is not None else torch.zeros(T, top, dtype=torch.float64)
+    g = (dloss * E * counts / max(1, rows * routed)).expand(T, E).double()
+    at = experts.clamp(min=0)
+    direct = torch.zeros_like(p)
+    mag = torch.zeros_like(p)
+    if renormalize:
+        direct.scatter_add_(1, at, w * (dw - (w * dw).sum(1, keepdim=True)))
+        mag.scatter_add_(1, at, w * (dw.abs() + (w * dw).abs().sum(1, keepdim=True)))
+    else:
+        g = g.clone().scatter_add_(1, at, dw)
+    ga = g.abs()
+    any_ = chosen[:, :1]
+    ref = torch.where(any_, direct + p * (g - (p * g).sum(1, keepdim=True)), 0.0)
+    return ref, mag + p * (ga + (p * ga).sum(1, keepdim=True)), spread

@@ -25,6 +25,7 @@ GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_ALIGNMENT, GEMM_ER
 GEMM_OP_N, GEMM_OP_T = 0, 1
 GEMM_F32, GEMM_F16, GEMM_BF16, GEMM_S8, GEMM_S32 = range(5)
 GEMM_ACT_NONE, GEMM_ACT_RELU = 0, 1
+GEMM_LINEAR_NONE, GEMM_LINEAR_RELU, GEMM_LINEAR_GELU, GEMM_LINEAR_GELU_TANH, GEMM_LINEAR_SILU = range(5)
 GEMM_BIAS_NONE, GEMM_BIAS_COL, GEMM_BIAS_ROW = 0, 1, 2
 (GEMM_KERNEL_AUTO, GEMM_KERNEL_NONE, GEMM_KERNEL_TC, GEMM_KERNEL_TC_INT8, GEMM_KERNEL_FFMA,
  GEMM_KERNEL_SIMT, GEMM_KERNEL_TC_PAIR, GEMM_KERNEL_DIAG) = range(8)
@@ -44,7 +45,8 @@ EXPORTED = ["gemm_plan_create", "gemm_plan_destroy", "gemm_run", "gemm_run_host"
             "gemm_run_s8_noalloc", "gemm_noalloc_device_status", "gemm_noalloc_set_timeout",
             "gemm_run_strided_batched", "gemm_run_diag", "gemm_run_complex",
             "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_run_q4", "gemm_orthogonalize",
-            "gemm_route", "gemm_route_grad", "gemm_dispatch", "gemm_combine", "gemm_combine_grad", "gemm_clip_norm"]
+            "gemm_run_linear", "gemm_run_linear_grad", "gemm_route", "gemm_route_grad", "gemm_dispatch", "gemm_combine",
+            "gemm_combine_grad", "gemm_clip_norm"]
 
 
 GEMM_XF_A, GEMM_XF_B = 1, 2
@@ -63,6 +65,12 @@ class gemm_q4_t(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("scale_dtype", ctypes.c_int), ("ld_scales", ctypes.c_int64),
                 ("stride_scales", ctypes.c_int64), ("zeros", ctypes.c_void_p), ("ld_zeros", ctypes.c_int64),
                 ("stride_zeros", ctypes.c_int64), ("group_size", ctypes.c_int64)]
+
+
+class gemm_linear_t(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("bias_dtype", ctypes.c_int), ("act", ctypes.c_int),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("pre", ctypes.c_void_p),
+                ("ld_pre", ctypes.c_int64), ("out_dtype", ctypes.c_int)]
 
 
 class gemm_routing_t(ctypes.Structure):
@@ -143,6 +151,9 @@ def load_library(path: str = LIB_PATH):
                                 epi_p, i64, vp]
     lib.gemm_orthogonalize.argtypes = [vp, i64, i64, i64, ci, ctypes.POINTER(dbl), dbl, vp, i64, i64, vp, i64,
                                        i64, ci, vp]
+    lib.gemm_run_linear.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, i64, vp, i64, ctypes.POINTER(gemm_linear_t), vp]
+    lib.gemm_run_linear_grad.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, i64, vp, i64, vp, i64,
+                                         ci, vp, vp]
     route_p = ctypes.POINTER(gemm_routing_t)
     lib.gemm_route.argtypes = [vp, i64, i64, vp, i64, vp, route_p, vp]
     lib.gemm_route_grad.argtypes = [vp, i64, i64, vp, i64, route_p, vp, dbl, vp, vp, i64, vp]
@@ -429,7 +440,7 @@ def matmul(a, b, *, c=None, alpha: float = 1.0, beta: float = 0.0, bias=None,
 
 _LAZY = {n: "expert" for n in ("grouped_matmul", "grouped_weight_grad", "quantize_q4", "q4_matmul", "orthogonalize",
                                "default_plan_status")}
-_LAZY.update({n: "layers" for n in ("Routing", "route", "route_grad", "dispatch", "dispatch_grad", "combine",
+_LAZY.update({n: "layers" for n in ("linear", "linear_grad", "Routing", "route", "route_grad", "dispatch", "dispatch_grad", "combine",
                                     "combine_grad", "TensorList", "clip_grad_norm", "grad_norm")})
 
 

@@ -19,8 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemm.so")
 SOURCES = ["gemm_api.cu", "tc_kernel.cu", "tc2_kernel.cu", "simt_kernels.cu", "diag_kernel.cu",
            "pair_kernel.cu", "expert_api.cu", "q4_kernel.cu", "repitch_kernel.cu", "ortho_kernels.cu", "seg_kernel.cu",
-           "layer_api.cu", "route_kernels.cu", "exchange_kernels.cu", "clip_kernels.cu"]
-HEADERS = ["common.cuh", "kernels.h", "plan.h", "expert.h", "layer.h"]
+           "layer_api.cu", "linear_kernel.cu", "route_kernels.cu", "exchange_kernels.cu", "clip_kernels.cu"]
+HEADERS = ["common.cuh", "kernels.h", "plan.h", "activation.cuh", "expert.h", "operands.h", "layer.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -2,6 +2,7 @@
 // expert, products with 4-bit weights, orthogonalised updates (internal).
 #pragma once
 
+#include "activation.cuh"
 #include "kernels.h"
 
 namespace gemmlib {
@@ -75,7 +76,16 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* tm) {
 #endif
 
 // What seg_kernel.cu computes (its head says how).
-enum { SEG_TOKENS = 0, SEG_WGRAD = 1, SEG_CHAIN = 2 };
+enum { SEG_TOKENS = 0, SEG_WGRAD = 1, SEG_CHAIN = 2, SEG_LINEAR = 3 };
+// What a fully connected layer does behind its product, beside EpiParams' bias and output:
+// z = acc + bias is stored in `pre`, and D = act(z) + residual.  Both of D's type, or null.
+struct LinearEpilogue {
+  const void* residual;
+  void* pre;
+  int64_t ldr, ldp;
+  int32_t act;
+  int32_t vec_p;   // pre's rows may be written with 16-byte vectors
+};
 // CHAIN's maps in tmB, beside E as M side in tmA: both X buffers as M side of E, as N side
 // of E, as N side of F X; F as M side; E as N side.
 enum { CHAIN_XK = 0, CHAIN_XB = 2, CHAIN_XN = 4, CHAIN_F = 6, CHAIN_EB = 7, SEG_MAPS = 8 };
@@ -109,6 +119,7 @@ struct SegParams {
     float a[2], b[2], c;        // early steps, the last two (see gemm_orthogonalize)
     float inv_x, scale_e, inv_e;   // X is held times 1 / inv_x, E and F times scale_e = 1 / inv_e
   } chain;
+  LinearEpilogue linear;        // LINEAR
   EpiParams epi;
   int32_t* err;
   uint64_t timeout_ns;

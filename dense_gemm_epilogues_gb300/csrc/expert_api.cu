@@ -5,7 +5,7 @@
 #include <cstring>
 
 #include "expert.h"
-#include "plan.h"
+#include "operands.h"
 
 using namespace gemmlib;
 
@@ -39,32 +39,6 @@ EpiParams epilogue_of(const gemm_epilogue_t* epi, gemm_dtype_t out, double alpha
   return e;
 }
 
-// A 16-bit operand as TMA can read it: itself, or a copy with another pitch in scratch.
-struct Operand {
-  const void* p;
-  int64_t ld, stride;
-};
-
-bool addressable(const Operand& x, int64_t batch) {
-  return tma_ok(x.p, x.ld, 2) && (batch <= 1 || x.stride % 8 == 0);
-}
-
-// Scratch bytes of the copy of `batch` rows x cols matrices (0: none needed).
-size_t repitch_bytes(const Operand& x, int64_t rows, int64_t cols, int64_t batch) {
-  return addressable(x, batch) ? 0 : align_up((size_t)(batch * rows * ((cols + 7) / 8 * 8)) * 2, 256);
-}
-
-gemm_status_t repitch(Operand* x, int64_t rows, int64_t cols, int64_t batch, const int32_t* offsets, char* to,
-                      cudaStream_t stream) {
-  if (addressable(*x, batch)) return GEMM_OK;
-  const int64_t ld = (cols + 7) / 8 * 8;
-  if (launch_repitch(x->p, x->ld, x->stride, to, ld, rows * ld, rows, cols, batch, offsets, 2, stream) !=
-      cudaSuccess)
-    return GEMM_ERR_CUDA;
-  *x = Operand{to, ld, batch > 1 ? rows * ld : 0};
-  return GEMM_OK;
-}
-
 // Are 4-bit weights decoded once into scratch and multiplied on the tensor-core kernel,
 // rather than inside the product, once per 32 rows?  Up to 32 rows never (one pass over
 // the weights, exact integers).  Beyond, by the times that both take, in us: a pass inside
@@ -85,38 +59,6 @@ bool q4_decode_once(int64_t N, int64_t K, int64_t rows, int64_t groups, int sm_c
   const double inside = (3.0 + 0.4 * millions) * (double)((rows + 31) / 32);
   const double once = 0.38 * millions + 0.45 * (double)((K + 127) / 128) * (double)waves + 3.0;
   return once < inside;
-}
-
-int workers_of(const gemm_plan* plan, int cg, int64_t tiles) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(tiles, cg == 2 ? plan->pair_clusters : plan->sm_count));
-}
-
-CUtensorMapDataType map_type(gemm_dtype_t t) {
-  return t == GEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-}
-
-constexpr int64_t kMaxTiles = int64_t(1) << 28;   // tile numbers are 32-bit
-
-// What gemm_plan_last_config reports for a product on seg_kernel.
-gemm_config_t seg_config(int cg, int64_t tiles, int workers) {
-  gemm_config_t c{};
-  c.kernel = cg == 2 ? GEMM_KERNEL_TC_PAIR : GEMM_KERNEL_TC;
-  c.bm = c.bn = 128 * cg;
-  c.bk = 2 * TC_BK;
-  c.stages = 3;
-  c.cta_group = c.cluster = cg;
-  c.split_k = 1;
-  c.raster = 8;
-  c.grid = workers * cg;
-  c.tiles = (int32_t)tiles;
-  return c;
-}
-
-// A call that launches nothing.
-gemm_status_t nothing(gemm_plan* plan) {
-  plan->last = gemm_config_t{};
-  plan->last.kernel = GEMM_KERNEL_NONE;
-  return GEMM_OK;
 }
 
 // D[r, :] = epilogue(x[r, :] * W_g) on seg_kernel: x M x K row-major, W_g K x N (w_mn: N
@@ -162,12 +104,6 @@ gemm_status_t tokens_product(gemm_plan* plan, const Groups& groups, int64_t M, i
   plan->last = seg_config(cg, tiles, workers);
   log_config(entry, M, N, K, groups.count, plan->last);
   return GEMM_OK;
-}
-
-bool too_large(std::initializer_list<int64_t> dims) {
-  for (int64_t d : dims)
-    if (d > kMaxDim - 512) return true;   // tile edges past a size stay within 32 bits
-  return false;
 }
 
 }  // namespace

@@ -6,6 +6,39 @@
 
 namespace gemmlib {
 
+// ---- fully connected layers (linear_kernel.cu; products of many tiles: seg_kernel.cu) ----
+constexpr int SPLIT_SMEM = 112 * 1024;   // of a CTA: two on an SM
+struct LinearSplitParams {
+  CUtensorMap tmW;           // weights: boxes of 64 k x 128 columns of D, or 64 columns x 64 k
+  CUtensorMap tmX;           // rows: boxes of 64 k x box_rows
+  int64_t rows, K, epi_n;    // epi_n: columns of D
+  int32_t box_rows;          // rows of a tile: 16, 32, 64 or 128
+  int32_t stages;            // split_stages(box_rows)
+  int32_t vec;               // D, pre and residual can be accessed four entries at a time
+  uint32_t idesc;            // instruction descriptor without N
+  LinearEpilogue linear;
+  EpiParams epi;             // bias and D
+  int32_t* err;
+  uint64_t timeout_ns;
+};
+int split_stages(int box_rows);
+// splits: CTAs that share a tile's K, 1 .. 8 and at most ceil(K / 64).
+cudaError_t launch_linear_split(const LinearSplitParams& p, bool a_mn, int splits, cudaStream_t stream);
+
+// dz = dy act'(pre) (16-bit types, rows of dz padded to whole 16 bytes), and the sums of dz's
+// columns over blocks of rows.  No activation: only the sums, of dy.
+struct ActGradParams {
+  const void *dy, *pre;
+  void* dz;
+  int64_t M, N, ldy, ldp, ldz;
+  int64_t block_rows;
+  int32_t act;
+  int32_t vec;               // rows of dy and pre can be read 16 bytes at a time
+  float* partials;           // blocks x N, or null
+};
+cudaError_t launch_act_grad(const ActGradParams& p, int dtype, int blocks, cudaStream_t stream);
+cudaError_t launch_column_sums(const float* partials, int blocks, int64_t N, float* out, cudaStream_t stream);
+
 // ---- routing (route_kernels.cu) ----
 constexpr int kMaxTop = 32;   // experts of one token
 struct RouteParams {

@@ -4,7 +4,7 @@
 #include <cstring>
 
 #include "layer.h"
-#include "plan.h"
+#include "operands.h"
 
 using namespace gemmlib;
 
@@ -64,9 +64,239 @@ gemm_status_t exchange_of(const gemm_plan* plan, int64_t tokens, int64_t top, in
   return GEMM_OK;
 }
 
+// ------------------------------ fully connected layers ------------------------------
+
+gemm_status_t check_linear(const gemm_plan* plan, gemm_layout_t lb, int64_t M, int64_t N, int64_t K) {
+  if (!is_f16ish(plan->ab)) return GEMM_ERR_UNSUPPORTED;
+  if ((lb != GEMM_OP_N && lb != GEMM_OP_T) || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  if (too_large({M, N, K})) return GEMM_ERR_UNSUPPORTED;
+  return GEMM_OK;
+}
+
+// How many CTAs share a tile's K on linear_split_kernel (0: the product runs on seg_kernel).
+int splits_of(int64_t M, int64_t N, int64_t K, int box_rows, int sm_count) {
+  const int64_t num_kb = (K + TC_BK - 1) / TC_BK;
+  const int64_t tiles = (N + 127) / 128 * ((M + box_rows - 1) / box_rows);
+  if (num_kb == 0 || tiles > sm_count) return 0;
+  const int64_t splits = std::min<int64_t>({8, num_kb, 2 * (int64_t)sm_count / tiles});
+  return splits >= 2 ? (int)splits : 0;
+}
+
+// D = act(x W + bias) + residual: x M x K row-major, W K x N (w_mn: N contiguous, else K);
+// TMA can address both.
+gemm_status_t linear_product(gemm_plan* plan, int64_t M, int64_t N, int64_t K, const Operand& x, const Operand& w,
+                             bool w_mn, const EpiParams& epi, const LinearEpilogue& lin, const char* entry,
+                             cudaStream_t stream) {
+  const CUtensorMapDataType dt = map_type(plan->ab);
+  const int box = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int splits = splits_of(M, N, K, box, plan->sm_count);
+  if (splits > 0) {
+    LinearSplitParams p;
+    std::memset(&p, 0, sizeof(p));
+    const bool ok = (w_mn ? encode_3d(&p.tmW, dt, w.p, N, K, w.ld, 1, 0, 64, TC_BK)
+                          : encode_3d(&p.tmW, dt, w.p, K, N, w.ld, 1, 0, TC_BK, 128)) &&
+                    encode_3d(&p.tmX, dt, x.p, K, M, x.ld, 1, 0, TC_BK, (uint32_t)box);
+    if (!ok) return GEMM_ERR_CUDA;
+    p.rows = M;
+    p.K = K;
+    p.epi_n = N;
+    p.box_rows = box;
+    p.stages = split_stages(box);
+    auto by_four = [&](const void* q, int64_t ld) {
+      return reinterpret_cast<uintptr_t>(q) % (4 * dtype_bytes(epi.d_dtype)) == 0 && ld % 4 == 0;
+    };
+    p.vec = by_four(epi.D, epi.ldd) && (!lin.pre || by_four(lin.pre, lin.ldp)) &&
+                    (!lin.residual || by_four(lin.residual, lin.ldr))
+                ? 1
+                : 0;
+    p.idesc = make_idesc(plan->ab == GEMM_BF16, 0, w_mn, false, 128);
+    p.linear = lin;
+    p.epi = epi;
+    p.err = plan->d_err;
+    p.timeout_ns = plan->timeout_ns;
+    if (launch_linear_split(p, w_mn, splits, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+    const int64_t tiles = (N + 127) / 128 * ((M + box - 1) / box);
+    gemm_config_t c = seg_config(1, tiles, (int)tiles * splits);
+    c.bn = box;
+    c.bk = TC_BK;
+    c.stages = p.stages;
+    c.split_k = splits;
+    c.cluster = splits;
+    plan->last = c;
+    log_config(entry, M, N, K, 1, plan->last);
+    return GEMM_OK;
+  }
+  SegParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int64_t tiles256 = (N + 255) / 256 * ((M + 255) / 256), tiles128 = (N + 127) / 128 * ((M + 127) / 128);
+  const bool fill = 4 * tiles256 >= 3 * plan->pair_clusters || tiles128 > plan->sm_count;
+  const int cg = plan->pair_clusters > 0 && M >= 128 && fill ? 2 : 1;
+  const int64_t tiles = cg == 2 ? tiles256 : tiles128;
+  if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
+  if (K > 0) {
+    bool ok = w_mn ? encode_3d(&p.tmA, dt, w.p, N, K, w.ld, 1, 0, 64, 2 * TC_BK)
+                   : encode_3d(&p.tmA, dt, w.p, K, N, w.ld, 1, 0, TC_BK, 128);
+    for (int b = 0; b < 5; ++b) ok = ok && encode_3d(&p.tmB[b], dt, x.p, K, M, x.ld, 1, 0, TC_BK, 128u >> b);
+    if (!ok) return GEMM_ERR_CUDA;
+  }
+  p.groups = Groups{nullptr, 1, (int32_t)M, plan->d_err};
+  p.M = N;
+  p.K = (int32_t)K;
+  p.tiles_m = (int32_t)((N + 128 * cg - 1) / (128 * cg));
+  p.idesc = make_idesc(plan->ab == GEMM_BF16, 0, w_mn, false, 128 * cg);
+  p.epi = epi;
+  p.linear = lin;
+  p.err = plan->d_err;
+  p.timeout_ns = plan->timeout_ns;
+  const int workers = workers_of(plan, cg, tiles);
+  if (launch_seg(p, SEG_LINEAR, cg, w_mn, workers, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  plan->last = seg_config(cg, tiles, workers);
+  log_config(entry, M, N, K, 1, plan->last);
+  return GEMM_OK;
+}
+
+EpiParams plain_epilogue(void* D, int64_t ldd, gemm_dtype_t type) {
+  EpiParams e{};
+  e.alpha = 1.0f;
+  e.D = D;
+  e.ldd = ldd;
+  e.d_dtype = type;
+  e.bias_dtype = GEMM_F32;
+  e.out_scale = 1.0f;
+  e.vec_d = wide_rows(D, ldd, dtype_bytes(type)) ? 1 : 0;
+  return e;
+}
+
 }  // namespace
 
 extern "C" {
+
+gemm_status_t gemm_run_linear(gemm_plan_t plan, gemm_layout_t lb, int64_t M, int64_t N, int64_t K, const void* A,
+                              int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd, const gemm_linear_t* epi,
+                              gemm_stream_t stream_) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  NvtxRange range("gemm_run_linear");
+  gemm_status_t s = check_linear(plan, lb, M, N, K);
+  if (s != GEMM_OK) return s;
+  const gemm_dtype_t out = epi ? epi->out_dtype : plan->ab;
+  if (!is_type(out) || (epi && (epi->act < GEMM_LINEAR_NONE || epi->act > GEMM_LINEAR_SILU))) return GEMM_ERR_INVALID_ARG;
+  if (epi && epi->bias && !is_type(epi->bias_dtype)) return GEMM_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return nothing(plan);
+  if (!D || ldd < N) return GEMM_ERR_INVALID_ARG;
+  if (epi && ((epi->residual && epi->ld_residual < N) || (epi->pre && epi->ld_pre < N))) return GEMM_ERR_INVALID_ARG;
+  if (K > 0 && (!A || !B || lda < K || ldb < (lb == GEMM_OP_N ? K : N))) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(plan->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  EpiParams e = plain_epilogue(D, ldd, out);
+  LinearEpilogue lin{};
+  if (epi) {
+    if (epi->bias) {
+      e.bias_mode = GEMM_BIAS_COL;
+      e.bias = epi->bias;
+      e.bias_dtype = epi->bias_dtype;
+    }
+    lin.residual = epi->residual;
+    lin.ldr = epi->ld_residual;
+    lin.pre = epi->pre;
+    lin.ldp = epi->ld_pre;
+    lin.act = epi->act;
+    lin.vec_p = epi->pre && wide_rows(epi->pre, epi->ld_pre, dtype_bytes(out)) ? 1 : 0;
+  }
+  Operand x{A, lda, 0}, w{B, ldb, 0};
+  const bool w_mn = lb == GEMM_OP_T;
+  if (K > 0) {   // operands that TMA cannot address are copied to a pitch it can
+    const int64_t wrows = w_mn ? K : N, wcols = w_mn ? N : K;
+    const size_t xb = repitch_bytes(x, M, K, 1), wb = repitch_bytes(w, wrows, wcols, 1);
+    if (xb + wb > 0) {
+      s = ensure_ws(plan, xb + wb, stream);
+      char* ws = static_cast<char*>(plan->ws.p);
+      if (s == GEMM_OK) s = repitch(&x, M, K, 1, nullptr, ws, stream);
+      if (s == GEMM_OK) s = repitch(&w, wrows, wcols, 1, nullptr, ws + xb, stream);
+      if (s != GEMM_OK) return s;
+    }
+  }
+  return linear_product(plan, M, N, K, x, w, w_mn, e, lin, "linear", stream);
+}
+
+gemm_status_t gemm_run_linear_grad(gemm_plan_t plan, gemm_layout_t lb, int64_t M, int64_t N, int64_t K, const void* dY,
+                                   int64_t lddy, const void* pre, int64_t ldp, gemm_linear_act_t act, const void* A,
+                                   int64_t lda, const void* B, int64_t ldb, void* dA, int64_t ldda, void* dB,
+                                   int64_t lddb, gemm_dtype_t db_dtype, float* dbias, gemm_stream_t stream_) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  NvtxRange range("gemm_run_linear_grad");
+  gemm_status_t s = check_linear(plan, lb, M, N, K);
+  if (s != GEMM_OK) return s;
+  if (act < GEMM_LINEAR_NONE || act > GEMM_LINEAR_SILU || (dB && !is_type(db_dtype))) return GEMM_ERR_INVALID_ARG;
+  const int64_t wld = lb == GEMM_OP_N ? K : N;
+  if (M > 0 && N > 0 && (!dY || lddy < N || (act != GEMM_LINEAR_NONE && (!pre || ldp < N)))) return GEMM_ERR_INVALID_ARG;
+  if (dA && (ldda < K || (N > 0 && K > 0 && (!B || ldb < wld)))) return GEMM_ERR_INVALID_ARG;
+  if (dB && (lddb < wld || (M > 0 && K > 0 && (!A || lda < K)))) return GEMM_ERR_INVALID_ARG;
+  const bool want_a = dA && M > 0 && K > 0, want_b = dB && N > 0 && K > 0, want_bias = dbias && N > 0;
+  if (!want_a && !want_b && !want_bias) return nothing(plan);
+  DeviceGuard g(plan->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const bool w_mn = lb == GEMM_OP_T, acts = act != GEMM_LINEAR_NONE && M > 0 && N > 0;
+  Operand dy{dY, lddy, 0}, x{A, lda, 0}, w{B, ldb, 0};
+  const int64_t wrows = w_mn ? K : N, wcols = w_mn ? N : K;
+  // dz (or dy at a pitch that TMA can address), x and w where they need a copy, partial sums.
+  const int64_t ldz = (N + 7) / 8 * 8;
+  const size_t zb = M == 0 || N == 0 ? 0 : acts ? align_up((size_t)(M * ldz) * 2, 256) : repitch_bytes(dy, M, N, 1);
+  const size_t xb = want_b && M > 0 ? repitch_bytes(x, M, K, 1) : 0;
+  const size_t wb = want_a && N > 0 ? repitch_bytes(w, wrows, wcols, 1) : 0;
+  // Blocks of rows: enough CTAs for eight per SM, at least 32 rows each.
+  const int64_t strips = (N + 255) / 256;
+  const int64_t want = std::max<int64_t>(1, 8 * (int64_t)plan->sm_count / std::max<int64_t>(1, strips));
+  const int64_t block_rows = std::max<int64_t>(32, (M + want - 1) / want);
+  const int blocks = (int)((M + block_rows - 1) / block_rows);
+  const size_t pb = want_bias ? (size_t)blocks * (size_t)N * sizeof(float) : 0;
+  if (zb + xb + wb + pb > 0) {
+    s = ensure_ws(plan, zb + xb + wb + pb, stream);
+    if (s != GEMM_OK) return s;
+  }
+  char* ws = static_cast<char*>(plan->ws.p);
+  float* partials = want_bias ? reinterpret_cast<float*>(ws + zb + xb + wb) : nullptr;
+  if (M > 0 && N > 0 && (acts || want_bias)) {
+    ActGradParams p{};
+    p.dy = dY;
+    p.pre = pre;
+    p.dz = acts ? ws : nullptr;
+    p.M = M;
+    p.N = N;
+    p.ldy = lddy;
+    p.ldp = ldp;
+    p.ldz = ldz;
+    p.block_rows = block_rows;
+    p.act = act;
+    p.vec = wide_rows(dY, lddy, 2) && (!acts || wide_rows(pre, ldp, 2)) ? 1 : 0;
+    p.partials = partials;
+    if (launch_act_grad(p, plan->ab, blocks, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  }
+  if (want_bias && launch_column_sums(partials, blocks, N, dbias, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (acts) dy = Operand{ws, ldz, 0};
+  else if (zb > 0) s = repitch(&dy, M, N, 1, nullptr, ws, stream);
+  if (s == GEMM_OK && xb > 0) s = repitch(&x, M, K, 1, nullptr, ws + zb, stream);
+  if (s == GEMM_OK && wb > 0) s = repitch(&w, wrows, wcols, 1, nullptr, ws + zb + xb, stream);
+  if (s != GEMM_OK) return s;
+  if (want_a) {   // dA = dz W': W' is N x K, N contiguous where W's K is
+    s = linear_product(plan, M, K, N, dy, w, !w_mn, plain_epilogue(dA, ldda, plan->ab), LinearEpilogue{}, "linear_grad",
+                       stream);
+    if (s != GEMM_OK) return s;
+  }
+  if (want_b) {   // dB = x' dz, or its transpose dz' x
+    gemm_epilogue_t e{};
+    e.out_dtype = db_dtype;
+    const gemm_kernel_t forced = plan->forced;
+    plan->forced = GEMM_KERNEL_AUTO;
+    s = w_mn ? gemm_run(plan, GEMM_OP_N, GEMM_OP_T, K, N, M, 1.0, x.p, std::max(x.ld, K), dy.p, std::max(dy.ld, N), 0.0,
+                        nullptr, 0, dB, lddb, &e, stream_)
+             : gemm_run(plan, GEMM_OP_N, GEMM_OP_T, N, K, M, 1.0, dy.p, std::max(dy.ld, N), x.p, std::max(x.ld, K), 0.0,
+                        nullptr, 0, dB, lddb, &e, stream_);
+    plan->forced = forced;
+  }
+  return s;
+}
 
 gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ld,
                          const uint8_t* mask, const gemm_routing_t* routing, gemm_stream_t stream_) {

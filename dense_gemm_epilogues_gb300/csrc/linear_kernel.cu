@@ -1,0 +1,397 @@
+// linear_kernel.cu -- fully connected layers where the product has few tiles, and the passes
+// around their gradients.
+//
+// linear_split_kernel: D = act(x W + b) + R for few rows (a decoding step, a short prompt).
+// Bound by memory: every weight is read once, so the weights have to stream at the chip's
+// rate, but 128 columns of D per CTA are 32 CTAs for a width of 4096.  So a cluster of up to
+// eight CTAs shares a tile's K: each streams its part of the depth with TMA through a ring
+// into one tensor-memory accumulator (weights on the M side, rows on the N side: the MMA's N
+// is the row count rounded up to 16), the partial sums go to shared memory, and after one
+// cluster barrier every CTA adds an equal share of the tile from all of them, in the order of
+// K, through distributed shared memory, and finishes it.  No scratch, no counters; two CTAs
+// per SM, so that one's start and end hide behind the other's stream.
+//
+// act_grad_kernel: dz = dy act'(z) in the operands' type, and its column sums (the bias's
+// gradient) from the unrounded values: one pass at memory speed; a column's sums are added
+// over row blocks by column_sums_kernel in one order.
+//
+// Every wait is bounded, as in tc_kernel.cu.
+#include "layer.h"
+
+namespace gemmlib {
+namespace {
+
+constexpr int THREADS = 192;                       // producer warp, MMA warp, four that read the accumulator
+constexpr int A_BYTES = 128 * TC_BK * 2;           // 16 KiB: 128 columns of weights, 64 deep
+constexpr uint32_t MN_BOX_BYTES = 64 * TC_BK * 2;  // MN-major box: 64 columns, 64 deep
+constexpr int MAX_STAGES = 8;
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t user_timeout_ns) {
+  const uint64_t timeout_ns = user_timeout_ns > 1000000000ull ? user_timeout_ns : 1000000000ull;
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > timeout_ns) return;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(one));
+  return one != 0;
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
+  const bool ok = mbar_wait(bar, parity, wc);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+__device__ __forceinline__ float4 lds_cluster(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// Four entries of a row (n of them exist) of a type.
+template <int DT>
+__device__ __forceinline__ void load4(const void* p, int64_t i, int n, bool vec, float (&x)[4]) {
+  if (vec && n >= 4) {
+    if constexpr (DT == GEMM_F32) {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+      const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (DT == GEMM_F16) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
+          x[2 * h] = f.x, x[2 * h + 1] = f.y;
+        } else {
+          x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = j < n ? load_as_float(p, DT, i + j) : 0.0f;
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store4(void* p, int64_t i, int n, bool vec, const float (&x)[4]) {
+  if (vec && n >= 4) {
+    if constexpr (DT == GEMM_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+      uint32_t w[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (DT == GEMM_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
+        else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(w[0], w[1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) store_float_as(p, DT, i + j, x[j]);
+  }
+}
+
+// Grid: (splits, column tiles, row tiles); a cluster is the splits of one tile.
+template <bool A_MN>
+__global__ void __launch_bounds__(THREADS) linear_split_kernel(const __grid_constant__ LinearSplitParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;   // the same offset in all CTAs of the cluster
+  const uint32_t b_bytes = (uint32_t)(p.box_rows * TC_BK * 2), stage_bytes = A_BYTES + b_bytes;
+  __shared__ uint64_t bars[2 * MAX_STAGES + 1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int32_t abort_word;
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(MAX_STAGES + s); };
+  const uint32_t done_bar = bar0 + 8u * (2 * MAX_STAGES);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int split = blockIdx.x, splits = gridDim.x;
+  const int64_t m0 = (int64_t)blockIdx.y * 128;                 // first column of D
+  const int64_t r0 = (int64_t)blockIdx.z * p.box_rows;          // first row
+  const int rows = (int)min((int64_t)p.box_rows, p.rows - r0);
+  const int n_mma = (rows + 15) & ~15;
+  const uint32_t tmem_cols = n_mma <= 32 ? 32u : n_mma <= 64 ? 64u : 128u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(done_bar, 1);
+    abort_word = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+  const WaitCtx wc{&abort_word, p.err, p.timeout_ns};
+  const int num_kb = (int)((p.K + TC_BK - 1) / TC_BK);
+  const int kb0 = (int)((int64_t)split * num_kb / splits), kb1 = (int)((int64_t)(split + 1) * num_kb / splits);
+
+  if (warp == 0) {
+    const bool one = elect_one();
+    if (one) {
+      tma_prefetch_desc(&p.tmW);
+      tma_prefetch_desc(&p.tmX);
+    }
+    int issued = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+      const int s = issued % p.stages;
+      if (!warp_wait(empty_bar(s), ((uint32_t)(issued / p.stages) & 1u) ^ 1u, wc)) break;
+      if (one) {
+        const uint32_t fb = full_bar(s), sa = base + (uint32_t)s * stage_bytes;
+        mbar_expect_tx(fb, stage_bytes);
+        if constexpr (A_MN) {
+          tma_load_3d(sa, &p.tmW, (int)m0, kb * TC_BK, 0, fb);
+          tma_load_3d(sa + MN_BOX_BYTES, &p.tmW, (int)m0 + 64, kb * TC_BK, 0, fb);
+        } else {
+          tma_load_3d(sa, &p.tmW, kb * TC_BK, (int)m0, 0, fb);
+        }
+        tma_load_3d(sa + A_BYTES, &p.tmX, kb * TC_BK, (int)r0, 0, fb);
+      }
+      __syncwarp();
+    }
+    // Every copy has landed before the ring is written below.
+    if (one)
+      for (int i = max(0, issued - p.stages); i < issued; ++i)
+        drain_wait(full_bar(i % p.stages), (uint32_t)(i / p.stages) & 1u, p.timeout_ns);
+    __syncwarp();
+  } else if (warp == 1) {
+    const bool one = elect_one();
+    const uint32_t idesc = p.idesc | ((uint32_t)(n_mma >> 3) << 17);
+    for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+      const int s = i % p.stages;
+      if (!warp_wait(full_bar(s), (uint32_t)(i / p.stages) & 1u, wc)) break;
+      tc_fence_after();
+      if (one) {
+        const uint32_t sa = base + (uint32_t)s * stage_bytes;
+        const uint64_t ad = A_MN ? smem_desc_sw128(sa, MN_BOX_BYTES, 1024) : smem_desc_sw128(sa, 16, 1024);
+        const uint64_t bd = smem_desc_sw128(sa + A_BYTES, 16, 1024);
+#pragma unroll
+        for (int q = 0; q < TC_BK / 16; ++q)   // (past K both operands read as zero)
+          tc_mma_f16(tmem_base, ad + (A_MN ? q * 2048u >> 4 : q * 32u >> 4), bd + (q * 32u >> 4), idesc, i > 0 || q > 0 ? 1u : 0u);
+        tc_commit(empty_bar(s));
+      }
+      __syncwarp();
+    }
+    if (one) {
+      tc_commit(done_bar);
+      drain_wait(done_bar, 0, p.timeout_ns);
+    }
+    __syncwarp();
+  }
+  // All MMAs are complete (warp 1 has waited for them), all copies have landed: the ring is free.
+  __syncthreads();
+  tc_fence_after();
+  if (warp >= 2) {
+    const int q = warp & 3;
+    for (int c = 0; c < n_mma; c += 32) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (c + j < n_mma)   // [row][column of D]: a warp's lanes lie side by side
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (uint32_t)(((c + j) * 128 + q * 32 + lane) * 4)), "r"(r[j]) : "memory");
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync();
+  // Four columns of a row at a time; this CTA's share of the tile's.
+  const int items = rows * 32;
+  const int64_t left = p.epi_n - m0;   // columns of D
+  with_type(p.epi.d_dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    for (int i = split * items / splits + (int)threadIdx.x; i < (split + 1) * items / splits; i += THREADS) {
+      const int row = i >> 5, col = (i & 31) * 4;
+      const int n = (int)min((int64_t)4, left - col);
+      if (n <= 0) continue;
+      const uint32_t at = base + (uint32_t)((row * 128 + col) * 4);
+      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s) {
+        const float4 v = lds_cluster(mapa_shared(at, (uint32_t)s));
+        x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+      }
+      const int64_t d = m0 + col;
+      if (p.epi.bias_mode == GEMM_BIAS_COL) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < n) x[j] += load_as_float(p.epi.bias, p.epi.bias_dtype, d + j);
+      }
+      if (p.linear.pre != nullptr) store4<DT>(p.linear.pre, (r0 + row) * p.linear.ldp + d, n, p.vec, x);
+      with_act(p.linear.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = activate<decltype(act)::value>(x[j]);
+      });
+      if (p.linear.residual != nullptr) {
+        float r[4];
+        load4<DT>(p.linear.residual, (r0 + row) * p.linear.ldr + d, n, p.vec, r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] += r[j];
+      }
+      store4<DT>(p.epi.D, (r0 + row) * p.epi.ldd + d, n, p.vec, x);
+    }
+  });
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();   // no CTA leaves while another may read its shared memory
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, tmem_cols);
+}
+
+// ------------------------- the gradient's elementwise pass -------------------------
+
+constexpr int GRAD_THREADS = 256, GRAD_COLS = 256;   // a warp takes a row's 256 columns, eight per lane
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int n, bool vec, float (&x)[8]) {
+  if (vec && n >= 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if constexpr (DT == GEMM_F16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
+        x[2 * h] = f.x, x[2 * h + 1] = f.y;
+      } else {
+        x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = j < n ? load_as_float(p, DT, i + j) : 0.0f;
+  }
+}
+
+// Grid: (256-column strips, row blocks).
+template <int DT>
+__global__ void __launch_bounds__(GRAD_THREADS) act_grad_kernel(const __grid_constant__ ActGradParams p) {
+  __shared__ float sums[GRAD_THREADS / 32][GRAD_COLS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t c = (int64_t)blockIdx.x * GRAD_COLS + lane * 8;
+  const int n = (int)max((int64_t)0, min((int64_t)8, p.N - c));
+  const int64_t lo = (int64_t)blockIdx.y * p.block_rows, hi = min(p.M, lo + p.block_rows);
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  with_act(p.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    if (n > 0) {
+#pragma unroll 2
+      for (int64_t r = lo + warp; r < hi; r += GRAD_THREADS / 32) {
+        float dy[8];
+        load8<DT>(p.dy, r * p.ldy + c, n, p.vec, dy);
+        if constexpr (ACT != ACT_NONE) {
+          float z[8];
+          load8<DT>(p.pre, r * p.ldp + c, n, p.vec, z);
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dy[j] *= activate_grad<ACT>(z[j]);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {   // (dz's rows are padded to whole pieces; what lies past N is 0)
+            if constexpr (DT == GEMM_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(dy[2 * h + 1]), "f"(dy[2 * h]));
+            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(dy[2 * h + 1]), "f"(dy[2 * h]));
+          }
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dz) + r * p.ldz + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += dy[j];
+      }
+    }
+  });
+  if (p.partials == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[warp][lane * 8 + j] = sum[j];
+  __syncthreads();
+  const int64_t col = (int64_t)blockIdx.x * GRAD_COLS + threadIdx.x;
+  if (col < p.N) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < GRAD_THREADS / 32; ++w) s += sums[w][threadIdx.x];
+    p.partials[(int64_t)blockIdx.y * p.N + col] = s;
+  }
+}
+
+__global__ void __launch_bounds__(256) column_sums_kernel(const float* partials, int blocks, int64_t N, float* out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= N) return;
+  float s = 0.0f;
+#pragma unroll 8
+  for (int b = 0; b < blocks; ++b) s += partials[(int64_t)b * N + c];
+  out[c] = s;
+}
+
+template <bool A_MN>
+cudaError_t launch_split(const LinearSplitParams& p, int splits, cudaStream_t stream) {
+  const size_t smem = 1024 + (size_t)p.stages * (size_t)(A_BYTES + p.box_rows * TC_BK * 2);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static bool configured[64] = {};
+  if (dev >= 64 || !configured[dev]) {
+    e = cudaFuncSetAttribute(linear_split_kernel<A_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, SPLIT_SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)splits, (unsigned)((p.epi_n + 127) / 128), (unsigned)((p.rows + p.box_rows - 1) / p.box_rows));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, linear_split_kernel<A_MN>, p);
+}
+
+}  // namespace
+
+int split_stages(int box_rows) {
+  return std::min(MAX_STAGES, (SPLIT_SMEM - 1024) / (A_BYTES + box_rows * TC_BK * 2));
+}
+
+cudaError_t launch_linear_split(const LinearSplitParams& p, bool a_mn, int splits, cudaStream_t stream) {
+  return a_mn ? launch_split<true>(p, splits, stream) : launch_split<false>(p, splits, stream);
+}
+
+cudaError_t launch_act_grad(const ActGradParams& p, int dtype, int blocks, cudaStream_t stream) {
+  const dim3 grid((unsigned)((p.N + GRAD_COLS - 1) / GRAD_COLS), (unsigned)blocks);
+  return dtype == GEMM_F16 ? launch_dependent(act_grad_kernel<GEMM_F16>, grid, GRAD_THREADS, stream, p)
+                           : launch_dependent(act_grad_kernel<GEMM_BF16>, grid, GRAD_THREADS, stream, p);
+}
+
+cudaError_t launch_column_sums(const float* partials, int blocks, int64_t N, float* out, cudaStream_t stream) {
+  return launch_dependent(column_sums_kernel, dim3((unsigned)((N + 255) / 256)), 256, stream, partials, blocks, N, out);
+}
+
+}  // namespace gemmlib

@@ -1,6 +1,8 @@
 // seg_kernel.cu -- tcgen05 products whose tiles are not one dense problem's:
 //   TOKENS  D[r, :] = act(alpha * A[r, :] * op(B_g) + bias_g) for the rows r of each
 //           group g (rows found on the device);
+//   LINEAR  the same with one group of all rows and a fully connected layer's epilogue:
+//           Z = A op(B) + bias, kept if asked;  D = act(Z) + R;
 //   WGRAD   D_g = alpha * A_g' * B_g + beta * C_g, the sum over the rows of group g;
 //   CHAIN   the products of the Newton-Schulz steps, all of them in one launch:
 //           E = X X' - h I,  F = c E E' + b E,  X <- F X + a X  for every matrix of a batch
@@ -353,6 +355,24 @@ __device__ __forceinline__ void add_c(const EpiParams& e, const void* C, int64_t
   }
 }
 
+// LINEAR: x[j] += R[n + j][m + lane], j < rows, lane < cols.  A row's 32 entries are one load
+// instruction; turning wider ones around in shared memory takes as many.
+template <int DT>
+__device__ __forceinline__ void add_residual(const LinearEpilogue& l, int64_t n, int64_t m, int rows, int cols,
+                                             float (&x)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (lane >= cols) return;
+  const int64_t at = n * l.ldr + m + lane;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {   // 16 loads under way
+    float r[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) r[j] = 16 * h + j < rows ? load_as_float(l.residual, DT, at + (16 * h + j) * l.ldr) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[16 * h + j] += r[j];
+  }
+}
+
 // ---------------------------------- tiles -----------------------------------
 
 struct Tile {
@@ -370,10 +390,13 @@ struct GroupTable {
   int *lo, *cnt, *cum;
 };
 
+// Rows of the N side are found through the group table, columns of D lie on the M side.
+__host__ __device__ constexpr bool by_rows(int mode) { return mode == SEG_TOKENS || mode == SEG_LINEAR; }
+
 template <int MODE, int CG>
 struct Tiles {
   static constexpr int BM = 128 * CG;
-  static constexpr int BN = BM;   // TOKENS, WGRAD
+  static constexpr int BN = BM;   // TOKENS, LINEAR, WGRAD
   const SegParams& p;
   GroupTable g;
   int t, step, e;
@@ -381,7 +404,7 @@ struct Tiles {
       : p(p_), g(g_), t(first), step(step_), e(0) {}
 
   __device__ __forceinline__ bool next(Tile& o) {
-    if constexpr (MODE == SEG_TOKENS) {
+    if constexpr (by_rows(MODE)) {
       if (t >= g.cum[p.groups.count]) return false;
       while (t >= g.cum[e + 1]) ++e;
       const int cnt = g.cnt[e], n_tiles = (cnt + BN - 1) / BN;
@@ -589,7 +612,7 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
   // The prologue above touches no global data: overlap it with the previous kernel.
   if (MODE != SEG_CHAIN) pdl_launch_dependents();
   pdl_wait();
-  if constexpr (MODE == SEG_TOKENS || MODE == SEG_WGRAD) {
+  if constexpr (by_rows(MODE) || MODE == SEG_WGRAD) {
     const int E = p.groups.count;
     for (int e = threadIdx.x; e < E; e += THREADS) {
       int lo, hi;
@@ -597,8 +620,8 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
       groups.lo[e] = lo;
       groups.cnt[e] = hi - lo;
     }
-    if (MODE == SEG_TOKENS) __syncthreads();
-    if (MODE == SEG_TOKENS && warp == 0) {
+    if (by_rows(MODE)) __syncthreads();
+    if (by_rows(MODE) && warp == 0) {
       // First tiles, saturated at MOST: offsets that decrease can give the same rows to many
       // groups, and a sum past 2^31 would wrap to tiles outside the buffers.  (What good
       // offsets give stays below 2^28, and a group's own tiles do in any case.)
@@ -657,7 +680,7 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
       int za = 0, zb = 0;
       const int m0 = t.m0 + (int)rank * 128, n0 = t.n0 + (int)rank * (t.n_mma / CG);
       uint32_t b_slab = (uint32_t)SLAB_BYTES;   // N-side bytes of one K-major slab
-      if constexpr (MODE == SEG_TOKENS) {
+      if constexpr (by_rows(MODE)) {
         za = p.a_batched ? t.e : 0;
         int box = 0;                            // boxes of 128, 64, 32, 16, 8 rows: the smallest that holds the tile's
         while (box < 4 && (64 >> box) >= t.n_mma / CG) ++box;
@@ -919,7 +942,7 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
       cc.held = cl.held = false;
       // (one answer for the warp: lanes that saw the flag and lanes that saw an abort must not part)
       if (MODE == SEG_CHAIN && !__all_sync(0xffffffffu, chain_seen(ready_seq, tile_no++, wc))) break;
-      if (MODE != SEG_TOKENS && ep.read_c)   // the first C chunk comes in during the MMAs
+      if (!by_rows(MODE) && ep.read_c)   // the first C chunk comes in during the MMAs
         load_c(ep, ptr.C, m, (int64_t)t.n0 + c_first * 32, m_left, ext(t.n_valid - c_first * 32), cc);
       if (MODE == SEG_CHAIN && c_lo != nullptr)
         load_c(ep, c_lo, m, (int64_t)t.n0 + c_first * 32, m_left, ext(t.n_valid - c_first * 32), cl);
@@ -975,6 +998,33 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
             }
             store_chunk_t<decltype(dt)::value>(p.epi.D, p.epi.ldd, (int64_t)t.n0 + c * 32, m, t.n_valid - c * 32, m_left,
                                                x, turn, p.epi.vec_d);
+          }
+        };
+        with_type(p.epi.d_dtype, run);
+      } else if constexpr (MODE == SEG_LINEAR) {
+        float bias = 0.0f;
+        if (p.epi.bias_mode == GEMM_BIAS_COL && lane < m_left)
+          bias = load_as_float(p.epi.bias, p.epi.bias_dtype, m + lane);
+        auto run = [&](auto dt) {
+          constexpr int DT = decltype(dt)::value;
+#pragma unroll 1
+          for (int c = c_first; c < chunks; c += 2) {
+            const int64_t n = (int64_t)t.n0 + c * 32;
+            const int n_left = t.n_valid - c * 32;
+            float x[32];
+            take(x);
+            if (c + 2 < chunks) fetch(c + 2);
+            else release();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] += bias;
+            if (p.linear.pre != nullptr)
+              store_chunk_t<DT>(p.linear.pre, p.linear.ldp, n, m, n_left, m_left, x, turn, p.linear.vec_p);
+            with_act(p.linear.act, [&](auto act) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = activate<decltype(act)::value>(x[j]);
+            });
+            if (p.linear.residual != nullptr) add_residual<DT>(p.linear, n, m, n_left, m_left, x);
+            store_chunk_t<DT>(p.epi.D, p.epi.ldd, n, m, n_left, m_left, x, turn, p.epi.vec_d);
           }
         };
         with_type(p.epi.d_dtype, run);
@@ -1065,7 +1115,7 @@ __global__ void __launch_bounds__(32) wgrad_maps_kernel(const __grid_constant__ 
 
 template <int CG, bool A_MN, bool B_MN, int MODE>
 cudaError_t launch_mode(const SegParams& p, int workers, cudaStream_t stream) {
-  constexpr bool GROUPED = MODE == SEG_TOKENS || MODE == SEG_WGRAD;
+  constexpr bool GROUPED = by_rows(MODE) || MODE == SEG_WGRAD;
   const size_t smem = FIXED_SMEM + (GROUPED ? (3 * (size_t)p.groups.count + 1) * sizeof(int) : 0);
   constexpr size_t MOST = FIXED_SMEM + (GROUPED ? (3 * (size_t)kMaxGroups + 1) * sizeof(int) : 0);
   static_assert(MOST <= 232448, "shared memory budget");
@@ -1106,6 +1156,9 @@ cudaError_t launch_cg(const SegParams& p, int mode, bool a_mn, int workers, cuda
     case SEG_TOKENS:
       return a_mn ? launch_mode<CG, true, false, SEG_TOKENS>(p, workers, stream)
                   : launch_mode<CG, false, false, SEG_TOKENS>(p, workers, stream);
+    case SEG_LINEAR:
+      return a_mn ? launch_mode<CG, true, false, SEG_LINEAR>(p, workers, stream)
+                  : launch_mode<CG, false, false, SEG_LINEAR>(p, workers, stream);
     case SEG_WGRAD: return launch_mode<CG, true, true, SEG_WGRAD>(p, workers, stream);
     default: return launch_mode<CG, false, false, SEG_CHAIN>(p, workers, stream);
   }

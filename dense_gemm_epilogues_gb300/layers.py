@@ -1,4 +1,5 @@
-"""What stands around the products of a layer, on torch tensors: the routing of tokens to
+"""What stands around the products of a layer, on torch tensors: fully connected layers with
+activation and residual, the routing of tokens to
 experts with its balance loss, rows between tokens and experts, gradients clipped by their
 global norm.
 
@@ -15,11 +16,132 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import GEMM_F32, GemmError, Plan, gemm_routing_t, gemm_tensor_t
+from . import (GEMM_F32, GEMM_LINEAR_GELU, GEMM_LINEAR_GELU_TANH, GEMM_LINEAR_NONE, GEMM_LINEAR_RELU, GEMM_LINEAR_SILU,
+               GEMM_OP_N, GEMM_OP_T, GemmError, Plan, gemm_linear_t, gemm_routing_t, gemm_tensor_t)
 from .expert import _LIB, _code, _device, _pitch, _plan_for, _raw_stream
 
 _I32, _F32 = torch.int32, torch.float32
+_ACTS = {None: GEMM_LINEAR_NONE, "relu": GEMM_LINEAR_RELU, "gelu": GEMM_LINEAR_GELU,
+         "gelu_tanh": GEMM_LINEAR_GELU_TANH, "silu": GEMM_LINEAR_SILU}
 
+
+# ------------------------- fully connected layers ---------------------------
+
+def _act(name) -> int:
+    try:
+        return _ACTS[name]
+    except KeyError:
+        raise ValueError(f"activation {name!r} is not one of {sorted(k for k in _ACTS if k)} or None") from None
+
+
+def _weights(w, K: int, N: int, name: str = "w"):
+    """(layout, leading dimension) of a [K, N] matrix with unit stride along N or K."""
+    a, b = w.stride()
+    if (b == 1 or N <= 1) and (a >= N or K <= 1):
+        return GEMM_OP_T, max(a, N, 1)
+    if (a == 1 or K <= 1) and (b >= K or N <= 1):
+        return GEMM_OP_N, max(b, K, 1)
+    raise ValueError(f"{name} must have unit stride along K or N and no overlapping rows")
+
+
+def _like(t, shape, dtype, name: str) -> int:
+    """The pitch of a row-major tensor that must have this shape and type."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {str(dtype)[6:]} of shape {tuple(shape)}")
+    return _pitch(shape, t.stride(), name)
+
+
+def linear(x, w, *, bias=None, activation: Optional[str] = None, residual=None, save_pre: bool = False, out=None,
+           out_dtype=None, plan: Optional[Plan] = None, stream=None):
+    """A fully connected layer in one kernel (gemm_run_linear):
+    z = x @ w + bias;  y = activation(z) + residual.  Returns y, or (y, z) with save_pre: what
+    linear_grad needs of an activation.
+
+    x: [rows, K] float16 or bfloat16; w: [K, N] of the same type with unit stride along N or K (a
+    transposed [N, K] matrix); bias: [N] of a floating type; residual: [rows, N] of the output's
+    type (it may be `out`).  activation: "relu", "gelu", "gelu_tanh", "silu" or None.  out_dtype
+    defaults to x's."""
+    dtype = x.dtype
+    M, K = x.shape
+    K2, N = w.shape
+    if K2 != K or w.dtype is not dtype:
+        raise ValueError("x must be [rows, K] and w [K, N] of the same type")
+    act = _act(activation)
+    layout, ldb = _weights(w, K, N)
+    lda = _pitch((M, K), x.stride(), "x")
+    device = _device(x, w, bias, residual, out)
+    if out is None:
+        out_dtype = out_dtype or dtype
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        ldd = max(N, 1)
+    else:
+        out_dtype = out.dtype
+        ldd = _like(out, (M, N), out_dtype, "out")
+    code = _code(out_dtype)
+    ldr = _like(residual, (M, N), out_dtype, "residual") if residual is not None else 0
+    pre = torch.empty((M, N), dtype=out_dtype, device=x.device) if save_pre else None
+    bias_code = GEMM_F32
+    if bias is not None:
+        if bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
+            raise ValueError("bias must be [N] and contiguous")
+        bias_code = _code(bias.dtype)
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(dtype), GEMM_F32, device, stream)
+    epi = gemm_linear_t(bias.data_ptr() if bias is not None else None, bias_code, act,
+                        residual.data_ptr() if residual is not None else None, ldr,
+                        pre.data_ptr() if save_pre else None, max(N, 1), code)
+    status = _LIB.gemm_run_linear(plan.handle, layout, M, N, K, x.data_ptr(), lda, w.data_ptr(), ldb, out.data_ptr(),
+                                  ldd, epi, stream)
+    if status:
+        raise GemmError(status, "gemm_run_linear")
+    return (out, pre) if save_pre else out
+
+
+def linear_grad(dy, x, w, *, activation: Optional[str] = None, pre=None, dw_dtype=None, input_grad: bool = True,
+                weight_grad: bool = True, bias_grad: bool = True, plan: Optional[Plan] = None, stream=None):
+    """(dx, dw, dbias) of linear for its output's gradient dy (gemm_run_linear_grad), None for
+    what is not asked for; the residual's gradient is dy itself.
+
+    dy: [rows, N] of x's type; pre: linear's z in x's type, needed with an activation.  dx has x's
+    type; dw has w's order of dimensions and dw_dtype (w's type by default); dbias is float32, from
+    values that are not rounded."""
+    dtype = x.dtype
+    M, K = x.shape
+    K2, N = w.shape
+    if K2 != K or w.dtype is not dtype:
+        raise ValueError("x must be [rows, K] and w [K, N] of the same type")
+    act = _act(activation)
+    layout, ldb = _weights(w, K, N)
+    lddy = _like(dy, (M, N), dtype, "dy")
+    ldp = 0
+    if act != GEMM_LINEAR_NONE:
+        if pre is None:
+            raise ValueError("an activation's gradient needs pre")
+        ldp = _like(pre, (M, N), dtype, "pre")
+    device = _device(x, w, dy, pre)
+    d = x.device
+    dx = torch.empty((M, K), dtype=dtype, device=d) if input_grad else None
+    dw_dtype = dw_dtype or dtype
+    dw = None
+    if weight_grad:
+        dw = (torch.empty((K, N), dtype=dw_dtype, device=d) if layout == GEMM_OP_T
+              else torch.empty((N, K), dtype=dw_dtype, device=d).t())
+    db = torch.empty((N,), dtype=_F32, device=d) if bias_grad else None
+    stream = _raw_stream(device) if stream is None else stream
+    plan = _plan_for(plan, _code(dtype), GEMM_F32, device, stream)
+    status = _LIB.gemm_run_linear_grad(plan.handle, layout, M, N, K, dy.data_ptr(), lddy,
+                                       pre.data_ptr() if ldp else None, ldp, act, x.data_ptr(),
+                                       _pitch((M, K), x.stride(), "x"), w.data_ptr(), ldb,
+                                       dx.data_ptr() if input_grad else None, max(K, 1),
+                                       dw.data_ptr() if weight_grad else None,
+                                       max(N if layout == GEMM_OP_T else K, 1), _code(dw_dtype),
+                                       db.data_ptr() if bias_grad else None, stream)
+    if status:
+        raise GemmError(status, "gemm_run_linear_grad")
+    return dx, dw, db
+
+
+# ------------------------------- routing ------------------------------------
 
 class Routing(NamedTuple):
     """Tokens routed to experts (route); the gradients and the exchange of rows read it."""

@@ -612,14 +612,71 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
                                  gemm_stream_t stream);
 
 /* ===========================================================================
- * Around the products: routing of tokens to experts, the exchange of rows between
- * tokens and experts, and gradients clipped by their global norm.  No page has a
- * counterpart; they are what an expert layer needs beside its products.  They use
+ * Around the products: fully connected layers with activation and residual, routing of
+ * tokens to experts, the exchange of rows between tokens and experts, and gradients
+ * clipped by their global norm.  No page has a counterpart; they are what layers of
+ * language models need beside the products.  They use
  * the plan's device, error word and scratch as the others do and are asynchronous
  * on `stream`.  No atomics decide an order: equal inputs give equal bits.
  * ======================================================================== */
 
-/* In PyTorch terms: route, route_grad, dispatch, dispatch_grad, combine, combine_grad and
+/* Activations of a fully connected layer.  GELU is x P(x) with the normal distribution P,
+ * GELU_TANH its usual approximation 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))), SILU
+ * x / (1 + exp(-x)).  All keep NaN. */
+typedef enum {
+    GEMM_LINEAR_NONE = 0,
+    GEMM_LINEAR_RELU = 1,
+    GEMM_LINEAR_GELU = 2,
+    GEMM_LINEAR_GELU_TANH = 3,
+    GEMM_LINEAR_SILU = 4
+} gemm_linear_act_t;
+
+typedef struct {
+    const void* bias;         /* N entries of bias_dtype (F32, F16 or BF16), or NULL */
+    gemm_dtype_t bias_dtype;
+    gemm_linear_act_t act;
+    const void* residual;     /* row-major M x N of out_dtype, or NULL */
+    int64_t ld_residual;
+    void* pre;                /* row-major M x N of out_dtype: what the activation is applied to; NULL: not kept */
+    int64_t ld_pre;
+    gemm_dtype_t out_dtype;   /* type of D: F32, F16 or BF16 */
+} gemm_linear_t;
+
+/* ---------------------------------------------------------------------------
+ * gemm_run_linear -- a fully connected layer:
+ *     Z = A op(B) + bias;   D = act(Z) + residual
+ * with everything behind the product in its epilogue: sums are fp32, Z (`pre`) and D are
+ * each rounded once, D from the unrounded Z.
+ *   plan        ab_dtype F16 or BF16 (else GEMM_ERR_UNSUPPORTED).
+ *   A, lda      row-major M x K.     B, ldb   K x N in layoutB, as for gemm_run.
+ *   epi         NULL: none of it, D of the plan's ab_dtype.
+ * Any sizes, alignments and pitches; operands that TMA cannot address cost a copy into the
+ * plan's scratch.  K == 0 gives act(bias) + residual.  D may be the residual, but must not
+ * overlap A, B or pre.  Where few rows give few tiles (a decoding step), up to eight CTAs
+ * of a cluster share a tile's K (gemm_config_t.split_k); the sum has one order all the same.
+ * ------------------------------------------------------------------------- */
+gemm_status_t gemm_run_linear(gemm_plan_t plan, gemm_layout_t layoutB, int64_t M, int64_t N, int64_t K, const void* A,
+                              int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd, const gemm_linear_t* epi,
+                              gemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gemm_run_linear_grad -- the gradients of gemm_run_linear for the gradient dY of its D:
+ *     dZ = dY * act'(pre);   dA = dZ op(B)';   dB = A' dZ;   dbias = sum over rows of dZ
+ * (the residual's gradient is dY itself).
+ *   dY, pre     row-major M x N of the plan's ab_dtype; pre is not read without an activation.
+ *   dA          row-major M x K of the plan's ab_dtype, or NULL: not wanted (B is not read).
+ *   dB          K x N in layoutB (B's own), of db_dtype F32, F16 or BF16, or NULL (A is not read).
+ *   dbias       N fp32 entries, or NULL.
+ * dZ is rounded to the operands' type for the two products, as the tensor cores take it, and
+ * summed unrounded, in fp32, for dbias.  It takes M x N entries of the plan's scratch (none
+ * without an activation).  M == 0 gives zeros.  The outputs must not overlap the inputs.
+ * ------------------------------------------------------------------------- */
+gemm_status_t gemm_run_linear_grad(gemm_plan_t plan, gemm_layout_t layoutB, int64_t M, int64_t N, int64_t K,
+                                   const void* dY, int64_t lddy, const void* pre, int64_t ldp, gemm_linear_act_t act,
+                                   const void* A, int64_t lda, const void* B, int64_t ldb, void* dA, int64_t ldda,
+                                   void* dB, int64_t lddb, gemm_dtype_t db_dtype, float* dbias, gemm_stream_t stream);
+
+/* In PyTorch terms: linear, linear_grad, route, route_grad, dispatch, dispatch_grad, combine, combine_grad and
  * clip_grad_norm of the Python package. */
 
 /* A routing of `tokens` tokens.  All pointers are device memory. */

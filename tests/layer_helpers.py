@@ -78,3 +78,52 @@ def route_grad_ref(logits, top, dweights, dloss, renormalize=True, mask=None):
     any_ = chosen[:, :1]
     ref = torch.where(any_, direct + p * (g - (p * g).sum(1, keepdim=True)), 0.0)
     return ref, mag + p * (ga + (p * ga).sum(1, keepdim=True)), spread
+
+
+# ------------------------- fully connected layers ---------------------------
+
+ACTS = [None, "relu", "gelu", "gelu_tanh", "silu"]
+
+
+def act_ref(z, act):
+    """(act(z), act'(z)) in 64 bits."""
+    if act == "relu":
+        return z.clamp(min=0), (z > 0).double()
+    if act == "gelu":
+        p = 0.5 * torch.special.erfc(-z / math.sqrt(2))
+        return z * p, p + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    if act in ("gelu_tanh", "silu"):
+        a = 2 * math.sqrt(2 / math.pi)
+        u, du = (z, torch.ones_like(z)) if act == "silu" else (a * (z + 0.044715 * z ** 3), a * (1 + 0.134145 * z * z))
+        s = torch.sigmoid(u)
+        return z * s, s + z * s * torch.sigmoid(-u) * du
+    return z, torch.ones_like(z)
+
+
+def act_error(z, act):
+    """How far fp32 activations may be off: the normal distribution by 2.3e-7 (its formula in fp32)
+    and two hardware steps (2^-22) of at most 1/2 each, times |z|; a sigmoid by two such steps and
+    the rounding of its exponent v, |v| 2^-23 of s(v) with |v| s(v) <= 0.4 where it is not near 1."""
+    return 5e-7 * (1 + z.abs()) if act not in (None, "relu") else torch.zeros_like(z)
+
+
+def act_grad_error(z, act):
+    """The same for derivatives: that of the distribution, and of z p(z) the exponential's, two steps
+    and z^2 2^-23 with |z|^3 p(z) < 0.5; of sigmoids the product of two, each as above."""
+    return 1e-6 * (1 + z.abs()) if act not in (None, "relu") else torch.zeros_like(z)
+
+
+def linear_ref(x, w, bias, act, residual):
+    """(y, z, the error that fp32 sums and the activation may make of y, and of z)."""
+    z = x.double() @ w.double()
+    mag = x.double().abs() @ w.double().abs()
+    if bias is not None:
+        z = z + bias.double()
+        mag = mag + bias.double().abs()
+    ez = (x.shape[1] + 4) * EPS * mag
+    y, _ = act_ref(z, act)
+    ey = 1.13 * ez + act_error(z, act)   # (no activation is steeper than 1.13)
+    if residual is not None:
+        y = y + residual.double()
+        ey = ey + 2.0 ** -23 * (y.abs() + residual.double().abs())
+    return y, z, ey, ez

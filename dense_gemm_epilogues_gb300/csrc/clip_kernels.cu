@@ -9,7 +9,9 @@
 // trips over lists longer than L2, of which two are the floor.
 //
 // Squares are added in fp32 over eight entries at a time and over four such sums, then in
-// fp64.  Eight entries whose sum leaves the range that fp32 holds well (below 1e-30, above
+// fp64, in which only one warp of a CTA adds up and one thread takes the root: this chip adds
+// two fp64 numbers per SM and clock (every thread taking the root itself cost 20 us).  Eight
+// entries whose sum leaves the range that fp32 holds well (below 1e-30, above
 // 1e37) are squared in fp64 instead, so entries of any size that fp32 holds count.
 #include "layer.h"
 
@@ -52,7 +54,10 @@ __host__ __device__ __forceinline__ int lead_of(const void* p, int es) {
 // Entries i .. i + 7 (zeros outside 0 .. n - 1).
 template <int DT>
 __device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, float (&x)[8]) {
-  if (i >= 0 && i + 8 <= n) {
+  if (i >= n) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+  } else if (i >= 0 && i + 8 <= n) {
     if constexpr (DT == GEMM_F32) {
       asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
@@ -121,23 +126,26 @@ __device__ __forceinline__ float squares(const float (&x)[8], double& wide) {
   return 0.0f;
 }
 
-// The sum of a double over the CTA, in one order; valid in every thread.
-__device__ __forceinline__ double block_sum(double v, double* smem) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
-  __syncthreads();
+// The sum of n doubles in shared or global memory by one warp, in one order; valid in lane 0.
+__device__ __forceinline__ double warp_total(const double* v, int n, int lane) {
   double s = 0.0;
+  for (int i = lane; i < n; i += 32 * 10) {   // (ten loads under way: all of 304 CTAs')
+    double x[10];
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) s += smem[w];
+    for (int u = 0; u < 10; ++u) x[u] = i + 32 * u < n ? v[i + 32 * u] : 0.0;
+#pragma unroll
+    for (int u = 0; u < 10; ++u)
+      if (i + 32 * u < n) s += x[u];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(THREADS) clip_norm_kernel(const __grid_constant__ ClipList<CAP> l,
                                                             const __grid_constant__ ClipPass p, int first_partial) {
-  __shared__ double smem[THREADS / 32];
+  __shared__ double smem[THREADS];
   pdl_launch_dependents();
   pdl_wait();
   double wide = 0.0;
@@ -155,28 +163,37 @@ __global__ void __launch_bounds__(THREADS) clip_norm_kernel(const __grid_constan
         for (int u = 0; u < UNROLL; ++u) load8<DT>(src, unit_at(at, u), hi, x[u]);
         float s = 0.0f;
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) s += squares(x[u], wide);
-        wide += (double)s;
+        for (int u = 0; u < UNROLL; ++u)
+          if (unit_at(at, u) < hi) s += squares(x[u], wide);
+        if (s != 0.0f) wide += (double)s;
       }
     });
   }
-  const double sum = block_sum(wide, smem);
-  if (threadIdx.x == 0) p.partials[first_partial + blockIdx.x] = sum;
+  smem[threadIdx.x] = wide;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const double sum = warp_total(smem, THREADS, (int)threadIdx.x);
+    if (threadIdx.x == 0) p.partials[first_partial + blockIdx.x] = sum;
+  }
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(THREADS) clip_scale_kernel(const __grid_constant__ ClipList<CAP> l,
                                                              const __grid_constant__ ClipPass p, int write_norm) {
-  __shared__ double smem[THREADS / 32];
+  __shared__ float factor;
   pdl_launch_dependents();
   pdl_wait();
-  double v = 0.0;
-  for (int i = threadIdx.x; i < p.num_partials; i += THREADS) v += __ldcg(p.partials + i);
-  const double n = sqrt(block_sum(v, smem));
-  const float norm = (float)n;
-  if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
-  float scale = 1.0f;
-  if (isfinite(norm)) scale = fminf(1.0f, (float)((double)p.max_norm / (n + (double)p.eps)));
+  if (threadIdx.x < 32) {
+    const double sum = warp_total(p.partials, p.num_partials, (int)threadIdx.x);
+    if (threadIdx.x == 0) {
+      const double n = sqrt(sum);
+      const float norm = (float)n;
+      if (write_norm && blockIdx.x == 0) *p.norm = norm;
+      factor = isfinite(norm) ? fminf(1.0f, (float)((double)p.max_norm / (n + (double)p.eps))) : 1.0f;
+    }
+  }
+  __syncthreads();
+  const float scale = factor;
   const int chunks = l.first[l.tensors];
   for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
     const int c = chunks - 1 - i, t = tensor_of(l, c);
@@ -241,7 +258,7 @@ int64_t clip_chunk(int64_t total, int sm_count) {
 int clip_blocks(const ClipTensor* t, int count, int64_t chunk, int sm_count) {
   int64_t chunks = 0;
   for (int i = 0; i < count; ++i) chunks += chunks_of(t[i], chunk);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, 4 * (int64_t)sm_count));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, 2 * (int64_t)sm_count));
 }
 
 cudaError_t launch_clip_norm(const ClipTensor* t, int count, const ClipPass& p, int first_partial, int blocks,

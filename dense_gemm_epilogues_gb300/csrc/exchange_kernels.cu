@@ -7,9 +7,9 @@
 // a long run of bytes; so every byte moves once, no atomics decide an order, and the sums
 // over a token's rows and over a row's entries have one order.
 //
-// Bound by memory.  dispatch and combine: a thread takes 16 bytes of a token and all of its
-// rows' (four rows' loads under way), and as many such pieces as the chip has room for.
-// combine_grad: a warp takes a token, four of its rows at a time.
+// Bound by memory.  A warp takes a token -- of few tokens with long rows, a part of one, up to
+// eight warps of a CTA together -- with its slots and weights in its lanes, and goes along the
+// row in pieces of 16 bytes per lane, several pieces and rows under way.
 //
 // A slot outside the sorted buffer is no row; one that is not -1 either is reported through
 // the error word.
@@ -20,130 +20,189 @@ namespace {
 
 constexpr int THREADS = 256;
 
-// Piece v of a row: VEC entries (16 bytes), or a single entry where rows are not aligned.
+// A piece of a row: 16 bytes as they lie in memory (half the registers of their values, so
+// that more are under way), or a single entry where rows are not aligned.
 template <int DT, bool WIDE>
 struct Piece {
   static constexpr int N = !WIDE ? 1 : DT == GEMM_F32 ? 4 : 8;
-  float x[N];
+  uint32_t w[WIDE ? 4 : 1];
 
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     if constexpr (!WIDE) {
-      x[0] = load_as_float(p, DT, i);
-    } else if constexpr (DT == GEMM_F32) {
-      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      w[0] = __float_as_uint(load_as_float(p, DT, i));
     } else {
-      set(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
-    }
-  }
-  __device__ __forceinline__ void set(const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int h = 0; h < N / 2; ++h) {
-      if constexpr (DT == GEMM_F16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-        x[2 * h] = f.x, x[2 * h + 1] = f.y;
-      } else {
-        x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
-      }
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (16 / N));
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     }
   }
   __device__ __forceinline__ void store(void* p, int64_t i) const {
-    if constexpr (!WIDE) {
-      store_float_as(p, DT, i, x[0]);
-    } else if constexpr (DT == GEMM_F32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+    if constexpr (!WIDE) store_float_as(p, DT, i, __uint_as_float(w[0]));
+    else *reinterpret_cast<uint4*>(static_cast<char*>(p) + i * (16 / N)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int h = 0; h < (WIDE ? 4 : 1); ++h) w[h] = 0u;
+  }
+  __device__ __forceinline__ void get(float (&x)[N]) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if constexpr (!WIDE || DT == GEMM_F32) {
+        x[k] = __uint_as_float(w[k]);
+      } else if constexpr (DT == GEMM_F16) {
+        const __half2 h = *reinterpret_cast<const __half2*>(&w[k / 2]);
+        x[k] = k % 2 ? __high2float(h) : __low2float(h);
+      } else {
+        x[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&x)[N]) {
+    if constexpr (!WIDE || DT == GEMM_F32) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) w[k] = __float_as_uint(x[k]);
     } else {
-      uint32_t w[4];
 #pragma unroll
       for (int h = 0; h < N / 2; ++h) {
         if constexpr (DT == GEMM_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
         else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
       }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 };
 
-// The row of (t, j), -1 for none.
-__device__ __forceinline__ int64_t row_of(const ExchangeParams& p, int64_t i) {
-  const int s = p.slots[i];
+constexpr int WARPS = THREADS / 32;
+
+// What warp `index` works on: a token and its part of the row, pieces first, first + stride, ...
+struct Part {
+  int64_t token;
+  int first, stride;
+};
+__device__ __forceinline__ Part part_of(const ExchangeParams& p, int64_t index) {
+  const int lane = threadIdx.x & 31;
+  return Part{index >> p.parts_shift, (int)(index & ((1 << p.parts_shift) - 1)) * 32 + lane, 32 << p.parts_shift};
+}
+
+// Lane j: the row of the token's j-th choice, -1 for none.
+__device__ __forceinline__ int row_of(const ExchangeParams& p, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  if (lane >= p.top) return -1;
+  const int s = p.slots[t * p.top + lane];
   if (s >= 0 && s < p.rows) return s;
   if (s != -1) atomicCAS(p.err, 0, (int32_t)GEMM_ERR_INVALID_ARG);
   return -1;
 }
 
-// Rows from the last used one on, as zeros.
+// Rows from the last used one on, as zeros: all warps share them.
 template <int DT, bool WIDE>
 __device__ __forceinline__ void clear_rest(const ExchangeParams& p) {
   if (p.used == nullptr) return;
   using P = Piece<DT, WIDE>;
-  const int64_t first = min(p.rows, max((int64_t)0, (int64_t)*p.used)), per = p.width / P::N;
+  const int per = (int)(p.width / P::N);
   P z;
-#pragma unroll
-  for (int k = 0; k < P::N; ++k) z.x[k] = 0.0f;
-  const int64_t stride = (int64_t)gridDim.x * THREADS;
-  for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < (p.rows - first) * per; i += stride) {
-    const int64_t r = i / per;
-    z.store(p.out, (first + r) * p.ldo + (i - r * per) * P::N);
-  }
+  z.clear();
+  const int64_t first = min(p.rows, max((int64_t)0, (int64_t)*p.used));
+  for (int64_t r = first + (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); r < p.rows; r += (int64_t)gridDim.x * WARPS)
+    for (int v = (int)threadIdx.x & 31; v < per; v += 32) z.store(p.out, r * p.ldo + (int64_t)v * P::N);
 }
 
 template <int DT, bool WIDE>
 __global__ void __launch_bounds__(THREADS) dispatch_kernel(const __grid_constant__ ExchangeParams p) {
   using P = Piece<DT, WIDE>;
+  constexpr int U = 4;   // pieces under way
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t per = p.width / P::N, stride = (int64_t)gridDim.x * THREADS;
-  for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < p.tokens * per; i += stride) {
-    const int64_t t = i / per, c = (i - t * per) * P::N;
-    P x;
-    x.load(p.x, t * p.ldx + c);
-    for (int j = 0; j < p.top; ++j) {
-      const int64_t r = row_of(p, t * p.top + j);
-      if (r >= 0) x.store(p.out, r * p.ldo + c);
+  const int per = (int)(p.width / P::N);
+  const int64_t warps = (int64_t)gridDim.x * WARPS;
+  for (int64_t i = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); i >> p.parts_shift < p.tokens; i += warps) {
+    const Part a = part_of(p, i);
+    const int mine = row_of(p, a.token);
+    const int64_t at = a.token * p.ldx;
+    for (int v0 = a.first; v0 - (int)(threadIdx.x & 31) < per; v0 += U * a.stride) {
+      P x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + u * a.stride < per) x[u].load(p.x, at + (int64_t)(v0 + u * a.stride) * P::N);
+      for (int j = 0; j < p.top; ++j) {
+        const int r = __shfl_sync(0xffffffffu, mine, j);
+        if (r < 0) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (v0 + u * a.stride < per) x[u].store(p.out, r * p.ldo + (int64_t)(v0 + u * a.stride) * P::N);
+      }
     }
   }
   clear_rest<DT, WIDE>(p);
 }
 
-template <int DT, bool WIDE>
+// Eight loads of sorted rows per lane under way, and as many of the residual as pieces: all
+// ROWS rows of 8 / ROWS pieces.  ROWS is at least top, or 8.
+template <int DT, bool WIDE, int ROWS>
 __global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant__ ExchangeParams p) {
   using P = Piece<DT, WIDE>;
-  constexpr int ROWS = 4;   // loads under way
+  constexpr int U = 8 / ROWS;
+  const int lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t per = p.width / P::N, stride = (int64_t)gridDim.x * THREADS;
-  for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < p.tokens * per; i += stride) {
-    const int64_t t = i / per, c = (i - t * per) * P::N;
-    P sum;
-    if (p.residual != nullptr) {
-      sum.load(p.residual, t * p.ldr + c);
-    } else {
+  const int per = (int)(p.width / P::N);
+  const int64_t warps = (int64_t)gridDim.x * WARPS;
+  for (int64_t i = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); i >> p.parts_shift < p.tokens; i += warps) {
+    const Part a = part_of(p, i);
+    const float weight = p.weights != nullptr && lane < p.top ? p.weights[a.token * p.top + lane] : 1.0f;
+    const int mine = row_of(p, a.token);
+    int r[ROWS];
+    float w[ROWS];
+    auto choices = [&](int j0) {
 #pragma unroll
-      for (int k = 0; k < P::N; ++k) sum.x[k] = 0.0f;
-    }
-    for (int j0 = 0; j0 < p.top; j0 += ROWS) {
-      P y[ROWS];
-      float w[ROWS];
-      bool ok[ROWS];
+      for (int q = 0; q < ROWS; ++q) {
+        r[q] = __shfl_sync(0xffffffffu, mine, (j0 + q) & 31);
+        w[q] = __shfl_sync(0xffffffffu, weight, (j0 + q) & 31);
+        if (j0 + q >= p.top) r[q] = -1;
+      }
+    };
+    choices(0);
+    for (int v0 = a.first; v0 - lane < per; v0 += U * a.stride) {
+      P y[U][ROWS], z[U];
+      auto load_rows = [&]() {
 #pragma unroll
-      for (int u = 0; u < ROWS; ++u) {
-        const int64_t r = j0 + u < p.top ? row_of(p, t * p.top + j0 + u) : -1;
-        ok[u] = r >= 0;
-        if (ok[u]) {
-          w[u] = p.weights != nullptr ? p.weights[t * p.top + j0 + u] : 1.0f;
-          y[u].load(p.y, r * p.ldy + c);
-        }
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int q = 0; q < ROWS; ++q)
+            if (r[q] >= 0 && v0 + u * a.stride < per) y[u][q].load(p.y, r[q] * p.ldy + (int64_t)(v0 + u * a.stride) * P::N);
+      };
+      auto add_rows = [&](int u, float (&sum)[P::N]) {
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q)
+          if (r[q] >= 0) {
+            float x[P::N];
+            y[u][q].get(x);
+#pragma unroll
+            for (int k = 0; k < P::N; ++k) sum[k] = fmaf(w[q], x[k], sum[k]);
+          }
+      };
+      if (ROWS == 8 && p.top > 8) choices(0);
+      load_rows();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        z[u].clear();
+        if (p.residual != nullptr && v0 + u * a.stride < per)
+          z[u].load(p.residual, a.token * p.ldr + (int64_t)(v0 + u * a.stride) * P::N);
       }
 #pragma unroll
-      for (int u = 0; u < ROWS; ++u)
-        if (ok[u]) {
-#pragma unroll
-          for (int k = 0; k < P::N; ++k) sum.x[k] = fmaf(w[u], y[u].x[k], sum.x[k]);
+      for (int u = 0; u < U; ++u) {
+        float sum[P::N];
+        z[u].get(sum);
+        add_rows(u, sum);
+        if constexpr (ROWS == 8) {
+          for (int j0 = 8; j0 < p.top; j0 += 8) {
+            choices(j0);
+            load_rows();
+            add_rows(u, sum);
+          }
         }
+        z[u].set(sum);
+        if (v0 + u * a.stride < per) z[u].store(p.out, a.token * p.ldo + (int64_t)(v0 + u * a.stride) * P::N);
+      }
     }
-    sum.store(p.out, t * p.ldo + c);
   }
 }
 
@@ -151,47 +210,68 @@ template <int DT, bool WIDE>
 __global__ void __launch_bounds__(THREADS) combine_grad_kernel(const __grid_constant__ ExchangeParams p) {
   using P = Piece<DT, WIDE>;
   constexpr int ROWS = 4;
-  const int lane = threadIdx.x & 31;
+  __shared__ float parts[WARPS][32];   // a token's parts: the warps' sums
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t warps = (int64_t)gridDim.x * (THREADS / 32), per = p.width / P::N;
-  for (int64_t t = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); t < p.tokens; t += warps) {
+  const int per = (int)(p.width / P::N);
+  const int64_t warps = (int64_t)gridDim.x * WARPS;
+  // (all warps of a CTA take the same turns: those of a token meet at a barrier)
+  for (int64_t i0 = (int64_t)blockIdx.x * WARPS; i0 >> p.parts_shift < p.tokens; i0 += warps) {
+    const Part a = part_of(p, i0 + warp);
+    const bool in = a.token < p.tokens;
+    const int mine = in ? row_of(p, a.token) : -1;
+    const float weight = mine >= 0 && p.weights != nullptr ? p.weights[a.token * p.top + lane] : 1.0f;
+    float result = 0.0f;   // lane j: the j-th sum
     for (int j0 = 0; j0 < p.top; j0 += ROWS) {
-      int64_t r[ROWS];
+      int r[ROWS];
       float w[ROWS], dot[ROWS];
 #pragma unroll
-      for (int u = 0; u < ROWS; ++u) {
-        const int64_t i = t * p.top + j0 + u;
-        r[u] = j0 + u < p.top ? row_of(p, i) : -1;
-        w[u] = r[u] >= 0 && p.weights != nullptr ? p.weights[i] : 1.0f;
-        dot[u] = 0.0f;
+      for (int q = 0; q < ROWS; ++q) {
+        r[q] = __shfl_sync(0xffffffffu, mine, (j0 + q) & 31);
+        if (j0 + q >= p.top) r[q] = -1;
+        w[q] = __shfl_sync(0xffffffffu, weight, (j0 + q) & 31);
+        dot[q] = 0.0f;
       }
 #pragma unroll 2
-      for (int64_t v = lane; v < per; v += 32) {
+      for (int v = a.first; in && v < per; v += a.stride) {
         P x, y[ROWS];
-        x.load(p.x, t * p.ldx + v * P::N);
+        x.load(p.x, a.token * p.ldx + (int64_t)v * P::N);
 #pragma unroll
-        for (int u = 0; u < ROWS; ++u)
-          if (r[u] >= 0) y[u].load(p.y, r[u] * p.ldy + v * P::N);
+        for (int q = 0; q < ROWS; ++q)
+          if (r[q] >= 0) y[q].load(p.y, r[q] * p.ldy + (int64_t)v * P::N);
 #pragma unroll
-        for (int u = 0; u < ROWS; ++u)
-          if (r[u] >= 0) {
+        for (int q = 0; q < ROWS; ++q)
+          if (r[q] >= 0) {
             P d;
+            float g[P::N], v_y[P::N];
+            x.get(g);
+            y[q].get(v_y);
 #pragma unroll
             for (int k = 0; k < P::N; ++k) {
-              dot[u] = fmaf(x.x[k], y[u].x[k], dot[u]);
-              d.x[k] = w[u] * x.x[k];
+              dot[q] = fmaf(g[k], v_y[k], dot[q]);
+              g[k] *= w[q];
             }
-            d.store(p.out, r[u] * p.ldo + v * P::N);
+            d.set(g);
+            d.store(p.out, r[q] * p.ldo + (int64_t)v * P::N);
           }
       }
 #pragma unroll
-      for (int u = 0; u < ROWS; ++u) {
+      for (int q = 0; q < ROWS; ++q) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-        if (lane == 0 && j0 + u < p.top) static_cast<float*>(p.dweights)[t * p.top + j0 + u] = dot[u];
+        for (int o = 16; o > 0; o >>= 1) dot[q] += __shfl_xor_sync(0xffffffffu, dot[q], o);
+        if (lane == j0 + q) result = dot[q];
       }
     }
+    const int group = 1 << p.parts_shift;
+    if (group > 1) {
+      __syncthreads();
+      parts[warp][lane] = result;
+      __syncthreads();
+      if ((warp & (group - 1)) == 0)
+        for (int h = 1; h < group; ++h) result += parts[warp + h][lane];
+    }
+    if (in && (warp & (group - 1)) == 0 && lane < p.top) static_cast<float*>(p.dweights)[a.token * p.top + lane] = result;
   }
   clear_rest<DT, WIDE>(p);
 }
@@ -199,13 +279,20 @@ __global__ void __launch_bounds__(THREADS) combine_grad_kernel(const __grid_cons
 enum { DISPATCH, COMBINE, COMBINE_GRAD };
 
 template <int WHAT, int DT, bool WIDE>
-cudaError_t launch_as(const ExchangeParams& p, int sm_count, cudaStream_t stream) {
+cudaError_t launch_as(ExchangeParams p, int sm_count, cudaStream_t stream) {
+  // Up to eight warps share a token while the chip has less than 16 warps per SM and a warp
+  // more than one turn of its row.
   const int64_t per = p.width / Piece<DT, WIDE>::N;
-  const int64_t work = WHAT == COMBINE_GRAD ? p.tokens * 32 : p.tokens * per;
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((work + THREADS - 1) / THREADS, 16 * (int64_t)sm_count));
-  if constexpr (WHAT == DISPATCH) return launch_dependent(dispatch_kernel<DT, WIDE>, dim3((unsigned)grid), THREADS, stream, p);
-  else if constexpr (WHAT == COMBINE) return launch_dependent(combine_kernel<DT, WIDE>, dim3((unsigned)grid), THREADS, stream, p);
-  else return launch_dependent(combine_grad_kernel<DT, WIDE>, dim3((unsigned)grid), THREADS, stream, p);
+  p.parts_shift = 0;
+  while (p.parts_shift < 3 && (p.tokens << p.parts_shift) < 16 * (int64_t)sm_count && per > (int64_t)(32 << p.parts_shift))
+    ++p.parts_shift;
+  const int64_t work = ((p.tokens << p.parts_shift) + WARPS - 1) / WARPS;
+  const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(work, 16 * (int64_t)sm_count)));
+  if constexpr (WHAT == DISPATCH) return launch_dependent(dispatch_kernel<DT, WIDE>, grid, THREADS, stream, p);
+  else if constexpr (WHAT == COMBINE) return p.top <= 2 ? launch_dependent(combine_kernel<DT, WIDE, 2>, grid, THREADS, stream, p)
+                                      : p.top <= 4 ? launch_dependent(combine_kernel<DT, WIDE, 4>, grid, THREADS, stream, p)
+                                                   : launch_dependent(combine_kernel<DT, WIDE, 8>, grid, THREADS, stream, p);
+  else return launch_dependent(combine_grad_kernel<DT, WIDE>, grid, THREADS, stream, p);
 }
 
 template <int WHAT>

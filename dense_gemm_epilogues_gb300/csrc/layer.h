@@ -55,7 +55,8 @@ struct RouteParams {
   int32_t *counts, *offsets, *routed;   // experts, experts + 1 and 1 entries
   float* loss;               // or null
   // Of the forward pass.
-  int32_t blocks;            // CTAs that choose
+  int32_t blocks, warps;     // CTAs that choose, and their warps
+  int32_t per_warp;          // tokens of a warp
   int32_t* hist;             // blocks x (experts + 1): rows of every expert, tokens with any
   float* mass;               // blocks x experts: sums of the probabilities
   // Of the gradient.
@@ -66,6 +67,7 @@ struct RouteParams {
   int64_t ldd;
 };
 int route_blocks(int64_t tokens, int64_t experts, int sm_count);   // RouteParams::blocks
+int route_warps(int64_t experts);                                  // RouteParams::warps
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);
 cudaError_t launch_route_grad(const RouteParams& p, int sm_count, cudaStream_t stream);
 
@@ -81,6 +83,7 @@ struct ExchangeParams {
   void *out, *dweights;      // dispatch, combine_grad: sorted rows; combine: token rows
   int64_t ldo;
   int32_t vec;               // all rows can be read and written 16 bytes at a time
+  int32_t parts_shift;       // log2 of the warps that share a token (set by the launch)
   int32_t* err;
 };
 cudaError_t launch_dispatch(const ExchangeParams& p, int sm_count, cudaStream_t stream);

@@ -51,7 +51,7 @@ gemm_status_t exchange_of(const gemm_plan* plan, int64_t tokens, int64_t top, in
                           const int32_t* slots, ExchangeParams* p) {
   if (!is_type(plan->ab)) return GEMM_ERR_UNSUPPORTED;
   if (tokens < 0 || top <= 0 || rows < 0 || width < 0) return GEMM_ERR_INVALID_ARG;
-  if (top > kMaxTop || rows > kMaxDim || width > kMaxDim || tokens > kMaxDim / top) return GEMM_ERR_UNSUPPORTED;
+  if (top > kMaxTop || rows > kMaxDim || width > (int64_t(1) << 30) || tokens > kMaxDim / top) return GEMM_ERR_UNSUPPORTED;
   if (tokens > 0 && !slots) return GEMM_ERR_INVALID_ARG;
   std::memset(p, 0, sizeof(*p));
   p->tokens = tokens;
@@ -77,7 +77,9 @@ gemm_status_t check_linear(const gemm_plan* plan, gemm_layout_t lb, int64_t M, i
 int splits_of(int64_t M, int64_t N, int64_t K, int box_rows, int sm_count) {
   const int64_t num_kb = (K + TC_BK - 1) / TC_BK;
   const int64_t tiles = (N + 127) / 128 * ((M + box_rows - 1) / box_rows);
-  if (num_kb == 0 || tiles > sm_count) return 0;
+  if (num_kb == 0) return 0;
+  
+  if (tiles > sm_count) return 0;
   const int64_t splits = std::min<int64_t>({8, num_kb, 2 * (int64_t)sm_count / tiles});
   return splits >= 2 ? (int)splits : 0;
 }
@@ -311,6 +313,8 @@ gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, cons
   RouteParams p = routing_of(plan, tokens, experts, logits, ld, routing);
   p.mask = mask;
   p.blocks = route_blocks(tokens, experts, plan->sm_count);
+  p.warps = route_warps(experts);
+  p.per_warp = (int32_t)((tokens + (int64_t)p.blocks * p.warps - 1) / ((int64_t)p.blocks * p.warps));
   if (p.blocks > 1) {
     const size_t hist = align_up((size_t)p.blocks * (size_t)(experts + 1) * sizeof(int32_t), 256);
     s = ensure_ws(plan, hist + (size_t)p.blocks * (size_t)experts * sizeof(float), stream);
@@ -448,7 +452,7 @@ gemm_status_t gemm_clip_norm(gemm_plan_t plan, int64_t count, const gemm_tensor_
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   constexpr int64_t PART = ClipTensors::LARGE;
   const int64_t parts = std::max<int64_t>(1, (count + PART - 1) / PART);
-  gemm_status_t s = ensure_ws(plan, (size_t)parts * 4 * (size_t)plan->sm_count * sizeof(double), stream);
+  gemm_status_t s = ensure_ws(plan, (size_t)parts * 2 * (size_t)plan->sm_count * sizeof(double), stream);
   if (s != GEMM_OK) return s;
   ClipPass p{};
   p.chunk = clip_chunk(total, plan->sm_count);

@@ -21,7 +21,7 @@
 namespace gemmlib {
 namespace {
 
-constexpr int THREADS = 192;                       // producer warp, MMA warp, four that read the accumulator
+constexpr int THREADS = 320;                       // producer warp, MMA warp, eight that read the accumulator
 constexpr int A_BYTES = 128 * TC_BK * 2;           // 16 KiB: 128 columns of weights, 64 deep
 constexpr uint32_t MN_BOX_BYTES = 64 * TC_BK * 2;  // MN-major box: 64 columns, 64 deep
 constexpr int MAX_STAGES = 8;
@@ -198,58 +198,91 @@ __global__ void __launch_bounds__(THREADS) linear_split_kernel(const __grid_cons
     }
     __syncwarp();
   }
-  // All MMAs are complete (warp 1 has waited for them), all copies have landed: the ring is free.
-  __syncthreads();
-  tc_fence_after();
-  if (warp >= 2) {
-    const int q = warp & 3;
-    for (int c = 0; c < n_mma; c += 32) {
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c, r);
-      tmem_wait_ld();
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (c + j < n_mma)   // [row][column of D]: a warp's lanes lie side by side
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (uint32_t)(((c + j) * 128 + q * 32 + lane) * 4)), "r"(r[j]) : "memory");
-    }
-    tc_fence_before();
-  }
-  __syncwarp();
-  cluster_sync();
-  // Four columns of a row at a time; this CTA's share of the tile's.
-  const int items = rows * 32;
-  const int64_t left = p.epi_n - m0;   // columns of D
+  // This CTA's share of the tile: four columns of a row at a time, a thread always the same
+  // columns.  The bias and the first of the residual come in while the weights stream.
+  const int items = rows * 32, lo = split * items / splits, hi = (split + 1) * items / splits;
+  const int first = lo + (int)threadIdx.x, col = (first & 31) * 4;
+  const int64_t d = m0 + col;
+  const int n = (int)max((int64_t)0, min((int64_t)4, p.epi_n - d));
   with_type(p.epi.d_dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    for (int i = split * items / splits + (int)threadIdx.x; i < (split + 1) * items / splits; i += THREADS) {
-      const int row = i >> 5, col = (i & 31) * 4;
-      const int n = (int)min((int64_t)4, left - col);
-      if (n <= 0) continue;
-      const uint32_t at = base + (uint32_t)((row * 128 + col) * 4);
-      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-      for (int s = 0; s < splits; ++s) {
-        const float4 v = lds_cluster(mapa_shared(at, (uint32_t)s));
-        x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
-      }
-      const int64_t d = m0 + col;
-      if (p.epi.bias_mode == GEMM_BIAS_COL) {
+    constexpr int U = 2;   // items under way (four cost every call 0.6 us: more code to fetch)
+    float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, res[U][4];
+    if (p.epi.bias_mode == GEMM_BIAS_COL) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < n) x[j] += load_as_float(p.epi.bias, p.epi.bias_dtype, d + j);
+      for (int j = 0; j < 4; ++j)
+        if (j < n) bias[j] = load_as_float(p.epi.bias, p.epi.bias_dtype, d + j);
+    }
+    auto load_residual = [&](int i0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * THREADS;
+        if (p.linear.residual != nullptr && i < hi) {
+          load4<DT>(p.linear.residual, (r0 + (i >> 5)) * p.linear.ldr + d, n, p.vec, res[u]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) res[u][j] = 0.0f;
+        }
       }
-      if (p.linear.pre != nullptr) store4<DT>(p.linear.pre, (r0 + row) * p.linear.ldp + d, n, p.vec, x);
+    };
+    load_residual(first);
+    // All MMAs are complete (warp 1 has waited for them), all copies have landed: the ring is free.
+    __syncthreads();
+    tc_fence_after();
+    if (warp >= 2) {
+      const int q = warp & 3;
+      for (int c = (warp - 2) >> 2 << 5; c < n_mma; c += 64) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c + j < n_mma)   // [row][column of D]: a warp's lanes lie side by side
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (uint32_t)(((c + j) * 128 + q * 32 + lane) * 4)), "r"(r[j]) : "memory");
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync();
+    for (int i0 = first; i0 < hi; i0 += U * THREADS) {
+      float x[U][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[u][j] = 0.0f;
+      for (int s = 0; s < splits; ++s) {   // in the order of K
+        const uint32_t from = mapa_shared(base, (uint32_t)s);
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u * THREADS < hi) v[u] = lds_cluster(from + (uint32_t)((((i0 + u * THREADS) >> 5) * 128 + col) * 4));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u * THREADS < hi) x[u][0] += v[u].x, x[u][1] += v[u].y, x[u][2] += v[u].z, x[u][3] += v[u].w;
+      }
+      if (p.linear.pre != nullptr || p.epi.bias_mode == GEMM_BIAS_COL) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[u][j] += bias[j];
+          const int i = i0 + u * THREADS;
+          if (p.linear.pre != nullptr && i < hi) store4<DT>(p.linear.pre, (r0 + (i >> 5)) * p.linear.ldp + d, n, p.vec, x[u]);
+        }
+      }
       with_act(p.linear.act, [&](auto act) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = activate<decltype(act)::value>(x[j]);
-      });
-      if (p.linear.residual != nullptr) {
-        float r[4];
-        load4<DT>(p.linear.residual, (r0 + row) * p.linear.ldr + d, n, p.vec, r);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] += r[j];
+          for (int j = 0; j < 4; ++j) x[u][j] = activate<decltype(act)::value>(x[u][j]);
+      });
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * THREADS;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[u][j] += res[u][j];
+        if (i < hi) store4<DT>(p.epi.D, (r0 + (i >> 5)) * p.epi.ldd + d, n, p.vec, x[u]);
       }
-      store4<DT>(p.epi.D, (r0 + row) * p.epi.ldd + d, n, p.vec, x);
+      if (p.linear.residual != nullptr && i0 + U * THREADS < hi) load_residual(i0 + U * THREADS);
     }
   });
   __syncwarp();
@@ -340,8 +373,13 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* partials,
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= N) return;
   float s = 0.0f;
-#pragma unroll 8
-  for (int b = 0; b < blocks; ++b) s += partials[(int64_t)b * N + c];
+  for (int b = 0; b < blocks; b += 16) {   // (16 loads under way)
+    float v[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) v[u] = b + u < blocks ? partials[(int64_t)(b + u) * N + c] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) s += v[u];
+  }
   out[c] = s;
 }
 

@@ -10,9 +10,9 @@
 //
 // Two launches.  The first chooses: a warp takes one token at a time, a lane experts lane,
 // lane + 32, ...; each of the `top` turns is one warp maximum of a key that orders like the
-// logits and one warp minimum of the index.  A lane keeps the counts and the sums of p of
-// its own experts in registers over all tokens of its warp, so a choice's number among its
-// warp's rows is known when it is made.  Warps take tokens in order, CTAs too; a CTA adds up
+// logits and one warp minimum of the index.  A lane keeps the sums of p of its own experts in
+// registers over all tokens of its warp, which counts its experts' rows in shared memory, so
+// a choice's number among its warp's rows is known when it is made.  Warps take tokens in order, CTAs too; a CTA adds up
 // its warps' counts and leaves its own in scratch.  The second launch places: every CTA adds
 // the counts of the CTAs before it (B x E integers, from L2) to its tokens' numbers, and one
 // more CTA adds up the loss.  Nothing waits for another CTA and no atomics decide an order,
@@ -23,8 +23,10 @@
 namespace gemmlib {
 namespace {
 
-constexpr int WARPS = 16;
-constexpr int THREADS = 32 * WARPS;
+// Warps of a CTA: 32 where a lane's experts leave room in the registers.
+__host__ __device__ constexpr int warps_of(int values) { return values <= 4 ? 32 : 16; }
+constexpr int MAX_WARPS = 32;
+constexpr int PLACE_THREADS = 1024;
 constexpr uint32_t LOWEST = 0x007fffffu;   // the key of -inf
 
 // Orders like the float: -inf lowest, zeros alike, NaN highest.
@@ -34,26 +36,32 @@ __device__ __forceinline__ uint32_t key_of(float z) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// The tokens of warp `w` of `warps`: in order, equal parts.
-__device__ __forceinline__ void token_range(int64_t tokens, int64_t warps, int64_t w, int64_t& lo, int64_t& hi) {
-  const int64_t per = (tokens + warps - 1) / warps;
-  lo = min(tokens, w * per);
-  hi = min(tokens, lo + per);
+// exp(x) for x <= 0, by the hardware's power of two: off by 2 steps and |x| 2^-24.
+__device__ __forceinline__ float exp_fast(float x) { return exp2_fast(LOG2_E * x); }
+
+// The tokens of warp `w`: in order, equal parts.
+__device__ __forceinline__ void token_range(const RouteParams& p, int w, int64_t& lo, int64_t& hi) {
+  lo = min(p.tokens, (int64_t)w * p.per_warp);
+  hi = min(p.tokens, lo + p.per_warp);
 }
 
 // z of a token: lane's experts; -inf where there is none.
-template <int V>
+template <int V, int DT>
 __device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int lane, float (&z)[V]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = lane + 32 * v;
-    z[v] = e < p.experts ? load_as_float(p.logits, p.dtype, t * p.ld + e) : -INFINITY;
+    z[v] = e < p.experts ? load_as_float(p.logits, DT, t * p.ld + e) : -INFINITY;
   }
 }
 
@@ -63,10 +71,10 @@ __device__ __forceinline__ float softmax(const float (&z)[V], float m, float (&e
   float s = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    e[v] = expf(z[v] - m);
+    e[v] = exp_fast(z[v] - m);
     s += e[v];
   }
-  return 1.0f / warp_sum(s);
+  return rcp_fast(warp_sum(s));
 }
 
 // Where experts begin: an exclusive sum of counts[0 .. E) into starts[0 .. E], by one warp.
@@ -86,50 +94,59 @@ __device__ __forceinline__ void scan_counts(const int* counts, int* starts, int 
 }
 
 // The loss from the counts and the sums of p over all tokens, by one warp.
-__device__ __forceinline__ void write_loss(const RouteParams& p, const int* counts, const double* mass, int rows,
+__device__ __forceinline__ void write_loss(const RouteParams& p, const int* counts, const float* mass, int rows,
                                            int routed, int lane) {
-  double s = 0.0;
-  for (int e = lane; e < p.experts; e += 32) s += (double)counts[e] * mass[e];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0 && p.loss != nullptr)
-    *p.loss = rows > 0 ? (float)(s * (double)p.experts / ((double)rows * (double)routed)) : 0.0f;
+  float s = 0.0f;
+  if (rows > 0) {
+    const float scale = (float)p.experts / (float)rows;
+    for (int e = lane; e < p.experts; e += 32) s += (float)counts[e] * scale * (mass[e] / (float)routed);
+  }
+  s = warp_sum(s);
+  if (lane == 0 && p.loss != nullptr) *p.loss = s;
 }
 
 // Chooses.  Dynamic shared memory: WARPS x E counts, then sums of p.
-template <int V>
-__global__ void __launch_bounds__(THREADS) route_choose_kernel(const __grid_constant__ RouteParams p) {
+template <int V, int DT>
+__global__ void __launch_bounds__(32 * warps_of(V)) route_choose_kernel(const __grid_constant__ RouteParams p) {
+  constexpr int WARPS = warps_of(V), THREADS = 32 * WARPS;
   extern __shared__ int smem[];
   const int E = p.experts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* counts = smem;                                             // [WARPS][E]
   float* mass = reinterpret_cast<float*>(smem + WARPS * E);       // [WARPS][E]
-  __shared__ int tokens_of[WARPS];
+  __shared__ int tokens_of[MAX_WARPS];
   pdl_launch_dependents();
   pdl_wait();
   int64_t lo, hi;
-  token_range(p.tokens, (int64_t)gridDim.x * WARPS, (int64_t)blockIdx.x * WARPS + warp, lo, hi);
-  int cnt[V];
+  token_range(p, (int)blockIdx.x * WARPS + warp, lo, hi);
   float sum[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) cnt[v] = 0, sum[v] = 0.0f;
+  for (int v = 0; v < V; ++v) {
+    sum[v] = 0.0f;
+    if (lane + 32 * v < E) counts[warp * E + lane + 32 * v] = 0;
+  }
+  __syncwarp();
   int routed = 0;
   constexpr bool AHEAD = V <= 8;   // the next token's logits come in during this one's turns (registers allow it)
   float z[V], ahead[AHEAD ? V : 1];
   if constexpr (AHEAD) {
-    if (lo < hi) load_logits<V>(p, lo, lane, ahead);
+    if (lo < hi) load_logits<V, DT>(p, lo, lane, ahead);
   }
+  auto masked = [&](int64_t t) { return p.mask != nullptr && p.mask[t] == 0; };
+  bool mask_ahead = lo < hi && masked(lo);
   for (int64_t t = lo; t < hi; ++t) {
     if constexpr (AHEAD) {
 #pragma unroll
       for (int v = 0; v < V; ++v) z[v] = ahead[v];
-      if (t + 1 < hi) load_logits<V>(p, t + 1, lane, ahead);
+      if (t + 1 < hi) load_logits<V, DT>(p, t + 1, lane, ahead);
     } else {
-      load_logits<V>(p, t, lane, z);
+      load_logits<V, DT>(p, t, lane, z);
     }
     // Choice j is kept by lane j.
     int expert = -1, number = -1;
-    float value = -INFINITY, first = 0.0f;
-    const bool counts_in = p.mask == nullptr || p.mask[t] != 0;
+    uint32_t mine_key = LOWEST;
+    const bool counts_in = !mask_ahead;
+    mask_ahead = t + 1 < hi && masked(t + 1);
+    uint32_t top_key = 0u;
     if (counts_in) {
       uint32_t key[V];
 #pragma unroll
@@ -140,25 +157,23 @@ __global__ void __launch_bounds__(THREADS) route_choose_kernel(const __grid_cons
         for (int v = 1; v < V; ++v) best = max(best, key[v]);
         const uint32_t most = __reduce_max_sync(0xffffffffu, best);
         if (most <= LOWEST) break;
-        int mine = 0x7fffffff;
-        float at = 0.0f;
+        unsigned own = 0xffffffffu;
 #pragma unroll
         for (int v = V - 1; v >= 0; --v)
-          if (key[v] == most) mine = lane + 32 * v, at = z[v];
-        const int e = (int)__reduce_min_sync(0xffffffffu, (unsigned)mine);
-        int rank = 0;
+          if (key[v] == most) own = (unsigned)(lane + 32 * v);
+        const unsigned e = __reduce_min_sync(0xffffffffu, own);
+        if (own == e) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (e == lane + 32 * v) {
-            rank = cnt[v]++;
-            key[v] = 0u;
-          }
-        rank = __shfl_sync(0xffffffffu, rank, e & 31);
-        at = __shfl_sync(0xffffffffu, at, e & 31);
-        if (j == 0) first = at;
-        if (lane == j) expert = e, number = rank, value = at;
+          for (int v = 0; v < V; ++v)
+            if (e == (unsigned)(lane + 32 * v)) key[v] = 0u;
+        }
+        if (j == 0) top_key = most;
+        if (lane == j) expert = (int)e, mine_key = most;
       }
+      if (expert >= 0) number = counts[warp * E + expert]++;   // (a token's experts differ)
+      __syncwarp();
     }
+    const float first = value_of(top_key), value = value_of(mine_key);
     const bool any = __shfl_sync(0xffffffffu, expert, 0) >= 0;
     float w = 0.0f;
     if (any) {
@@ -167,8 +182,8 @@ __global__ void __launch_bounds__(THREADS) route_choose_kernel(const __grid_cons
       const float inv = softmax<V>(z, first, e);
 #pragma unroll
       for (int v = 0; v < V; ++v) sum[v] += e[v] * inv;
-      w = expert >= 0 ? expf(value - first) : 0.0f;
-      w = p.renormalize ? w / warp_sum(w) : w * inv;
+      w = expert >= 0 ? exp_fast(value - first) : 0.0f;
+      w *= p.renormalize ? rcp_fast(warp_sum(w)) : inv;
     }
     if (lane < p.top) {
       const int64_t i = t * p.top + lane;
@@ -180,34 +195,32 @@ __global__ void __launch_bounds__(THREADS) route_choose_kernel(const __grid_cons
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = lane + 32 * v;
-    if (e < E) {
-      counts[warp * E + e] = cnt[v];
-      mass[warp * E + e] = sum[v];
-    }
+    if (e < E) mass[warp * E + e] = sum[v];
   }
   if (lane == 0) tokens_of[warp] = routed;
   __syncthreads();
-  // The warps' counts become the numbers that their rows start at; row 0 takes the CTA's.
+  // The warps' counts become the numbers that their rows start at.
   const bool alone = gridDim.x == 1;
-  int* starts = reinterpret_cast<int*>(mass + WARPS * E);         // alone: [E + 1]
-  int* all = starts + E + 1;                                      // alone: [E]
-  double* dmass = reinterpret_cast<double*>(smem + ((2 * WARPS * E + 2 * E + 2) & ~1));   // alone: [E]
+  int* starts = reinterpret_cast<int*>(mass + WARPS * E);   // alone: [E + 1]
+  int* all = starts + E + 1;                                // alone: [E]
+  float* total = reinterpret_cast<float*>(all + E);         // alone: [E]
   for (int e = threadIdx.x; e < E; e += THREADS) {
     int n = 0;
-    double m = 0.0;
+    float m = 0.0f;
+#pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       const int c = counts[w * E + e];
       counts[w * E + e] = n;
       n += c;
-      m += (double)mass[w * E + e];
+      m += mass[w * E + e];
     }
     if (alone) {
       all[e] = n;
-      dmass[e] = m;
+      total[e] = m;
       p.counts[e] = n;
     } else {
       p.hist[(int64_t)blockIdx.x * (E + 1) + e] = n;
-      p.mass[(int64_t)blockIdx.x * E + e] = (float)m;
+      p.mass[(int64_t)blockIdx.x * E + e] = m;
     }
   }
   if (threadIdx.x == 0) {
@@ -222,24 +235,22 @@ __global__ void __launch_bounds__(THREADS) route_choose_kernel(const __grid_cons
     if (warp == 0) {
       scan_counts(all, starts, E, lane);
       __syncwarp();
-      write_loss(p, all, dmass, starts[E], tokens_of[0], lane);
+      write_loss(p, all, total, starts[E], tokens_of[0], lane);
     }
     __syncthreads();
     for (int e = threadIdx.x; e <= E; e += THREADS) p.offsets[e] = starts[e];
   }
-  // (a warp's own slots: the lane that wrote an entry reads it)
-  for (int64_t t = lo; t < hi; ++t) {
-    if (lane < p.top) {
-      const int64_t i = t * p.top + lane;
-      const int e = p.chosen[i];
-      if (e >= 0) p.slots[i] += counts[warp * E + e] + (alone ? starts[e] : 0);
-    }
+  // The warp's own slots.
+#pragma unroll 2
+  for (int64_t i = lo * p.top + lane; i < hi * p.top; i += 32) {
+    const int e = p.chosen[i], number = p.slots[i];
+    if (e >= 0) p.slots[i] = number + counts[warp * E + e] + (alone ? starts[e] : 0);
   }
 }
 
 // Places.  CTA b < p.blocks adds what lies before its rows to its tokens' numbers; the last
-// CTA writes the counts, offsets and the loss.
-__global__ void __launch_bounds__(THREADS) route_place_kernel(const __grid_constant__ RouteParams p) {
+// CTA writes the counts, offsets and the loss.  Dynamic shared memory: see place_smem.
+__global__ void __launch_bounds__(PLACE_THREADS) route_place_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ int smem[];
   const int E = p.experts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x;
@@ -247,74 +258,89 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(const __grid_const
   int* all = smem;             // [E + 1] all rows of an expert; tokens with any
   int* before = all + E + 1;   // [E] those of the CTAs before this one
   int* starts = before + E;    // [E + 1]
-  double* dmass = reinterpret_cast<double*>(smem + ((3 * E + 3) & ~1));   // last CTA: [E]
+  float* mass = reinterpret_cast<float*>(starts + E + 1);   // last CTA: [groups][E]
   pdl_launch_dependents();
-  for (int e = threadIdx.x; e < 2 * E + 1; e += THREADS) smem[e] = 0;
+  for (int e = threadIdx.x; e < 2 * E + 1; e += PLACE_THREADS) smem[e] = 0;
   __syncthreads();
   pdl_wait();
-  // Rows of the table are shared out over groups of threads as wide as the table.
-  const int cols = E + 1, width = (cols + 31) / 32 * 32, groups = max(1, THREADS / width);
+  // The table's rows are shared out over groups of threads as wide as the table, so that each
+  // thread reads few of them, all under way at once.
+  const int cols = E + 1, width = (cols + 31) / 32 * 32, groups = max(1, PLACE_THREADS / width);
   const int g = (int)threadIdx.x / width;
-  for (int c = (int)threadIdx.x % width; g < groups && c < cols; c += width * groups >= THREADS ? THREADS : width) {
+  const int step = width >= PLACE_THREADS ? PLACE_THREADS : width * groups;
+  for (int c = (int)threadIdx.x % width; g < groups && c < cols; c += step) {
     int sum = 0, part = 0;
-#pragma unroll 8
-    for (int r = g; r < p.blocks; r += groups) {
-      const int n = __ldcg(p.hist + (int64_t)r * cols + c);
-      sum += n;
-      part += r < b ? n : 0;
+    float m = 0.0f;
+    for (int r0 = g; r0 < p.blocks; r0 += 16 * groups) {
+      int n[16];
+      float f[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int r = r0 + u * groups;
+        n[u] = r < p.blocks ? __ldcg(p.hist + (int64_t)r * cols + c) : 0;
+        f[u] = last && r < p.blocks && c < E ? __ldcg(p.mass + (int64_t)r * E + c) : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        sum += n[u];
+        part += r0 + u * groups < b ? n[u] : 0;
+        m += f[u];
+      }
     }
     atomicAdd(&all[c], sum);   // (integers: any order)
-    if (c < E) atomicAdd(&before[c], part);
-  }
-  if (last) {
-    for (int e = threadIdx.x; e < E; e += THREADS) {
-      double m = 0.0;
-#pragma unroll 8
-      for (int r = 0; r < p.blocks; ++r) m += (double)__ldcg(p.mass + (int64_t)r * E + e);
-      dmass[e] = m;
+    if (c < E) {
+      atomicAdd(&before[c], part);
+      if (last) mass[g * E + c] = m;
     }
   }
   __syncthreads();
-  if (warp == 0) {
-    scan_counts(all, starts, E, lane);
-    __syncwarp();
-    if (last) write_loss(p, all, dmass, starts[E], all[E], lane);
+  if (last && (int)threadIdx.x < E) {
+    for (int e = threadIdx.x; e < E; e += PLACE_THREADS)
+      for (int h = 1; h < groups; ++h) mass[e] += mass[h * E + e];
   }
+  if (warp == PLACE_THREADS / 32 - 1) scan_counts(all, starts, E, lane);
   __syncthreads();
   if (last) {
-    for (int e = threadIdx.x; e <= E; e += THREADS) {
+    if (warp == 0) write_loss(p, all, mass, starts[E], all[E], lane);
+    for (int e = threadIdx.x; e <= E; e += PLACE_THREADS) {
       if (e < E) p.counts[e] = all[e];
       else *p.routed = all[E];
       p.offsets[e] = starts[e];
     }
     return;
   }
-  int64_t lo, hi, t1;
-  token_range(p.tokens, (int64_t)p.blocks * WARPS, (int64_t)b * WARPS, lo, t1);
-  token_range(p.tokens, (int64_t)p.blocks * WARPS, (int64_t)b * WARPS + WARPS - 1, t1, hi);
-  for (int64_t i = lo * p.top + threadIdx.x; i < hi * p.top; i += THREADS) {
+  int64_t lo, hi, t;
+  token_range(p, b * p.warps, lo, t);
+  token_range(p, b * p.warps + p.warps - 1, t, hi);
+  for (int64_t i = lo * p.top + threadIdx.x; i < hi * p.top; i += PLACE_THREADS) {
     const int e = p.chosen[i];
     if (e >= 0) p.slots[i] += starts[e] + before[e];
   }
 }
 
+size_t place_smem(int experts) {
+  const int width = (experts + 1 + 31) / 32 * 32, groups = std::max(1, PLACE_THREADS / width);
+  return (size_t)(3 * experts + 2 + groups * experts) * sizeof(int);
+}
+
 // dz_i = [renormalised: w_i (dw_i - sum_j w_j dw_j) at the chosen] + p_i (g_i - sum p g),
 // g_e = dloss E c_e / (C n) [+ dw_e at the chosen].  A warp takes one token at a time.
-template <int V>
-__global__ void __launch_bounds__(THREADS) route_grad_kernel(const __grid_constant__ RouteParams p) {
+template <int V, int DT>
+__global__ void __launch_bounds__(512) route_grad_kernel(const __grid_constant__ RouteParams p) {
+  constexpr int WARPS = 16;
   const int E = p.experts, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
   const int n = *p.routed, rows = p.offsets[E];
   const float dloss = p.dloss_scale * (p.dloss != nullptr ? *p.dloss : 1.0f);
-  const float per_row = rows > 0 && n > 0 ? (float)((double)dloss * E / ((double)rows * (double)n)) : 0.0f;
+  const float per_row = rows > 0 && n > 0 ? dloss / (float)n * ((float)E / (float)rows) : 0.0f;
   float share[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) share[v] = lane + 32 * v < E ? per_row * (float)p.counts[lane + 32 * v] : 0.0f;
   const int64_t warps = (int64_t)gridDim.x * WARPS;
   for (int64_t t = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); t < p.tokens; t += warps) {
     float z[V], e[V], g[V], direct[V];
-    load_logits<V>(p, t, lane, z);
+    load_logits<V, DT>(p, t, lane, z);
     int expert = -1;
     float w = 0.0f, dw = 0.0f;
     if (lane < p.top) {
@@ -326,11 +352,10 @@ __global__ void __launch_bounds__(THREADS) route_grad_kernel(const __grid_consta
       }
     }
     const bool any = __shfl_sync(0xffffffffu, expert, 0) >= 0;
-    float m = z[0];
+    uint32_t most = key_of(z[0]);
 #pragma unroll
-    for (int v = 1; v < V; ++v) m = fmaxf(m, z[v]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int v = 1; v < V; ++v) most = max(most, key_of(z[v]));
+    const float m = value_of(__reduce_max_sync(0xffffffffu, most));
     const float inv = softmax<V>(z, m, e);
     // What a choice adds: to dz at once (renormalised), or to dL/dp.
     const float add = p.renormalize ? w * (dw - warp_sum(w * dw)) : dw;
@@ -362,29 +387,36 @@ __global__ void __launch_bounds__(THREADS) route_grad_kernel(const __grid_consta
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (lane + 32 * v < E)
-        store_float_as(p.dlogits, p.dtype, t * p.ldd + lane + 32 * v, any ? direct[v] + e[v] * (g[v] - s) : 0.0f);
+        store_float_as(p.dlogits, DT, t * p.ldd + lane + 32 * v, any ? direct[v] + e[v] * (g[v] - s) : 0.0f);
   }
 }
 
-template <typename F>
+template <int DT, typename F>
 cudaError_t with_values(int experts, F&& f) {
-  if (experts <= 32) return f(TypeTag<1>{});
-  if (experts <= 64) return f(TypeTag<2>{});
-  if (experts <= 128) return f(TypeTag<4>{});
-  if (experts <= 256) return f(TypeTag<8>{});
-  if (experts <= 512) return f(TypeTag<16>{});
-  return f(TypeTag<32>{});
+  if (experts <= 32) return f(TypeTag<1>{}, TypeTag<DT>{});
+  if (experts <= 64) return f(TypeTag<2>{}, TypeTag<DT>{});
+  if (experts <= 128) return f(TypeTag<4>{}, TypeTag<DT>{});
+  if (experts <= 256) return f(TypeTag<8>{}, TypeTag<DT>{});
+  if (experts <= 512) return f(TypeTag<16>{}, TypeTag<DT>{});
+  return f(TypeTag<32>{}, TypeTag<DT>{});
+}
+template <typename F>
+cudaError_t with_values(const RouteParams& p, F&& f) {
+  if (p.dtype == GEMM_F32) return with_values<GEMM_F32>(p.experts, f);
+  if (p.dtype == GEMM_F16) return with_values<GEMM_F16>(p.experts, f);
+  return with_values<GEMM_BF16>(p.experts, f);
 }
 
 template <typename... P>
-cudaError_t launch_smem(void (*kernel)(P...), int grid, size_t smem, cudaStream_t stream, const RouteParams& p) {
+cudaError_t launch_smem(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t stream,
+                        const RouteParams& p) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -397,27 +429,29 @@ cudaError_t launch_smem(void (*kernel)(P...), int grid, size_t smem, cudaStream_
 
 }  // namespace
 
-// CTAs that choose: one for up to 64 tokens (four per warp: one launch takes less than two),
-// else one per SM as long as a warp has a token.
+// CTAs that choose: one for up to 64 tokens (two or four per warp: one launch takes less than
+// two), else one per SM as long as a warp has a token.
+int route_warps(int64_t experts) { return warps_of(experts <= 32 ? 1 : experts <= 64 ? 2 : experts <= 128 ? 4 : 8); }
 int route_blocks(int64_t tokens, int64_t experts, int sm_count) {
-  (void)experts;
-  if (tokens <= 4 * WARPS) return 1;
-  return (int)std::min<int64_t>(sm_count, (tokens + WARPS - 1) / WARPS);
+  if (tokens <= 64) return 1;
+  const int warps = route_warps(experts);
+  return (int)std::min<int64_t>(sm_count, (tokens + warps - 1) / warps);
 }
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
   const size_t E = (size_t)p.experts;
-  const cudaError_t e = with_values(p.experts, [&](auto v) {
-    return launch_smem(route_choose_kernel<decltype(v)::value>, p.blocks, (2 * WARPS * E + 4 * E + 6) * 4, stream, p);
+  const cudaError_t e = with_values(p, [&](auto v, auto dt) {
+    constexpr int V = decltype(v)::value, WARPS = warps_of(V);
+    return launch_smem(route_choose_kernel<V, decltype(dt)::value>, p.blocks, 32 * WARPS, (2 * WARPS * E + 3 * E + 1) * 4, stream, p);
   });
   if (e != cudaSuccess || p.blocks == 1) return e;
-  return launch_smem(route_place_kernel, p.blocks + 1, (5 * E + 6) * 4, stream, p);
+  return launch_smem(route_place_kernel, p.blocks + 1, PLACE_THREADS, place_smem(p.experts), stream, p);
 }
 
 cudaError_t launch_route_grad(const RouteParams& p, int sm_count, cudaStream_t stream) {
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(2 * (int64_t)sm_count, (p.tokens + WARPS - 1) / WARPS));
-  return with_values(p.experts, [&](auto v) {
-    return launch_smem(route_grad_kernel<decltype(v)::value>, grid, 0, stream, p);
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(4 * (int64_t)sm_count, (p.tokens + 15) / 16));
+  return with_values(p, [&](auto v, auto dt) {
+    return launch_smem(route_grad_kernel<decltype(v)::value, decltype(dt)::value>, grid, 512, 0, stream, p);
   });
 }
 

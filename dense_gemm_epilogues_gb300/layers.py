@@ -25,6 +25,11 @@ _ACTS = {None: GEMM_LINEAR_NONE, "relu": GEMM_LINEAR_RELU, "gelu": GEMM_LINEAR_G
          "gelu_tanh": GEMM_LINEAR_GELU_TANH, "silu": GEMM_LINEAR_SILU}
 
 
+def _ld(t, cols: int, name: str) -> int:
+    """The pitch of a row-major 2-D tensor."""
+    return (cols or 1) if t.is_contiguous() else _pitch(t.shape, t.stride(), name)
+
+
 # ------------------------- fully connected layers ---------------------------
 
 def _act(name) -> int:
@@ -48,7 +53,7 @@ def _like(t, shape, dtype, name: str) -> int:
     """The pitch of a row-major tensor that must have this shape and type."""
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {str(dtype)[6:]} of shape {tuple(shape)}")
-    return _pitch(shape, t.stride(), name)
+    return _ld(t, shape[1], name)
 
 
 def linear(x, w, *, bias=None, activation: Optional[str] = None, residual=None, save_pre: bool = False, out=None,
@@ -68,7 +73,7 @@ def linear(x, w, *, bias=None, activation: Optional[str] = None, residual=None, 
         raise ValueError("x must be [rows, K] and w [K, N] of the same type")
     act = _act(activation)
     layout, ldb = _weights(w, K, N)
-    lda = _pitch((M, K), x.stride(), "x")
+    lda = _ld(x, K, "x")
     device = _device(x, w, bias, residual, out)
     if out is None:
         out_dtype = out_dtype or dtype
@@ -257,61 +262,72 @@ def route_grad(logits, routing: Routing, *, dweights=None, dloss=None, out=None,
     return out
 
 
-def _exchange(routing, x, out, rows: int, *others):
-    """(tokens, top, width, device, out) of an exchange: x [.., width], out [rows, width] of x's type."""
-    shape = routing.slots.shape
-    if len(shape) != 2 or x.dim() != 2:
-        raise ValueError("rows must be [rows, width] and slots [tokens, top]")
-    _flat(routing.slots, _I32, shape, "slots")
-    width = x.shape[1]
+def _slots(routing):
+    """The slots of a routing and their shape."""
+    slots = routing.slots
+    shape = slots.shape
+    if slots.dtype is not _I32 or len(shape) != 2 or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int32 tensor [tokens, top]")
+    return slots, shape
+
+
+def _rows_out(out, rows: int, width: int, like):
     if out is None:
-        out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
-    elif out.shape != (rows, width) or out.dtype is not x.dtype:
+        return torch.empty((rows, width), dtype=like.dtype, device=like.device), width or 1
+    if out.shape != (rows, width) or out.dtype is not like.dtype:
         raise ValueError("out must be [rows, width] of the rows' type")
-    return shape[0], shape[1], width, _device(x, out, routing.slots, *others), out
+    return out, _ld(out, width, "out")
 
 
-def _used(routing):
+def _used(routing) -> int:
+    """Where the number of rows in use stands: the last offset."""
     e = routing.offsets
-    if e.dtype is not _I32 or e.dim() != 1 or e.stride(0) != 1 or e.shape[0] < 1:
+    if e.dtype is not _I32 or e.dim() != 1 or not e.is_contiguous() or e.numel() < 1:
         raise ValueError("offsets must be a contiguous int32 tensor")
-    return e.data_ptr() + 4 * (e.shape[0] - 1)
+    return e.data_ptr() + 4 * (e.numel() - 1)
 
 
 def dispatch(x, routing: Routing, *, out=None, plan: Optional[Plan] = None, stream=None):
     """Every token's row to the places of its experts' rows (gemm_dispatch): [tokens * top, width]
     rows sorted by expert, those behind the last used one zero.  x: [tokens, width] float32,
     float16 or bfloat16 with contiguous rows."""
-    rows = out.shape[0] if out is not None else routing.slots.numel()
-    tokens, top, width, device, out = _exchange(routing, x, out, rows, routing.offsets)
-    if x.shape[0] != tokens:
+    slots, (tokens, top) = _slots(routing)
+    n, width = x.shape
+    if n != tokens:
         raise ValueError("x must have one row per token")
+    used, ldx = _used(routing), _ld(x, width, "x")
+    rows = tokens * top if out is None else out.shape[0]
+    out, ldo = _rows_out(out, rows, width, x)
+    device = _device(x, out, slots, routing.offsets)
     stream = _raw_stream(device) if stream is None else stream
     plan = _plan_for(plan, _code(x.dtype), GEMM_F32, device, stream)
-    status = _LIB.gemm_dispatch(plan.handle, tokens, top, rows, width, x.data_ptr(), _pitch(x.shape, x.stride(), "x"),
-                                routing.slots.data_ptr(), _used(routing), out.data_ptr(),
-                                _pitch(out.shape, out.stride(), "out"), stream)
+    status = _LIB.gemm_dispatch(plan.handle, tokens, top, rows, width, x.data_ptr(), ldx, slots.data_ptr(), used,
+                                out.data_ptr(), ldo, stream)
     if status:
         raise GemmError(status, "gemm_dispatch")
     return out
 
 
 def _combine(y, routing, weights, residual, out, plan, stream):
-    tokens, top, width, device, out = _exchange(routing, y, out, routing.slots.shape[0], weights, residual)
-    if weights is not None:
-        _flat(weights, _F32, (tokens, top), "weights")
+    slots, shape = _slots(routing)
+    tokens, top = shape
+    rows, width = y.shape
+    w = r = None
     ldr = 0
+    if weights is not None:
+        _flat(weights, _F32, shape, "weights")
+        w = weights.data_ptr()
     if residual is not None:
         if residual.shape != (tokens, width) or residual.dtype is not y.dtype:
             raise ValueError("residual must be [tokens, width] of y's type")
-        ldr = _pitch(residual.shape, residual.stride(), "residual")
+        r, ldr = residual.data_ptr(), _ld(residual, width, "residual")
+    ldy = _ld(y, width, "y")
+    out, ldo = _rows_out(out, tokens, width, y)
+    device = _device(y, out, slots, weights, residual)
     stream = _raw_stream(device) if stream is None else stream
     plan = _plan_for(plan, _code(y.dtype), GEMM_F32, device, stream)
-    status = _LIB.gemm_combine(plan.handle, tokens, top, y.shape[0], width, y.data_ptr(),
-                               _pitch(y.shape, y.stride(), "y"), routing.slots.data_ptr(),
-                               weights.data_ptr() if weights is not None else None,
-                               residual.data_ptr() if residual is not None else None, ldr, out.data_ptr(),
-                               _pitch(out.shape, out.stride(), "out"), stream)
+    status = _LIB.gemm_combine(plan.handle, tokens, top, rows, width, y.data_ptr(), ldy, slots.data_ptr(), w, r, ldr,
+                               out.data_ptr(), ldo, stream)
     if status:
         raise GemmError(status, "gemm_combine")
     return out
@@ -335,19 +351,22 @@ def combine_grad(dout, y, routing: Routing, *, out=None, plan: Optional[Plan] = 
     """(dy, dweights) of combine (gemm_combine_grad): dy like y, rows behind the last used one
     zero; dweights [tokens, top] float32, 0 where there is no row.  The residual's gradient is
     dout itself.  out: where dy goes."""
-    rows = y.shape[0]
-    tokens, top, width, device, out = _exchange(routing, y, out, rows, dout, routing.weights, routing.offsets)
+    slots, shape = _slots(routing)
+    tokens, top = shape
+    rows, width = y.shape
     if dout.shape != (tokens, width) or dout.dtype is not y.dtype:
         raise ValueError("dout must be [tokens, width] of y's type")
-    _flat(routing.weights, _F32, (tokens, top), "weights")
-    dweights = torch.empty((tokens, top), dtype=_F32, device=y.device)
+    weights = routing.weights
+    _flat(weights, _F32, shape, "weights")
+    used, ldd, ldy = _used(routing), _ld(dout, width, "dout"), _ld(y, width, "y")
+    out, ldo = _rows_out(out, rows, width, y)
+    device = _device(y, out, slots, dout, weights, routing.offsets)
+    dweights = torch.empty(shape, dtype=_F32, device=y.device)
     stream = _raw_stream(device) if stream is None else stream
     plan = _plan_for(plan, _code(y.dtype), GEMM_F32, device, stream)
-    status = _LIB.gemm_combine_grad(plan.handle, tokens, top, rows, width, dout.data_ptr(),
-                                    _pitch(dout.shape, dout.stride(), "dout"), y.data_ptr(),
-                                    _pitch(y.shape, y.stride(), "y"), routing.slots.data_ptr(), _used(routing),
-                                    routing.weights.data_ptr(), out.data_ptr(),
-                                    _pitch(out.shape, out.stride(), "out"), dweights.data_ptr(), stream)
+    status = _LIB.gemm_combine_grad(plan.handle, tokens, top, rows, width, dout.data_ptr(), ldd, y.data_ptr(), ldy,
+                                    slots.data_ptr(), used, weights.data_ptr(), out.data_ptr(), ldo,
+                                    dweights.data_ptr(), stream)
     if status:
         raise GemmError(status, "gemm_combine_grad")
     return out, dweights
@@ -410,7 +429,9 @@ def _norm_of(tensors, max_norm: float, eps: float, scales: bool, plan, stream):
     device = tensors.device
     if device is None:
         device = plan.device if plan is not None else torch.cuda.current_device()
-    norm = torch.empty((), dtype=_F32, device=f"cuda:{device}")
+        norm = torch.empty((), dtype=_F32, device=f"cuda:{device}")
+    else:
+        norm = torch.empty((), dtype=_F32, device=tensors.tensors[0].device)
     stream = _raw_stream(device) if stream is None else stream
     if plan is None:
         plan = _plan_for(None, GEMM_F32, GEMM_F32, device, stream)

@@ -704,7 +704,7 @@ typedef struct {
  *     which is 1 for an even routing; the sum runs over the tokens that have any expert.
  *   mask        tokens bytes, 0: the token gets no expert and counts nowhere; NULL: all do.
  *   experts     1 .. 1024, tokens * top < 2^31 (else GEMM_ERR_UNSUPPORTED).
- * Softmax and sums are fp32, the loss's last sums fp64.
+ * Softmax and sums are fp32.
  * ------------------------------------------------------------------------- */
 gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ld,
                          const uint8_t* mask, const gemm_routing_t* routing, gemm_stream_t stream);

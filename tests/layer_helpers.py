@@ -29,12 +29,17 @@ def route_ref(logits, top, renormalize=True, mask=None):
     order = torch.where(z.isnan(), math.inf, z)
     nan = z.isnan()
     experts = torch.full((T, top), -1, dtype=torch.long)
-    for t in range(T):
-        if mask is not None and not bool(mask[t]):
-            continue
-        ranked = sorted((e for e in range(E) if order[t, e] != -math.inf),
-                        key=lambda e: (not bool(nan[t, e]), -float(order[t, e]), e))[:top]
-        experts[t, :len(ranked)] = torch.tensor(ranked, dtype=torch.long)
+    left = order.clone()
+    if mask is not None:
+        left[~mask.bool().cpu()] = -math.inf
+    index = torch.arange(E).expand(T, E)
+    for j in range(top):   # NaN before infinity, then by value, then by index
+        most = left.amax(1, keepdim=True)
+        ties = (left == most) & (most > -math.inf)
+        ties = torch.where((ties & nan).any(1, keepdim=True), ties & nan, ties)
+        first = torch.where(ties, index, E).amin(1)
+        experts[:, j] = torch.where(first < E, first, -1)
+        left = torch.where(index == first[:, None], -math.inf, left)
     chosen = experts >= 0
     any_ = chosen[:, :1]
     p = torch.where(any_, torch.softmax(torch.where(any_, z, 0.0), 1), 0.0)
@@ -43,14 +48,10 @@ def route_ref(logits, top, renormalize=True, mask=None):
         w = torch.where(chosen, w / w.sum(1, keepdim=True), 0.0)
     counts = torch.bincount(experts[chosen], minlength=E)
     offsets = torch.cat((torch.zeros(1, dtype=torch.long), counts.cumsum(0)))
-    slots = torch.full((T, top), -1, dtype=torch.long)
-    flat = experts.flatten()
-    at = offsets[:-1].clone()
-    for i in range(flat.numel()):
-        e = int(flat[i])
-        if e >= 0:
-            slots.view(-1)[i] = at[e]
-            at[e] += 1
+    flat = torch.where(chosen, experts, E).flatten()
+    places = torch.empty_like(flat)
+    places[torch.argsort(flat, stable=True)] = torch.arange(flat.numel())
+    slots = torch.where(chosen, places.view(T, top), -1)
     rows, routed = int(counts.sum()), int(any_.sum())
     loss = E * (counts * p.sum(0)).sum() / max(1, rows * routed) if rows else torch.tensor(0.0, dtype=torch.float64)
     finite = torch.where(torch.isfinite(z), z, 0.0)

@@ -9,10 +9,10 @@
 // substitution makes R, which falls from 1/2 like 1 / t, smooth up to k = 0.  Q of degree 8
 // was fitted here to erfcx by weighted least squares; in fp32 P is off by at most 2.3e-7, and
 // by 9e-7 of its value down to x = -4 (3.4e-6 at -9).  The derivative needs the same
-// exponential.  About 18 instructions, of which two on the special function unit, where
-// erfcf takes twice as many: the epilogue of a product of short depth would no longer hide
-// behind its MMAs.  Exponentials and quotients are the hardware's (2 steps of fp32).  All
-// keep NaN.
+// exponential.  Two numbers at a time (paired FMAs): about 11 issue slots and two special
+// functions each, where erfcf takes four times as many: the epilogue of a product of short
+// depth would no longer hide behind its MMAs, nor the gradient's pass behind its loads.
+// Exponentials and quotients are the hardware's (2 steps of fp32).  All keep NaN.
 #pragma once
 
 #include "common.cuh"
@@ -38,33 +38,56 @@ constexpr float LOG2_E = 1.4426950408889634f;
 // 1 / (1 + exp(-v))
 __device__ __forceinline__ float sigmoid_fast(float v) { return rcp_fast(1.0f + exp2_fast(-LOG2_E * v)); }
 
-// The normal distribution at x; e = exp(-x^2 / 2).
-__device__ __forceinline__ float normal_fast(float x, float& e) {
-  const float k = rcp_fast(fmaf(0.35f, fabsf(x), 1.0f));
-  e = exp2_fast(-0.5f * LOG2_E * x * x);
-  float q = fmaf(-0.0285310932f, k, 0.1412722766f);
-  q = fmaf(q, k, -0.2507375181f);
-  q = fmaf(q, k, 0.1541662067f);
-  q = fmaf(q, k, -0.0201176628f);
-  q = fmaf(q, k, 0.1044274792f);
-  q = fmaf(q, k, 0.1200617179f);
-  q = fmaf(q, k, 0.1398360431f);
-  q = fmaf(q, k, 0.1396225840f);
-  const float half = q * k * e;   // the distribution at -|x|
-  return x < 0.0f ? half : 1.0f - half;
+// Two fp32 numbers in one register pair, for the paired FMA.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void split_pair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float a) { return pair_of(a, a); }
+
+// The normal distribution at x and y: p, q; e = exp(-x^2 / 2), exp(-y^2 / 2).
+__device__ __forceinline__ void normal_pair(float x, float y, float& p, float& q, uint64_t& e) {
+  const uint64_t k = pair_of(rcp_fast(fmaf(0.35f, fabsf(x), 1.0f)), rcp_fast(fmaf(0.35f, fabsf(y), 1.0f)));
+  const uint64_t z = pair_of(x, y);
+  float a, b;
+  split_pair(mul_pair(mul_pair(both(-0.5f * LOG2_E), z), z), a, b);
+  e = pair_of(exp2_fast(a), exp2_fast(b));
+  uint64_t v = fma_pair(both(-0.0285310932f), k, both(0.1412722766f));
+  v = fma_pair(v, k, both(-0.2507375181f));
+  v = fma_pair(v, k, both(0.1541662067f));
+  v = fma_pair(v, k, both(-0.0201176628f));
+  v = fma_pair(v, k, both(0.1044274792f));
+  v = fma_pair(v, k, both(0.1200617179f));
+  v = fma_pair(v, k, both(0.1398360431f));
+  v = fma_pair(v, k, both(0.1396225840f));
+  split_pair(mul_pair(mul_pair(v, k), e), a, b);   // the distribution at -|x|, -|y|
+  p = x < 0.0f ? a : 1.0f - a;
+  q = y < 0.0f ? b : 1.0f - b;
 }
 
 constexpr float TANH_A = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 
+// Activations but GELU, which takes two numbers at a time.
 template <int ACT>
-__device__ __forceinline__ float activate(float x) {
+__device__ __forceinline__ float activate_one(float x) {
   if constexpr (ACT == ACT_RELU) {
     float y;
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
     return y;
-  } else if constexpr (ACT == ACT_GELU) {
-    float e;
-    return x * normal_fast(x, e);
   } else if constexpr (ACT == ACT_GELU_TANH) {
     return x * sigmoid_fast(TANH_A * x * fmaf(0.044715f * x, x, 1.0f));
   } else if constexpr (ACT == ACT_SILU) {
@@ -74,15 +97,11 @@ __device__ __forceinline__ float activate(float x) {
   }
 }
 
-// The derivative at x.
+// Their derivatives.
 template <int ACT>
-__device__ __forceinline__ float activate_grad(float x) {
+__device__ __forceinline__ float activate_grad_one(float x) {
   if constexpr (ACT == ACT_RELU) {
     return x > 0.0f ? 1.0f : x <= 0.0f ? 0.0f : x;
-  } else if constexpr (ACT == ACT_GELU) {
-    float e;
-    const float p = normal_fast(x, e);
-    return fmaf(x * 0.3989422804f, e, p);
   } else if constexpr (ACT == ACT_GELU_TANH) {
     // Beyond +-16 it is 1 or 0; x^2 would overflow far out.
     float c;
@@ -99,6 +118,42 @@ __device__ __forceinline__ float activate_grad(float x) {
     return s * fmaf(c, sigmoid_fast(-c), 1.0f);
   } else {
     return 1.0f;
+  }
+}
+
+// x[i] = act(x[i]);  g[i] *= act'(z[i]).
+template <int ACT, int N>
+__device__ __forceinline__ void activate(float (&x)[N]) {
+  static_assert(N % 2 == 0, "");
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    if constexpr (ACT == ACT_GELU) {
+      float p, q;
+      uint64_t e;
+      normal_pair(x[i], x[i + 1], p, q, e);
+      x[i] *= p;
+      x[i + 1] *= q;
+    } else {
+      x[i] = activate_one<ACT>(x[i]);
+      x[i + 1] = activate_one<ACT>(x[i + 1]);
+    }
+  }
+}
+template <int ACT, int N>
+__device__ __forceinline__ void activate_grad(const float (&z)[N], float (&g)[N]) {
+  static_assert(N % 2 == 0, "");
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    if constexpr (ACT == ACT_GELU) {
+      float p, q;
+      uint64_t e;
+      normal_pair(z[i], z[i + 1], p, q, e);
+      const uint64_t d = fma_pair(mul_pair(pair_of(z[i], z[i + 1]), both(0.3989422804f)), e, pair_of(p, q));
+      split_pair(mul_pair(d, pair_of(g[i], g[i + 1])), g[i], g[i + 1]);
+    } else {
+      g[i] *= activate_grad_one<ACT>(z[i]);
+      g[i + 1] *= activate_grad_one<ACT>(z[i + 1]);
+    }
   }
 }
 

@@ -85,6 +85,7 @@ struct LinearEpilogue {
   int64_t ldr, ldp;
   int32_t act;
   int32_t vec_p;   // pre's rows may be written with 16-byte vectors
+  int32_t vec_r;   // the residual's entries have 16 bits and its rows may be read with 16-byte vectors
 };
 // CHAIN's maps in tmB, beside E as M side in tmA: both X buffers as M side of E, as N side
 // of E, as N side of F X; F as M side; E as N side.

@@ -74,14 +74,24 @@ gemm_status_t check_linear(const gemm_plan* plan, gemm_layout_t lb, int64_t M, i
 }
 
 // How many CTAs share a tile's K on linear_split_kernel (0: the product runs on seg_kernel).
+// A CTA takes 1024 k, or less down to 128 as long as four share a tile, and two CTAs have room
+// on an SM.  Up to 32 rows always: the weights' stream bounds the product.  Beyond, a tile's
+// partial sums (up to 64 KB per CTA) cost 3 to 7 us, what 16 to 32 K blocks of a tile take, so
+// the split pays where tiles are few beside K blocks.  Measured, split / seg_kernel, us: 1 row,
+// 4096 to 4096 9.5 / 16.1, 1024 to 20000 (not split) 10.8 / 13.6; 64 rows, 4096 to 11008 19.4 /
+// 23.3, 256 to 4096 5.6 / 5.3; 128 rows, 4096 to 11008 22.0 / 26.2, 1024 to 1024 7.2 / 8.3, 512 to
+// 4096 8.2 / 7.2; 256 rows, 4096 to 4096 16.5 / 19.6, 1024 to 4096 10.6 / 9.2; 300 rows, 11008 to
+// 4096 31.7 / 42.5, 2048 to 4096 13.8 / 12.8; 1000 rows, 4096 to 1024 15.6 / 19.9, 2048 to 1024
+// 12.2 / 12.3, 1000 to 2048 12.5 / 10.7.
 int splits_of(int64_t M, int64_t N, int64_t K, int box_rows, int sm_count) {
   const int64_t num_kb = (K + TC_BK - 1) / TC_BK;
   const int64_t tiles = (N + 127) / 128 * ((M + box_rows - 1) / box_rows);
-  if (num_kb == 0) return 0;
-  
-  if (tiles > sm_count) return 0;
-  const int64_t splits = std::min<int64_t>({8, num_kb, 2 * (int64_t)sm_count / tiles});
-  return splits >= 2 ? (int)splits : 0;
+  if (num_kb == 0 || N > 65535 * int64_t(128)) return 0;
+  const int64_t want = std::max<int64_t>({1, num_kb / 16, std::min<int64_t>(4, num_kb / 2)});
+  const int64_t splits = std::min<int64_t>({8, want, std::max<int64_t>(1, 2 * (int64_t)sm_count / tiles)});
+  if (M <= 32) return (int)splits;
+  if (M <= 64) return tiles <= 4 * num_kb ? (int)splits : 0;
+  return splits >= 2 && 2 * tiles <= 3 * num_kb ? (int)splits : 0;
 }
 
 // D = act(x W + bias) + residual: x M x K row-major, W K x N (w_mn: N contiguous, else K);
@@ -203,6 +213,7 @@ gemm_status_t gemm_run_linear(gemm_plan_t plan, gemm_layout_t lb, int64_t M, int
     lin.pre = epi->pre;
     lin.ldp = epi->ld_pre;
     lin.act = epi->act;
+    lin.vec_r = epi->residual && out != GEMM_F32 && wide_rows(epi->residual, epi->ld_residual, 2) ? 1 : 0;
     lin.vec_p = epi->pre && wide_rows(epi->pre, epi->ld_pre, dtype_bytes(out)) ? 1 : 0;
   }
   Operand x{A, lda, 0}, w{B, ldb, 0};
@@ -247,9 +258,9 @@ gemm_status_t gemm_run_linear_grad(gemm_plan_t plan, gemm_layout_t lb, int64_t M
   const size_t zb = M == 0 || N == 0 ? 0 : acts ? align_up((size_t)(M * ldz) * 2, 256) : repitch_bytes(dy, M, N, 1);
   const size_t xb = want_b && M > 0 ? repitch_bytes(x, M, K, 1) : 0;
   const size_t wb = want_a && N > 0 ? repitch_bytes(w, wrows, wcols, 1) : 0;
-  // Blocks of rows: enough CTAs for eight per SM, at least 32 rows each.
+  // Blocks of rows: CTAs for four per SM, at least 32 rows each.
   const int64_t strips = (N + 255) / 256;
-  const int64_t want = std::max<int64_t>(1, 8 * (int64_t)plan->sm_count / std::max<int64_t>(1, strips));
+  const int64_t want = std::max<int64_t>(1, 4 * (int64_t)plan->sm_count / std::max<int64_t>(1, strips));
   const int64_t block_rows = std::max<int64_t>(32, (M + want - 1) / want);
   const int blocks = (int)((M + block_rows - 1) / block_rows);
   const size_t pb = want_bias ? (size_t)blocks * (size_t)N * sizeof(float) : 0;

@@ -271,9 +271,7 @@ __global__ void __launch_bounds__(THREADS) linear_split_kernel(const __grid_cons
       }
       with_act(p.linear.act, [&](auto act) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[u][j] = activate<decltype(act)::value>(x[u][j]);
+        for (int u = 0; u < U; ++u) activate<decltype(act)::value>(x[u]);
       });
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -295,31 +293,52 @@ __global__ void __launch_bounds__(THREADS) linear_split_kernel(const __grid_cons
 // ------------------------- the gradient's elementwise pass -------------------------
 
 constexpr int GRAD_THREADS = 256, GRAD_COLS = 256;   // a warp takes a row's 256 columns, eight per lane
+constexpr int GRAD_WARPS = GRAD_THREADS / 32, GRAD_STAGES = 4;   // rows of a warp under way
 
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// At most N of the newest groups are still under way.
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// Eight entries of a row (n of them exist) as they lie in memory.
+__device__ __forceinline__ uint4 load8_raw(const void* p, int64_t i, int n, bool vec) {
+  const uint16_t* src = static_cast<const uint16_t*>(p) + i;
+  if (vec && n >= 8) return *reinterpret_cast<const uint4*>(src);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) w[j / 2] |= (uint32_t)src[j] << (16 * (j % 2));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int n, bool vec, float (&x)[8]) {
-  if (vec && n >= 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      if constexpr (DT == GEMM_F16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-        x[2 * h] = f.x, x[2 * h + 1] = f.y;
-      } else {
-        x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
-      }
+  for (int h = 0; h < 4; ++h) {
+    if constexpr (DT == GEMM_F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
+      x[2 * h] = f.x, x[2 * h + 1] = f.y;
+    } else {
+      x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = j < n ? load_as_float(p, DT, i + j) : 0.0f;
   }
 }
 
-// Grid: (256-column strips, row blocks).
+// Grid: (256-column strips, row blocks).  A lane copies its pieces of four rows ahead into
+// shared memory of its own (nobody else's, so no barrier): 32 warps per SM then have 128 KB
+// under way, which registers do not hold beside the derivative's.
 template <int DT>
-__global__ void __launch_bounds__(GRAD_THREADS) act_grad_kernel(const __grid_constant__ ActGradParams p) {
-  __shared__ float sums[GRAD_THREADS / 32][GRAD_COLS];
+__global__ void __launch_bounds__(GRAD_THREADS, 4) act_grad_kernel(const __grid_constant__ ActGradParams p) {
+  __shared__ __align__(16) uint8_t ring[GRAD_STAGES][2][GRAD_THREADS * 16];
+  __shared__ float sums[GRAD_WARPS][GRAD_COLS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
@@ -331,28 +350,44 @@ __global__ void __launch_bounds__(GRAD_THREADS) act_grad_kernel(const __grid_con
   for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
   with_act(p.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
-    if (n > 0) {
-#pragma unroll 2
-      for (int64_t r = lo + warp; r < hi; r += GRAD_THREADS / 32) {
-        float dy[8];
-        load8<DT>(p.dy, r * p.ldy + c, n, p.vec, dy);
-        if constexpr (ACT != ACT_NONE) {
-          float z[8];
-          load8<DT>(p.pre, r * p.ldp + c, n, p.vec, z);
-          uint32_t w[4];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dy[j] *= activate_grad<ACT>(z[j]);
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {   // (dz's rows are padded to whole pieces; what lies past N is 0)
-            if constexpr (DT == GEMM_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(dy[2 * h + 1]), "f"(dy[2 * h]));
-            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(dy[2 * h + 1]), "f"(dy[2 * h]));
-          }
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dz) + r * p.ldz + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += dy[j];
+    const bool async = p.vec && n == 8;
+    auto slot = [&](int stage, int which) { return smem_u32(&ring[stage][which][threadIdx.x * 16]); };
+    auto copy = [&](int64_t r, int stage) {
+      if (async && r < hi) {
+        copy16_async(slot(stage, 0), static_cast<const uint16_t*>(p.dy) + r * p.ldy + c);
+        if constexpr (ACT != ACT_NONE) copy16_async(slot(stage, 1), static_cast<const uint16_t*>(p.pre) + r * p.ldp + c);
       }
+      copies_commit();
+    };
+    const int64_t first = n > 0 ? lo + warp : hi;
+#pragma unroll
+    for (int s = 0; s < GRAD_STAGES; ++s) copy(first + s * GRAD_WARPS, s);
+    int stage = 0;
+#pragma unroll 1
+    for (int64_t r = first; r < hi; r += GRAD_WARPS) {
+      copies_wait<GRAD_STAGES - 1>();
+      float g[8];
+      widen8<DT>(async ? lds16(slot(stage, 0)) : load8_raw(p.dy, r * p.ldy + c, n, p.vec), g);
+      if constexpr (ACT != ACT_NONE) {
+        float z[8];
+        uint32_t w[4];
+        widen8<DT>(async ? lds16(slot(stage, 1)) : load8_raw(p.pre, r * p.ldp + c, n, p.vec), z);
+        copy(r + GRAD_STAGES * GRAD_WARPS, stage);
+        activate_grad<ACT>(z, g);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {   // (dz's rows are padded to whole pieces; what lies past N is 0)
+          if constexpr (DT == GEMM_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(g[2 * h + 1]), "f"(g[2 * h]));
+          else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(g[2 * h + 1]), "f"(g[2 * h]));
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dz) + r * p.ldz + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        copy(r + GRAD_STAGES * GRAD_WARPS, stage);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += g[j];
+      stage = stage + 1 == GRAD_STAGES ? 0 : stage + 1;
     }
+    copies_wait<0>();
   });
   if (p.partials == nullptr) return;
 #pragma unroll
@@ -362,25 +397,36 @@ __global__ void __launch_bounds__(GRAD_THREADS) act_grad_kernel(const __grid_con
   if (col < p.N) {
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < GRAD_THREADS / 32; ++w) s += sums[w][threadIdx.x];
+    for (int w = 0; w < GRAD_WARPS; ++w) s += sums[w][threadIdx.x];
     p.partials[(int64_t)blockIdx.y * p.N + col] = s;
   }
 }
 
+// out[c] = the sum of partials[b][c] over the row blocks, in one order: a CTA takes 32 columns,
+// its warps equal parts of the blocks.
 __global__ void __launch_bounds__(256) column_sums_kernel(const float* partials, int blocks, int64_t N, float* out) {
+  __shared__ float sums[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= N) return;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int per = (blocks + 7) / 8, lo = warp * per, hi = min(blocks, lo + per);
   float s = 0.0f;
-  for (int b = 0; b < blocks; b += 16) {   // (16 loads under way)
-    float v[16];
+  for (int b = lo; b < hi; b += 8) {   // (eight loads under way)
+    float v[8];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) v[u] = b + u < blocks ? partials[(int64_t)(b + u) * N + c] : 0.0f;
+    for (int u = 0; u < 8; ++u) v[u] = b + u < hi && c < N ? partials[(int64_t)(b + u) * N + c] : 0.0f;
 #pragma unroll
-    for (int u = 0; u < 16; ++u) s += v[u];
+    for (int u = 0; u < 8; ++u) s += v[u];
   }
-  out[c] = s;
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < N) {
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += sums[w][lane];
+    out[c] = s;
+  }
 }
 
 template <bool A_MN>
@@ -429,7 +475,7 @@ cudaError_t launch_act_grad(const ActGradParams& p, int dtype, int blocks, cudaS
 }
 
 cudaError_t launch_column_sums(const float* partials, int blocks, int64_t N, float* out, cudaStream_t stream) {
-  return launch_dependent(column_sums_kernel, dim3((unsigned)((N + 255) / 256)), 256, stream, partials, blocks, N, out);
+  return launch_dependent(column_sums_kernel, dim3((unsigned)((N + 31) / 32)), 256, stream, partials, blocks, N, out);
 }
 
 }  // namespace gemmlib

@@ -355,12 +355,47 @@ __device__ __forceinline__ void add_c(const EpiParams& e, const void* C, int64_t
   }
 }
 
-// LINEAR: x[j] += R[n + j][m + lane], j < rows, lane < cols.  A row's 32 entries are one load
-// instruction; turning wider ones around in shared memory takes as many.
-template <int DT>
-__device__ __forceinline__ void add_residual(const LinearEpilogue& l, int64_t n, int64_t m, int rows, int cols,
-                                             float (&x)[32]) {
+// LINEAR: the residual of a chunk, whose lanes hold columns of D: R[n + j][m + lane], j < rows,
+// lane < cols.  In two steps so that the loads run ahead of the accumulator: aligned rows of 16
+// bits straight into registers, four rows' 64 bytes per lane, turned around in the warp's
+// buffer when they are added; others are read when they are added, a row per instruction.
+struct RChunk {
+  uint4 v[4];
+  bool held;
+};
+__device__ __forceinline__ void load_residual(const LinearEpilogue& l, bool wide, int64_t n, int64_t m, int rows, int cols,
+                                              RChunk& c) {
   const int lane = threadIdx.x & 31;
+  c.held = wide && cols % 8 == 0;
+  if (!c.held) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    c.v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows && (lane & 3) * 8 < cols)
+      c.v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(l.residual) + (n + r) * l.ldr + m + (lane & 3) * 8);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void add_residual(const LinearEpilogue& l, const RChunk& c, int64_t n, int64_t m, int rows, int cols,
+                                             float (&x)[32], uint32_t turn) {
+  const int lane = threadIdx.x & 31;
+  if (DT != GEMM_F32 && c.held) {
+    __syncwarp();   // the buffer's last readers are done
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      sts128(turn + (uint32_t)(r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)), c.v[i].x, c.v[i].y, c.v[i].z, c.v[i].w);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      uint16_t w;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(turn + (uint32_t)(j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2)) : "memory");
+      x[j] += load_as_float(&w, DT, 0);
+    }
+    return;
+  }
   if (lane >= cols) return;
   const int64_t at = n * l.ldr + m + lane;
 #pragma unroll
@@ -946,6 +981,11 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
         load_c(ep, ptr.C, m, (int64_t)t.n0 + c_first * 32, m_left, ext(t.n_valid - c_first * 32), cc);
       if (MODE == SEG_CHAIN && c_lo != nullptr)
         load_c(ep, c_lo, m, (int64_t)t.n0 + c_first * 32, m_left, ext(t.n_valid - c_first * 32), cl);
+      RChunk rc;
+      rc.held = false;
+      const bool wide_r = MODE == SEG_LINEAR && p.linear.residual != nullptr && p.linear.vec_r;
+      if (MODE == SEG_LINEAR && c_first * 32 < t.n_valid)   // the first chunk of the residual too
+        load_residual(p.linear, wide_r, (int64_t)t.n0 + c_first * 32, m, t.n_valid - c_first * 32, m_left, rc);
       if (t.k > 0) {
         if (!warp_wait(tfull_bar(buf), (acc_it >> 1) & 1u, wc)) break;
         tc_fence_after();
@@ -1019,11 +1059,11 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
             for (int j = 0; j < 32; ++j) x[j] += bias;
             if (p.linear.pre != nullptr)
               store_chunk_t<DT>(p.linear.pre, p.linear.ldp, n, m, n_left, m_left, x, turn, p.linear.vec_p);
-            with_act(p.linear.act, [&](auto act) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = activate<decltype(act)::value>(x[j]);
-            });
-            if (p.linear.residual != nullptr) add_residual<DT>(p.linear, n, m, n_left, m_left, x);
+            with_act(p.linear.act, [&](auto act) { activate<decltype(act)::value>(x); });
+            if (p.linear.residual != nullptr) {
+              add_residual<DT>(p.linear, rc, n, m, n_left, m_left, x, turn);
+              if (c + 2 < chunks) load_residual(p.linear, wide_r, n + 64, m, n_left - 64, m_left, rc);
+            }
             store_chunk_t<DT>(p.epi.D, p.epi.ldd, n, m, n_left, m_left, x, turn, p.epi.vec_d);
           }
         };

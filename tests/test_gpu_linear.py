@@ -50,10 +50,11 @@ def _check(x, w, act, bias, residual, out, dtype, save=True, **kw):
         within(pre, z, U[out] * (z.abs() + ez) + ez + TINY[out], "pre")
 
 
-# (rows, K, N, CTAs that share a tile's K: 1 on the tile kernel)
-SIZES = [(1, 64, 16, 1), (1, 65, 128, 2), (1, 4096, 11008, 3), (7, 1024, 1000, 8), (16, 200, 130, 4), (17, 256, 384, 4),
-         (33, 2048, 4096, 8), (64, 512, 5000, 7), (65, 320, 300, 5), (128, 1000, 2048, 8), (129, 192, 640, 3),
-         (300, 700, 1024, 8), (1000, 1000, 2048, 2), (1, 128, 20000, 1), (200, 256, 12000, 1), (513, 264, 9000, 1)]
+# (rows, K, N, CTAs that share a tile's K; 0: the tile kernel, on single CTAs or pairs)
+SIZES = [(1, 64, 16, 1), (1, 65, 128, 1), (1, 4096, 11008, 3), (7, 1024, 1000, 4), (16, 200, 130, 2), (17, 256, 384, 2),
+         (1, 128, 20000, 1), (32, 8200, 1000, 8), (33, 2048, 4096, 4), (64, 512, 5000, 0), (60, 1030, 2000, 4), (64, 4096, 20000, 1),
+         (65, 320, 300, 2), (65, 1100, 300, 4), (128, 1000, 2048, 4), (129, 2050, 640, 4), (300, 4100, 3900, 3), (300, 700, 1024, 0),
+         (1000, 1000, 2048, 0), (200, 256, 12000, 0), (513, 264, 9000, 0)]
 
 
 @pytest.mark.parametrize("M,K,N,splits", SIZES)
@@ -64,7 +65,8 @@ def test_linear(M, K, N, splits, layout, dtype, act):
     bias, res = _rand((N,), "f32", 3, 0.3), _rand((M, N), dtype, 4)
     plan = G.Plan(G.DTYPE_CODES[dtype], G.GEMM_F32)
     _check(x, w, act, bias, res, dtype, dtype, plan=plan)
-    assert plan.last_config()["split_k"] == splits and plan.device_status() == 0
+    c = plan.last_config()
+    assert (c["split_k"] if c["bk"] == 64 else 0) == splits and plan.device_status() == 0
 
 
 @pytest.mark.parametrize("act", ACTS, ids=str)

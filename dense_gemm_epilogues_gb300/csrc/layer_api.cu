@@ -73,25 +73,32 @@ gemm_status_t check_linear(const gemm_plan* plan, gemm_layout_t lb, int64_t M, i
   return GEMM_OK;
 }
 
-// How many CTAs share a tile's K on linear_split_kernel (0: the product runs on seg_kernel).
-// A CTA takes 1024 k, or less down to 128 as long as four share a tile, and two CTAs have room
-// on an SM.  Up to 32 rows always: the weights' stream bounds the product.  Beyond, a tile's
-// partial sums (up to 64 KB per CTA) cost 3 to 7 us, what 16 to 32 K blocks of a tile take, so
-// the split pays where tiles are few beside K blocks.  Measured, split / seg_kernel, us: 1 row,
-// 4096 to 4096 9.5 / 16.1, 1024 to 20000 (not split) 10.8 / 13.6; 64 rows, 4096 to 11008 19.4 /
-// 23.3, 256 to 4096 5.6 / 5.3; 128 rows, 4096 to 11008 22.0 / 26.2, 1024 to 1024 7.2 / 8.3, 512 to
-// 4096 8.2 / 7.2; 256 rows, 4096 to 4096 16.5 / 19.6, 1024 to 4096 10.6 / 9.2; 300 rows, 11008 to
-// 4096 31.7 / 42.5, 2048 to 4096 13.8 / 12.8; 1000 rows, 4096 to 1024 15.6 / 19.9, 2048 to 1024
-// 12.2 / 12.3, 1000 to 2048 12.5 / 10.7.
-int splits_of(int64_t M, int64_t N, int64_t K, int box_rows, int sm_count) {
-  const int64_t num_kb = (K + TC_BK - 1) / TC_BK;
-  const int64_t tiles = (N + 127) / 128 * ((M + box_rows - 1) / box_rows);
-  if (num_kb == 0 || N > 65535 * int64_t(128)) return 0;
+// How linear_split_kernel runs a product: rows of a tile, and CTAs that share a tile's K (0: the
+// product runs on seg_kernel).  A CTA takes 1024 k, or less down to 128 as long as four share a
+// tile, and two CTAs have room on an SM.  Up to 32 rows always: the weights' stream bounds the
+// product.  Beyond, tiles of 64 rows wherever they are few enough to be split; a tile's partial
+// sums cost a CTA 1 us per 16 KB, so tiles of 128 rows only where K is long beside their number.
+// Measured with a residual, tiles of 64 rows / of 128 / seg_kernel, us: 128 rows, 1024 to 1024
+// 6.5 / 7.9 / 8.8, 4096 to 11008 29.9 / 24.7 / 27.0, 512 to 4096 7.4 / 8.9 / 7.8; 200 rows, 2048 to
+// 2048 10.0 / 12.0 / 12.2; 256 rows, 4096 to 4096 17.5 / 18.5 / 20.2; 512 rows, 11008 to 1024 20.3
+// / 24.0 / 43.7; 1000 rows, 2048 to 1024 12.3 / 13.8 / 12.9, 1000 to 2048 14.9 / 15.1 / 11.2.
+// Fewer rows, split / seg_kernel: 1 row, 4096 to 4096 9.5 / 16.1, 1024 to 20000 (not split) 10.8
+// / 13.6; 64 rows, 4096 to 20000 (not split) 33.5 / 42, 4096 to 4096 12.9 / 17.2.
+struct SplitShape {
+  int box_rows, splits;
+};
+SplitShape split_shape(int64_t M, int64_t N, int64_t K, int sm_count) {
+  const int64_t num_kb = (K + TC_BK - 1) / TC_BK, cols = (N + 127) / 128;
+  if (num_kb == 0 || cols > 65535) return {0, 0};
   const int64_t want = std::max<int64_t>({1, num_kb / 16, std::min<int64_t>(4, num_kb / 2)});
-  const int64_t splits = std::min<int64_t>({8, want, std::max<int64_t>(1, 2 * (int64_t)sm_count / tiles)});
-  if (M <= 32) return (int)splits;
-  if (M <= 64) return tiles <= 4 * num_kb ? (int)splits : 0;
-  return splits >= 2 && 2 * tiles <= 3 * num_kb ? (int)splits : 0;
+  auto splits = [&](int64_t tiles) {
+    return (int)std::min<int64_t>({8, want, std::max<int64_t>(1, 2 * (int64_t)sm_count / tiles)});
+  };
+  const int box = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int64_t tiles = cols * ((M + box - 1) / box), tiles128 = cols * ((M + 127) / 128);
+  if (M <= 32 || splits(tiles) >= 2 || (M <= 64 && tiles <= 4 * num_kb)) return {box, splits(tiles)};
+  if (splits(tiles128) >= 2 && 2 * tiles128 <= 3 * num_kb) return {128, splits(tiles128)};
+  return {0, 0};
 }
 
 // D = act(x W + bias) + residual: x M x K row-major, W K x N (w_mn: N contiguous, else K);
@@ -100,8 +107,8 @@ gemm_status_t linear_product(gemm_plan* plan, int64_t M, int64_t N, int64_t K, c
                              bool w_mn, const EpiParams& epi, const LinearEpilogue& lin, const char* entry,
                              cudaStream_t stream) {
   const CUtensorMapDataType dt = map_type(plan->ab);
-  const int box = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  const int splits = splits_of(M, N, K, box, plan->sm_count);
+  const SplitShape shape = split_shape(M, N, K, plan->sm_count);
+  const int box = shape.box_rows, splits = shape.splits;
   if (splits > 0) {
     LinearSplitParams p;
     std::memset(&p, 0, sizeof(p));

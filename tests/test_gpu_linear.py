@@ -50,23 +50,25 @@ def _check(x, w, act, bias, residual, out, dtype, save=True, **kw):
         within(pre, z, U[out] * (z.abs() + ez) + ez + TINY[out], "pre")
 
 
-# (rows, K, N, CTAs that share a tile's K; 0: the tile kernel, on single CTAs or pairs)
-SIZES = [(1, 64, 16, 1), (1, 65, 128, 1), (1, 4096, 11008, 3), (7, 1024, 1000, 4), (16, 200, 130, 2), (17, 256, 384, 2),
-         (1, 128, 20000, 1), (32, 8200, 1000, 8), (33, 2048, 4096, 4), (64, 512, 5000, 0), (60, 1030, 2000, 4), (64, 4096, 20000, 1),
-         (65, 320, 300, 2), (65, 1100, 300, 4), (128, 1000, 2048, 4), (129, 2050, 640, 4), (300, 4100, 3900, 3), (300, 700, 1024, 0),
-         (1000, 1000, 2048, 0), (200, 256, 12000, 0), (513, 264, 9000, 0)]
+# (rows, K, N, rows of a tile and CTAs that share its K; 0: the tile kernel, on single CTAs or pairs)
+SIZES = [(1, 64, 16, 16, 1), (1, 65, 128, 16, 1), (1, 4096, 11008, 16, 3), (7, 1024, 1000, 16, 4),
+         (16, 200, 130, 16, 2), (17, 256, 384, 32, 2), (1, 128, 20000, 16, 1), (32, 8200, 1000, 32, 8),
+         (33, 2048, 4096, 64, 4), (64, 512, 20000, 0, 0), (64, 4096, 20000, 64, 1), (60, 1030, 2000, 64, 4),
+         (65, 320, 300, 64, 2), (65, 130, 300, 0, 0), (128, 1000, 2048, 64, 4), (129, 2050, 640, 64, 4),
+         (300, 700, 1024, 64, 4), (128, 4100, 11000, 128, 3), (250, 9000, 7000, 128, 2), (1000, 1000, 2048, 0, 0),
+         (200, 256, 12000, 0, 0), (513, 264, 9000, 0, 0)]
 
 
-@pytest.mark.parametrize("M,K,N,splits", SIZES)
+@pytest.mark.parametrize("M,K,N,box,splits", SIZES)
 @pytest.mark.parametrize("layout", ["kn", "nk"])
 @pytest.mark.parametrize("dtype,act", [("bf16", "gelu"), ("f16", "silu")])
-def test_linear(M, K, N, splits, layout, dtype, act):
+def test_linear(M, K, N, box, splits, layout, dtype, act):
     x, w = _layer(M, K, N, dtype, layout)
     bias, res = _rand((N,), "f32", 3, 0.3), _rand((M, N), dtype, 4)
     plan = G.Plan(G.DTYPE_CODES[dtype], G.GEMM_F32)
     _check(x, w, act, bias, res, dtype, dtype, plan=plan)
     c = plan.last_config()
-    assert (c["split_k"] if c["bk"] == 64 else 0) == splits and plan.device_status() == 0
+    assert ((c["bn"], c["split_k"]) if c["bk"] == 64 else (0, 0)) == (box, splits) and plan.device_status() == 0
 
 
 @pytest.mark.parametrize("act", ACTS, ids=str)

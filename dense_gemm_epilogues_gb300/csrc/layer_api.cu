@@ -155,7 +155,13 @@ gemm_status_t linear_product(gemm_plan* plan, int64_t M, int64_t N, int64_t K, c
   if (K > 0) {
     bool ok = w_mn ? encode_3d(&p.tmA, dt, w.p, N, K, w.ld, 1, 0, 64, 2 * TC_BK)
                    : encode_3d(&p.tmA, dt, w.p, K, N, w.ld, 1, 0, TC_BK, 128);
-    for (int b = 0; b < 5; ++b) ok = ok && encode_3d(&p.tmB[b], dt, x.p, K, M, x.ld, 1, 0, TC_BK, 128u >> b);
+    // The boxes that the tiles' rows take: all tiles but the last have equally many.
+    const int64_t n_tiles = (M + 128 * cg - 1) / (128 * cg), per = ((M + n_tiles - 1) / n_tiles + 15) / 16 * 16;
+    for (const int64_t rows : {per, (M - (n_tiles - 1) * per + 15) / 16 * 16}) {
+      int b = 0;
+      while (b < 4 && (64 >> b) >= rows / cg) ++b;
+      ok = ok && encode_3d(&p.tmB[b], dt, x.p, K, M, x.ld, 1, 0, TC_BK, 128u >> b);
+    }
     if (!ok) return GEMM_ERR_CUDA;
   }
   p.groups = Groups{nullptr, 1, (int32_t)M, plan->d_err};

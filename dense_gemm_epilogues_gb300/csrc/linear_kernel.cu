@@ -51,10 +51,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
   return __all_sync(0xffffffffu, ok) != 0;
 }
 
-__device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* tm, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tm), "r"(x), "r"(y), "r"(0) : "memory");
-}
-
 __device__ __forceinline__ float4 lds_cluster(uint32_t a) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
@@ -147,20 +143,9 @@ __global__ void __launch_bounds__(THREADS) linear_split_kernel(const __grid_cons
   const int num_kb = (int)((p.K + TC_BK - 1) / TC_BK);
   const int kb0 = (int)((int64_t)split * num_kb / splits), kb1 = (int)((int64_t)(split + 1) * num_kb / splits);
   pdl_launch_dependents();
-  // What the ring's first turn will load of the weights is fetched into L2 while the previous
-  // kernel ends: a hint, which reads nothing into this CTA (L2 is where all SMs' writes meet, so
-  // a weight that the previous kernel still writes is loaded as written, after the wait).
   if (warp == 0 && elect_one()) {
     tma_prefetch_desc(&p.tmW);
     tma_prefetch_desc(&p.tmX);
-    for (int kb = kb0; kb < min(kb1, kb0 + p.stages); ++kb) {
-      if constexpr (A_MN) {
-        tma_prefetch_l2(&p.tmW, (int)m0, kb * TC_BK);
-        tma_prefetch_l2(&p.tmW, (int)m0 + 64, kb * TC_BK);
-      } else {
-        tma_prefetch_l2(&p.tmW, kb * TC_BK, (int)m0);
-      }
-    }
   }
   __syncwarp();
   pdl_wait();

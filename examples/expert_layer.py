@@ -2,14 +2,15 @@
 
     python examples/expert_layer.py
 
-Tokens are routed to two of the experts each, sorted by expert, and run through
-y = relu(x W1 + b1) W2 (grouped_matmul, bias and ReLU in its epilogue).  The
-backward pass is the input gradient (grouped_matmul with the transposed weights)
-and the weight gradients (grouped_weight_grad), the update an orthogonalised
-momentum (orthogonalize) of every expert's matrices at once.  The trained
-weights are then rounded to 4 bits (quantize_q4) and single tokens served with
-q4_matmul.  The layer learns to imitate another expert layer with fixed random
-weights; routing, loss and token bookkeeping are plain torch.
+Tokens are routed to two of the experts each (route), their rows sorted by expert
+(dispatch) and run through y = relu(x W1 + b1) W2 (grouped_matmul, bias and ReLU in its
+epilogue), and added up again with the routing's weights (combine).  The backward pass is
+combine's gradient (combine_grad), the input gradient (grouped_matmul with the transposed
+weights) and the weight gradients (grouped_weight_grad), clipped by their global norm
+(clip_grad_norm), the update an orthogonalised momentum (orthogonalize) of every expert's
+matrices at once.  The trained weights are then rounded to 4 bits (quantize_q4) and single
+tokens served with q4_matmul.  The layer learns to imitate another expert layer with fixed
+random weights and the same router; the loss is plain torch.
 """
 import os
 import sys
@@ -20,16 +21,6 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import dense_gemm_epilogues_gb300 as G  # noqa: E402
 
 TOP = 2   # experts per token
-
-
-def route(x, router):
-    """(offsets, order, weight): rows sorted by expert, each row's token, and its
-    share of the token's output.  Nothing waits for the host."""
-    share, expert = torch.softmax(x.float() @ router, -1).topk(TOP, -1)
-    expert, order = expert.flatten().sort(stable=True)
-    offsets = torch.zeros(router.shape[1] + 1, dtype=torch.int32, device=x.device)
-    offsets[1:] = torch.bincount(expert, minlength=router.shape[1]).cumsum(0)
-    return offsets, order // TOP, (share / share.sum(-1, keepdim=True)).flatten()[order]
 
 
 class Experts:
@@ -59,6 +50,7 @@ class Experts:
 
     def update(self, grads, rate, beta=0.9):
         """Each expert's matrices move along their orthogonalised momentum."""
+        G.clip_grad_norm(grads, 1.0, plan=self.plan32)
         for w, m, g in zip((self.w1, self.w2), self.momentum, grads):
             m.mul_(beta).add_(g)
             step = G.orthogonalize(m, plan=self.plan32)
@@ -75,11 +67,6 @@ def serve_q4(x, offsets, packed, b1, group, plan):
     return G.q4_matmul(h, q2, s2, group, zeros=z2, offsets=offsets, plan=plan)
 
 
-def combine(y, order, weight, tokens):
-    out = torch.zeros((tokens, y.shape[1]), device=y.device)
-    return out.index_add_(0, order, y.float() * weight[:, None])
-
-
 def main(experts=8, d=256, h=512, tokens=1024, steps=60, rate=0.02, group=64, seed=0, verbose=True):
     gen = torch.Generator("cuda").manual_seed(seed)
     router = torch.randn((d, experts), generator=gen, device="cuda") * d ** -0.5
@@ -87,25 +74,25 @@ def main(experts=8, d=256, h=512, tokens=1024, steps=60, rate=0.02, group=64, se
     losses = []
     for step in range(steps):
         x = torch.randn((tokens, d), generator=gen, device="cuda").bfloat16()
-        offsets, order, weight = route(x, router)
-        rows = x[order]
-        target = combine(teacher.forward(rows, offsets)[0], order, weight, tokens)
-        y, hidden = student.forward(rows, offsets)
-        error = combine(y, order, weight, tokens) - target
+        r = G.route(x.float() @ router, TOP, plan=student.plan32)
+        rows = G.dispatch(x, r, plan=student.plan)
+        target = G.combine(teacher.forward(rows, r.offsets)[0], r, plan=teacher.plan)
+        y, hidden = student.forward(rows, r.offsets)
+        error = G.combine(y, r, plan=student.plan).float() - target
         losses.append(float(error.square().mean()))
-        dy = (error[order] * weight[:, None] * (2.0 / error.numel())).bfloat16()
-        student.update(student.backward(rows, hidden, dy, offsets), rate * (1 - step / steps))
+        dy, _ = G.combine_grad((error * (2.0 / error.numel())).bfloat16(), y, r, plan=student.plan)
+        student.update(student.backward(rows, hidden, dy, r.offsets), rate * (1 - step / steps))
         if verbose and step % 10 == 0:
-            print(f"step {step:3d}  loss {losses[-1]:.4f}")
+            print(f"step {step:3d}  loss {losses[-1]:.4f}  balance {float(r.loss):.3f}")
     # One token at a time, with 4-bit weights.
     packed = student.quantised(group)
     worst = 0.0
     for _ in range(4):
         x = torch.randn((1, d), generator=gen, device="cuda").bfloat16()
-        offsets, order, weight = route(x, router)
-        rows = x[order]
-        full = combine(student.forward(rows, offsets)[0], order, weight, 1)
-        low = combine(serve_q4(rows, offsets, packed, student.b1, group, student.plan), order, weight, 1)
+        r = G.route(x.float() @ router, TOP, plan=student.plan32)
+        rows = G.dispatch(x, r, plan=student.plan)
+        full = G.combine(student.forward(rows, r.offsets)[0], r, plan=student.plan).float()
+        low = G.combine(serve_q4(rows, r.offsets, packed, student.b1, group, student.plan), r, plan=student.plan).float()
         worst = max(worst, float((low - full).norm() / full.norm()))
     if verbose:
         print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f}; 4-bit weights change an output by {100 * worst:.1f} % at most")

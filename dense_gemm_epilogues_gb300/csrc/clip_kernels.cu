@@ -6,7 +6,9 @@
 // and scales its share, last entries first, since those are what the first pass left in L2.
 // A CTA takes chunks of the tensors laid end to end (each tensor starts a chunk), so one
 // long tensor and a thousand short ones occupy the chip alike.  Bound by memory: three
-// trips over lists longer than L2, of which two are the floor.
+// trips over lists longer than L2, of which two are the floor.  369 million fp32 entries to
+// bf16: 557 us, 6.6 TB/s over the three trips (2.2 GB are the floor's, 3.7 move); 2.1 million,
+// fp32: 9.9 us.
 //
 // Squares are added in fp32 over eight entries at a time and over four such sums, then in
 // fp64, in which only one warp of a CTA adds up and one thread takes the root: this chip adds

@@ -57,8 +57,8 @@ struct RouteParams {
   // Of the forward pass.
   int32_t blocks, warps;     // CTAs that choose, and their warps
   int32_t per_warp;          // tokens of a warp
-  int32_t* hist;             // blocks x (experts + 1): rows of every expert, tokens with any
-  float* mass;               // blocks x experts: sums of the probabilities
+  int32_t* hist;             // blocks x route_pitch: rows of every expert, tokens with any
+  float* mass;               // blocks x route_pitch: sums of the probabilities
   // Of the gradient.
   const float* dweights;     // tokens x top, or null
   const float* dloss;        // or null: 1
@@ -66,6 +66,7 @@ struct RouteParams {
   void* dlogits;             // tokens x experts, pitch ldd, logits' type
   int64_t ldd;
 };
+__host__ __device__ inline int route_pitch(int experts) { return (experts + 4) / 4 * 4; }   // experts + 1, whole 16 bytes
 int route_blocks(int64_t tokens, int64_t experts, int sm_count);   // RouteParams::blocks
 int route_warps(int64_t experts);                                  // RouteParams::warps
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);

@@ -340,8 +340,8 @@ gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, cons
   p.warps = route_warps(experts);
   p.per_warp = (int32_t)((tokens + (int64_t)p.blocks * p.warps - 1) / ((int64_t)p.blocks * p.warps));
   if (p.blocks > 1) {
-    const size_t hist = align_up((size_t)p.blocks * (size_t)(experts + 1) * sizeof(int32_t), 256);
-    s = ensure_ws(plan, hist + (size_t)p.blocks * (size_t)experts * sizeof(float), stream);
+    const size_t hist = align_up((size_t)p.blocks * (size_t)route_pitch((int)experts) * sizeof(int32_t), 256);
+    s = ensure_ws(plan, 2 * hist, stream);
     if (s != GEMM_OK) return s;
     p.hist = static_cast<int32_t*>(plan->ws.p);
     p.mass = reinterpret_cast<float*>(static_cast<char*>(plan->ws.p) + hist);

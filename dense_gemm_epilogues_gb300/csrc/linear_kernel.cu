@@ -11,9 +11,15 @@
 // K, through distributed shared memory, and finishes it.  No scratch, no counters; two CTAs
 // per SM, so that one's start and end hide behind the other's stream.
 //
+// Measured (graph replays, weights from HBM): 1 row, 4096 to 11008 17.4 us for 90 MB, of which
+// 13.3 at the copy rate; the slope over larger widths is 7 TB/s, and 4.2 us go to the launch,
+// the first loads' latency and the last sums. 4096 to 4096 9.5 us (four CTAs per tile; one
+// 20), 7 rows of 11008 to 4096 18.4, 128 rows of 1024 to 1024 6.5.
+//
 // act_grad_kernel: dz = dy act'(z) in the operands' type, and its column sums (the bias's
 // gradient) from the unrounded values: one pass at memory speed; a column's sums are added
-// over row blocks by column_sums_kernel in one order.
+// over row blocks by column_sums_kernel in one order.  4096 x 11008 with GELU: 46 us for both,
+// 5.9 TB/s; with loads into registers instead of copies ahead 64.
 //
 // Every wait is bounded, as in tc_kernel.cu.
 #include "layer.h"

@@ -390,8 +390,9 @@ def _fills(t) -> bool:
 
 class TensorList:
     """Tensors whose global norm is taken and that are scaled together, laid out once: the
-    gradients that a program keeps from step to step.  out: where the scaled values go, tensors
-    of the same shapes and strides and any of the types (None: in place)."""
+    gradients that a program keeps from step to step (a tensor that has other memory by the time
+    of a call is refused).  out: where the scaled values go, tensors of the same shapes and
+    strides and any of the types (None: in place)."""
 
     def __init__(self, tensors, out=None):
         self.tensors, self.out = list(tensors), list(out) if out is not None else None
@@ -419,10 +420,18 @@ class TensorList:
             end = max(end, hi)
             written_end = max(written_end, hi) if written else written_end
         self.device = _device(*self.tensors, *(self.out or ())) if self.tensors else None
+        self._all = self.tensors + (self.out or [])
+        self._at = [t.data_ptr() for t in self._all]
+
+    def check(self):
+        if [t.data_ptr() for t in self._all] != self._at:
+            raise ValueError("a tensor of the list has moved")
 
 
 def _norm_of(tensors, max_norm: float, eps: float, scales: bool, plan, stream):
-    if not isinstance(tensors, TensorList):
+    if isinstance(tensors, TensorList):
+        tensors.check()
+    else:
         tensors = TensorList(tensors)
     if not max_norm >= 0 or not 0 <= eps < math.inf:
         raise ValueError("max_norm and eps must not be negative, and eps finite")

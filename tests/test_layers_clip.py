@@ -178,4 +178,10 @@ def test_refusals():
                 lambda: G.TensorList([a], out=[torch.zeros(99, device="cuda")]), lambda: G.TensorList([a[:50]], out=[a[10:60]])):
         with pytest.raises(ValueError):
             bad()
+    moved = torch.zeros(100, device="cuda")
+    kept = G.TensorList([moved])
+    G.clip_grad_norm(kept, 1.0)
+    moved.data = torch.zeros(100, device="cuda")
+    with pytest.raises(ValueError):
+        G.clip_grad_norm(kept, 1.0)
     G.TensorList([a[:50], a[:50]], out=[torch.zeros(50, device="cuda"), torch.zeros(50, device="cuda")])

@@ -250,6 +250,50 @@ def test_layers_together_in_a_graph_and_on_another_stream(M):
     assert plan.device_status() == 0
 
 
+def test_a_forced_kernel_is_for_other_calls():
+    """set_kernel is gemm_run's: the layers choose for themselves and leave it as it was."""
+    x, w = _layer(100, 264, 200, "f16")
+    dy = _rand((100, 200), "f16", 3)
+    plan = G.Plan(G.GEMM_F16, G.GEMM_F32)
+    want = G.linear_grad(dy, x, w, plan=plan)
+    plan.set_kernel(G.GEMM_KERNEL_SIMT)
+    got = G.linear_grad(dy, x, w, plan=plan)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    G.matmul(x, w, plan=plan)
+    assert plan.last_config()["kernel"] == G.GEMM_KERNEL_SIMT
+
+
+@pytest.mark.parametrize("planned", [False, True])
+def test_calls_on_two_streams_at_once(planned):
+    """Two layers on two streams behind queued work, with default plans or one each: their scratch
+    (operands that TMA cannot address, dz) is not shared."""
+    sets = []
+    for i in range(2):
+        x, w = _layer(300 + 40 * i, 131, 517, "bf16", seed=10 * i)
+        sets.append((x, w, _rand((x.shape[0], 517), "bf16", 5 + i), _rand((x.shape[0], 517), "bf16", 7 + i)))
+    plans = [G.Plan(G.GEMM_BF16, G.GEMM_F32) if planned else None for _ in range(2)]
+
+    def run(i):
+        x, w, dy, pre = sets[i]
+        y = G.linear(x, w, activation="gelu", residual=dy, plan=plans[i])
+        return [y, *G.linear_grad(dy, x, w, activation="gelu", pre=pre, plan=plans[i])]
+
+    want = [[t.clone() for t in run(i)] for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(50_000_000)
+    for turn in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, run(i)))
+    torch.cuda.synchronize()
+    for i, r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
+
+
 @pytest.mark.parametrize("M,N", [(5, 4096), (600, 9000)])
 def test_expired_waits_are_reported_and_the_plan_survives(M, N):
     x, w = _layer(M, 8192, N, "f16")

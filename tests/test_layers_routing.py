@@ -40,7 +40,7 @@ def _check(z, top, renormalize=True, mask=None, r=None, **kw):
 
 
 SIZES = [(1, 1, 1), (1, 8, 2), (3, 5, 5), (16, 8, 2), (64, 64, 6), (65, 33, 4), (257, 32, 8), (1000, 64, 1),
-         (300, 100, 7), (90, 160, 6), (77, 257, 32), (130, 512, 8), (70, 1000, 9), (66, 1024, 32), (4097, 16, 3)]
+         (300, 100, 7), (90, 160, 6), (77, 257, 32), (130, 512, 8), (70, 1000, 9), (66, 1024, 32), (4097, 16, 3), (150000, 12, 2), (700, 1023, 3)]
 
 
 @pytest.mark.parametrize("tokens,experts,top", SIZES)

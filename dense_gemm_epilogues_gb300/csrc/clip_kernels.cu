@@ -7,8 +7,8 @@
 // A CTA takes chunks of the tensors laid end to end (each tensor starts a chunk), so one
 // long tensor and a thousand short ones occupy the chip alike.  Bound by memory: three
 // trips over lists longer than L2, of which two are the floor.  369 million fp32 entries to
-// bf16: 557 us, 6.6 TB/s over the three trips (2.2 GB are the floor's, 3.7 move); 2.1 million,
-// fp32: 9.9 us.
+// bf16: 549 us, 6.7 TB/s over the three trips (2.2 GB are the floor's, 3.7 move); 2.1 million,
+// fp32: 8.6 us.
 //
 // Squares are added in fp32 over eight entries at a time and over four such sums, then in
 // fp64, in which only one warp of a CTA adds up and one thread takes the root: this chip adds
@@ -21,7 +21,9 @@ namespace gemmlib {
 namespace {
 
 constexpr int THREADS = 512;
-constexpr int UNROLL = 4;   // units of 8 entries that a thread has under way
+// Units of 8 entries that a thread has under way: 128 bytes where they are only read (beside the
+// scaled values eight units would leave room for one CTA per SM).
+__host__ __device__ constexpr int units_of(int dtype, bool scales) { return dtype == GEMM_F32 || scales ? 4 : 8; }
 
 template <int CAP>
 struct ClipList {
@@ -53,36 +55,50 @@ __host__ __device__ __forceinline__ int lead_of(const void* p, int es) {
   return (int)((reinterpret_cast<uintptr_t>(p) & (uintptr_t)(8 * es - 1)) / (unsigned)es);
 }
 
-// Entries i .. i + 7 (zeros outside 0 .. n - 1).
+// Entries i .. i + 7 (zeros outside 0 .. n - 1) as they lie in memory: 16 bits take half the
+// registers of their values while a thread's units are under way.
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, float (&x)[8]) {
-  if (i >= n) {
+struct Unit {
+  static constexpr int WORDS = DT == GEMM_F32 ? 8 : 4;
+  uint32_t w[WORDS];
+
+  __device__ __forceinline__ void load(const void* p, int64_t i, int64_t n) {
+    if (i >= 0 && i + 8 <= n) {
+      if constexpr (DT == GEMM_F32) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(static_cast<const float*>(p) + i)
+                     : "memory");
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      }
+      return;
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-  } else if (i >= 0 && i + 8 <= n) {
-    if constexpr (DT == GEMM_F32) {
-      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
-                   : "l"(static_cast<const float*>(p) + i)
-                   : "memory");
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int k = 0; k < WORDS; ++k) w[k] = 0u;
+    if (i >= n) return;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        if constexpr (DT == GEMM_F16) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-          x[2 * h] = f.x, x[2 * h + 1] = f.y;
-        } else {
-          x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
-        }
+    for (int j = 0; j < 8; ++j) {
+      if (i + j < 0 || i + j >= n) continue;
+      if constexpr (DT == GEMM_F32) w[j] = static_cast<const uint32_t*>(p)[i + j];
+      else w[j / 2] |= (uint32_t) static_cast<const uint16_t*>(p)[i + j] << (16 * (j % 2));
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if constexpr (DT == GEMM_F32) {
+        x[2 * h] = __uint_as_float(w[2 * h]), x[2 * h + 1] = __uint_as_float(w[2 * h + 1]);
+      } else if constexpr (DT == GEMM_F16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
+        x[2 * h] = f.x, x[2 * h + 1] = f.y;
+      } else {
+        x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
       }
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = i + j >= 0 && i + j < n ? load_as_float(p, DT, i + j) : 0.0f;
   }
-}
+};
 
 // vec: the units are aligned in this tensor too.
 template <int DT>
@@ -145,7 +161,7 @@ __device__ __forceinline__ double warp_total(const double* v, int n, int lane) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(THREADS) clip_norm_kernel(const __grid_constant__ ClipList<CAP> l,
+__global__ void __launch_bounds__(THREADS, 2) clip_norm_kernel(const __grid_constant__ ClipList<CAP> l,
                                                             const __grid_constant__ ClipPass p, int first_partial) {
   __shared__ double smem[THREADS];
   pdl_launch_dependents();
@@ -159,15 +175,22 @@ __global__ void __launch_bounds__(THREADS) clip_norm_kernel(const __grid_constan
       constexpr int DT = decltype(dt)::value;
       const int64_t lo = (int64_t)(c - l.first[t]) * p.chunk - lead_of(src, DT == GEMM_F32 ? 4 : 2);
       const int64_t hi = min(l.count[t], lo + p.chunk);
-      for (int64_t at = lo; at < hi; at += 8 * THREADS * UNROLL) {
-        float x[UNROLL][8];
+      constexpr int UNITS = units_of(DT, false);
+      for (int64_t at = lo; at < hi; at += 8 * THREADS * UNITS) {
+        Unit<DT> v[UNITS];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) load8<DT>(src, unit_at(at, u), hi, x[u]);
-        float s = 0.0f;
+        for (int u = 0; u < UNITS; ++u) v[u].load(src, unit_at(at, u), hi);
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
-          if (unit_at(at, u) < hi) s += squares(x[u], wide);
-        if (s != 0.0f) wide += (double)s;
+        for (int h = 0; h < UNITS; h += 4) {
+          float s = 0.0f;
+#pragma unroll
+          for (int u = h; u < h + 4; ++u) {
+            float x[8];
+            v[u].get(x);
+            if (unit_at(at, u) < hi) s += squares(x, wide);
+          }
+          if (s != 0.0f) wide += (double)s;
+        }
       }
     });
   }
@@ -180,7 +203,7 @@ __global__ void __launch_bounds__(THREADS) clip_norm_kernel(const __grid_constan
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(THREADS) clip_scale_kernel(const __grid_constant__ ClipList<CAP> l,
+__global__ void __launch_bounds__(THREADS, 2) clip_scale_kernel(const __grid_constant__ ClipList<CAP> l,
                                                              const __grid_constant__ ClipPass p, int write_norm) {
   __shared__ float factor;
   pdl_launch_dependents();
@@ -196,7 +219,7 @@ __global__ void __launch_bounds__(THREADS) clip_scale_kernel(const __grid_consta
   }
   __syncthreads();
   const float scale = factor;
-  const int chunks = l.first[l.tensors];
+  const int chunks = p.scales ? l.first[l.tensors] : 0;
   for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
     const int c = chunks - 1 - i, t = tensor_of(l, c);
     const void* src = l.src[t];
@@ -210,15 +233,18 @@ __global__ void __launch_bounds__(THREADS) clip_scale_kernel(const __grid_consta
         const int64_t lo = (int64_t)(c - l.first[t]) * p.chunk - lead, hi = min(l.count[t], lo + p.chunk);
         const uintptr_t from = reinterpret_cast<uintptr_t>(dst) - (uintptr_t)(lead * (DT == GEMM_F32 ? 4 : 2));
         const bool vec = (from & 15) == 0;
-        for (int64_t at = lo; at < hi; at += 8 * THREADS * UNROLL) {
-          float x[UNROLL][8];
+        constexpr int UNITS = units_of(ST, true);
+        for (int64_t at = lo; at < hi; at += 8 * THREADS * UNITS) {
+          Unit<ST> v[UNITS];
 #pragma unroll
-          for (int u = 0; u < UNROLL; ++u) load8<ST>(src, unit_at(at, u), hi, x[u]);
+          for (int u = 0; u < UNITS; ++u) v[u].load(src, unit_at(at, u), hi);
 #pragma unroll
-          for (int u = 0; u < UNROLL; ++u) {
+          for (int u = 0; u < UNITS; ++u) {
+            float x[8];
+            v[u].get(x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[u][j] *= scale;
-            if (unit_at(at, u) < hi) store8<DT>(dst, unit_at(at, u), hi, vec, x[u]);
+            for (int j = 0; j < 8; ++j) x[j] *= scale;
+            if (unit_at(at, u) < hi) store8<DT>(dst, unit_at(at, u), hi, vec, x);
           }
         }
       });
@@ -247,13 +273,15 @@ ClipList<CAP> list_of(const ClipTensor* t, int count, int64_t chunk) {
 
 }  // namespace
 
-// Chunks of 4096 to 32768 entries: small enough that the list gives every resident CTA
-// several, large enough that finding a chunk's tensor costs nothing beside it.
+// Up to 32768 entries, so that finding a chunk's tensor costs nothing beside it, and as many
+// that all resident CTAs (two per SM) take equally many: 10.5 million bf16 entries 17 us, with
+// chunks of 8192 22.
 int64_t clip_chunk(int64_t total, int sm_count) {
-  int64_t chunk = 4096;
-  while (chunk < 32768 && total / chunk > 16 * (int64_t)sm_count) chunk *= 2;
-  // (chunk numbers are 32-bit)
-  while (total / chunk >= (int64_t(1) << 30)) chunk *= 2;
+  const int64_t ctas = 2 * (int64_t)sm_count;
+  const int64_t rounds = std::max<int64_t>(1, (total + ctas * 32768 - 1) / (ctas * 32768));
+  int64_t chunk = std::max<int64_t>(1, (total + ctas * rounds - 1) / (ctas * rounds) + 4095) / 4096 * 4096;
+  chunk = std::max<int64_t>(4096, chunk);
+  while (total / chunk >= (int64_t(1) << 30)) chunk *= 2;   // (chunk numbers are 32-bit)
   return chunk;
 }
 

@@ -107,6 +107,7 @@ struct ClipPass {
   int64_t chunk;             // entries that a CTA takes at a time (a multiple of 8)
   double* partials;          // one per CTA of every norm launch
   int32_t num_partials;
+  int32_t scales;            // some tensor has a place for its scaled values
   float max_norm, eps;
   float* norm;
 };

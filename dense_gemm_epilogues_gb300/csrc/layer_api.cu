@@ -484,6 +484,7 @@ gemm_status_t gemm_clip_norm(gemm_plan_t plan, int64_t count, const gemm_tensor_
   p.max_norm = (float)max_norm;
   p.eps = (float)eps;
   p.norm = norm;
+  p.scales = scales ? 1 : 0;
   ClipTensor part[PART];
   auto fill = [&](int64_t i) {
     const int n = (int)std::min<int64_t>(PART, count - i * PART);

@@ -622,7 +622,8 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
 
 /* Activations of a fully connected layer.  GELU is x P(x) with the normal distribution P,
  * GELU_TANH its usual approximation 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))), SILU
- * x / (1 + exp(-x)).  All keep NaN. */
+ * x / (1 + exp(-x)).  All keep NaN.  P is off by at most 2.3e-7 (1e-6 of its value down to
+ * x = -4), exponentials and quotients by two fp32 steps each. */
 typedef enum {
     GEMM_LINEAR_NONE = 0,
     GEMM_LINEAR_RELU = 1,

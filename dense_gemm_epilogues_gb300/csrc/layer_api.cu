@@ -271,18 +271,19 @@ gemm_status_t gemm_run_linear_grad(gemm_plan_t plan, gemm_layout_t lb, int64_t M
   const size_t zb = M == 0 || N == 0 ? 0 : acts ? align_up((size_t)(M * ldz) * 2, 256) : repitch_bytes(dy, M, N, 1);
   const size_t xb = want_b && M > 0 ? repitch_bytes(x, M, K, 1) : 0;
   const size_t wb = want_a && N > 0 ? repitch_bytes(w, wrows, wcols, 1) : 0;
-  // Blocks of rows: CTAs for four per SM, at least 32 rows each.
+  // Blocks of rows: CTAs for four per SM, at least 32 rows each.  One block (up to 64 rows) writes
+  // the bias's gradient itself: one launch less.
   const int64_t strips = (N + 255) / 256;
   const int64_t want = std::max<int64_t>(1, 4 * (int64_t)plan->sm_count / std::max<int64_t>(1, strips));
-  const int64_t block_rows = std::max<int64_t>(32, (M + want - 1) / want);
+  const int64_t block_rows = M <= 64 ? std::max<int64_t>(M, 1) : std::max<int64_t>(32, (M + want - 1) / want);
   const int blocks = (int)((M + block_rows - 1) / block_rows);
-  const size_t pb = want_bias ? (size_t)blocks * (size_t)N * sizeof(float) : 0;
+  const size_t pb = want_bias && blocks > 1 ? (size_t)blocks * (size_t)N * sizeof(float) : 0;
   if (zb + xb + wb + pb > 0) {
     s = ensure_ws(plan, zb + xb + wb + pb, stream);
     if (s != GEMM_OK) return s;
   }
   char* ws = static_cast<char*>(plan->ws.p);
-  float* partials = want_bias ? reinterpret_cast<float*>(ws + zb + xb + wb) : nullptr;
+  float* partials = !want_bias ? nullptr : blocks == 1 ? dbias : reinterpret_cast<float*>(ws + zb + xb + wb);
   if (M > 0 && N > 0 && (acts || want_bias)) {
     ActGradParams p{};
     p.dy = dY;
@@ -299,7 +300,8 @@ gemm_status_t gemm_run_linear_grad(gemm_plan_t plan, gemm_layout_t lb, int64_t M
     p.partials = partials;
     if (launch_act_grad(p, plan->ab, blocks, stream) != cudaSuccess) return GEMM_ERR_CUDA;
   }
-  if (want_bias && launch_column_sums(partials, blocks, N, dbias, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (want_bias && blocks != 1 && launch_column_sums(partials, blocks, N, dbias, stream) != cudaSuccess)
+    return GEMM_ERR_CUDA;
   if (acts) dy = Operand{ws, ldz, 0};
   else if (zb > 0) s = repitch(&dy, M, N, 1, nullptr, ws, stream);
   if (s == GEMM_OK && xb > 0) s = repitch(&x, M, K, 1, nullptr, ws + zb, stream);

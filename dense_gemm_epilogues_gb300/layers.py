@@ -421,10 +421,10 @@ class TensorList:
             written_end = max(written_end, hi) if written else written_end
         self.device = _device(*self.tensors, *(self.out or ())) if self.tensors else None
         self._all = self.tensors + (self.out or [])
-        self._at = [t.data_ptr() for t in self._all]
+        self._at = list(map(torch.Tensor.data_ptr, self._all))
 
     def check(self):
-        if [t.data_ptr() for t in self._all] != self._at:
+        if list(map(torch.Tensor.data_ptr, self._all)) != self._at:
             raise ValueError("a tensor of the list has moved")
 
 

@@ -93,6 +93,20 @@ def test_residual_in_place_and_rows_that_are_not_read():
     assert not dy.isnan().any() and not dw.isnan().any()
 
 
+@pytest.mark.parametrize("width", [64, 61])
+def test_nothing_is_written_around_the_outputs(width):
+    T, top = 90, 3
+    r = _routing(T, 16, top)
+    x, y = _rand((T, width), "bf16", 1), _rand((T * top, width), "bf16", 2)
+    for call, rows in ((lambda o: G.dispatch(x, r, out=o), T * top), (lambda o: G.combine(y, r, residual=x, out=o), T),
+                       (lambda o: G.dispatch_grad(y, r, out=o), T), (lambda o: G.combine_grad(x, y, r, out=o), T * top)):
+        wide = torch.full((rows + 4, width + 24), 7.0, device="cuda", dtype=torch.bfloat16)
+        call(wide[2:-2, 8:8 + width])
+        inner = torch.zeros_like(wide, dtype=torch.bool)
+        inner[2:-2, 8:8 + width] = True
+        assert (wide[~inner] == 7).all() and not (wide[inner] == 7).all()
+
+
 def test_bad_slots_touch_nothing_and_are_reported():
     r = _routing(40, 8, 2, padded=False)
     bad = r.slots.clone()

@@ -141,6 +141,26 @@ def test_strides_and_kept_buffers(tokens, experts, top):
     assert (d[:, :2] == 7).all() and (d[:, 2 + experts:] == 7).all()
 
 
+@pytest.mark.parametrize("tokens,experts,top", [(9, 5, 3), (64, 8, 2), (65, 33, 4), (2000, 100, 6), (300, 1024, 5)])
+def test_nothing_is_written_around_a_routing(tokens, experts, top):
+    z = _logits(tokens, experts, "f32", 3)
+    f = torch.full((tokens * top + 9,), 7.0, device="cuda")
+    i = torch.full((2 * tokens * top + 2 * experts + 40,), 7, dtype=torch.int32, device="cuda")
+    at, views = 4, []
+    for n, shape in ((tokens * top, (tokens, top)), (tokens * top, (tokens, top)), (experts, (experts,)),
+                     (experts + 1, (experts + 1,)), (1, ())):
+        views.append(i[at:at + n].view(shape))
+        at += n + 4
+    out = G.Routing(f[4:4 + tokens * top].view(tokens, top), *views, f[-1:].view(()))
+    guard = torch.ones_like(i, dtype=torch.bool)
+    at = 4
+    for n in (tokens * top, tokens * top, experts, experts + 1, 1):
+        guard[at:at + n] = False
+        at += n + 4
+    _check(z, top, r=G.route(z, top, out=out))
+    assert (i[guard] == 7).all() and (f[:4] == 7).all() and (f[4 + tokens * top:-1] == 7).all()
+
+
 @pytest.mark.parametrize("tokens,experts,top", SIZES)
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("renormalize", [True, False])

@@ -11,8 +11,8 @@
 // eight warps of a CTA together -- with its slots and weights in its lanes, and goes along the
 // row in pieces of 16 bytes per lane, several pieces and rows under way.  16384 tokens, top 2,
 // width 2048, bf16: dispatch and combine 68 us, 5.9 TB/s of what they have to move (with half the
-// loads under way 93); 8191 tokens, top 4, width 4096: combine_grad and dispatch's gradient 148
-// us, 6.4 TB/s.
+// loads under way 93); 8191 tokens, top 4, width 4096: combine_grad and dispatch's gradient 143
+// us, 6.6 TB/s.
 //
 // A slot outside the sorted buffer is no row; one that is not -1 either is reported through
 // the error word.
@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(THREADS) dispatch_kernel(const __grid_constant
 }
 
 // Eight loads of sorted rows per lane under way, and as many of the residual as pieces: all
-// ROWS rows of 8 / ROWS pieces.  ROWS is at least top, or 8.
+// ROWS rows of 8 / ROWS pieces.  ROWS is the least of 2, 4 and 8 that holds top, or 8: 16384 tokens,
+// top 2, 2048 wide 41, 44 and 59 us with ROWS of 2, 4 and 8.
 template <int DT, bool WIDE, int ROWS>
 __global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant__ ExchangeParams p) {
   using P = Piece<DT, WIDE>;
@@ -283,10 +284,17 @@ enum { DISPATCH, COMBINE, COMBINE_GRAD };
 
 template <int WHAT, int DT, bool WIDE>
 cudaError_t launch_as(ExchangeParams p, int sm_count, cudaStream_t stream) {
-  // Up to eight warps share a token while the chip has less than 16 warps per SM and a warp
-  // more than one turn of its row.
+  // Warps of a token: as many as leave each lane two turns of its loads (four pieces of dispatch,
+  // eight of combine_grad), so that a row's bytes are asked for closer together; more,
+  // down to one piece per lane, while the chip has less than 16 warps per SM.  At most eight.
+  // Measured with one warp / the rule's, us: dispatch of 3000 tokens, top 2, 4096 wide 11.7 / 10.7
+  // (four), 6000 of 8192 52.3 / 45.7 (eight), 16 tokens of 8192 6.6 / 2.4 (eight); combine of 8191,
+  // top 4, 4096 63.6 / 59.7 (four), of 16384, top 2, 2048 41.0 with one, 48.5 with four; combine_grad
+  // of 6000, top 2, 8192 88.9 / 78.4 (four), of 16384, top 2, 1024 31.7 with one, 34.1 with two.
   const int64_t per = p.width / Piece<DT, WIDE>::N;
+  const int64_t keep = WHAT == DISPATCH ? 4 : WHAT == COMBINE_GRAD ? 8 : p.top <= 2 ? 8 : p.top <= 4 ? 4 : 2;
   p.parts_shift = 0;
+  while (p.parts_shift < 3 && per >= (32 * keep << (p.parts_shift + 1))) ++p.parts_shift;
   while (p.parts_shift < 3 && (p.tokens << p.parts_shift) < 16 * (int64_t)sm_count && per > (int64_t)(32 << p.parts_shift))
     ++p.parts_shift;
   const int64_t work = ((p.tokens << p.parts_shift) + WARPS - 1) / WARPS;

@@ -272,7 +272,8 @@ gemm_status_t gemm_run_linear_grad(gemm_plan_t plan, gemm_layout_t lb, int64_t M
   const size_t xb = want_b && M > 0 ? repitch_bytes(x, M, K, 1) : 0;
   const size_t wb = want_a && N > 0 ? repitch_bytes(w, wrows, wcols, 1) : 0;
   // Blocks of rows: CTAs for four per SM, at least 32 rows each.  One block (up to 64 rows) writes
-  // the bias's gradient itself: one launch less.
+  // the bias's gradient itself, one launch less: blocks of 32 / one, us: 64 x 11008 5.3 / 3.7, 128 x
+  // 4096 5.4 / 5.7, 256 x 1024 3.7 / 10.1.
   const int64_t strips = (N + 255) / 256;
   const int64_t want = std::max<int64_t>(1, 4 * (int64_t)plan->sm_count / std::max<int64_t>(1, strips));
   const int64_t block_rows = M <= 64 ? std::max<int64_t>(M, 1) : std::max<int64_t>(32, (M + want - 1) / want);

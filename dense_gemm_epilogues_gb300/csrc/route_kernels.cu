@@ -445,12 +445,13 @@ cudaError_t launch_smem(void (*kernel)(P...), int grid, int threads, size_t smem
 
 }  // namespace
 
-// CTAs that choose: one for up to 64 tokens (two or four per warp: one launch takes less than
-// two), else one per SM as long as a warp has a token.
+// CTAs that choose: one, and one launch, for up to two tokens per warp; else one per SM as long
+// as a warp has a token.  One launch / two, us: 64 tokens, top 6 of 64 6.7 / 7.4, 128 tokens 10.0 / 7.5;
+// 64 tokens, top 8 of 512 (half the warps) 23.1 / 12.3.
 int route_warps(int64_t experts) { return warps_of(experts <= 32 ? 1 : experts <= 64 ? 2 : experts <= 128 ? 4 : 8); }
 int route_blocks(int64_t tokens, int64_t experts, int sm_count) {
-  if (tokens <= 64) return 1;
   const int warps = route_warps(experts);
+  if (tokens <= 2 * warps) return 1;
   return (int)std::min<int64_t>(sm_count, (tokens + warps - 1) / warps);
 }
 

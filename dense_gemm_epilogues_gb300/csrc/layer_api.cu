@@ -147,9 +147,21 @@ gemm_status_t linear_product(gemm_plan* plan, int64_t M, int64_t N, int64_t K, c
   }
   SegParams p;
   std::memset(&p, 0, sizeof(p));
+  // Single CTAs (128 x 128) or CTA pairs (256 x 256) by the times that both take, in us: single ones
+  // share the operands' supply, so part of a wave costs its part; a pair's tile costs 0.33 per 64 k
+  // like a single one's, but its epilogue and first loads more, and its waves are whole.  Measured,
+  // single / pairs (with GELU and residual): 4096 rows, 1024 to 1024 15.7 / 16.9; 1500 rows, 1024 to
+  // 4096 20.3 / 24.4; 1000 rows, 1000 to 2048 11.0 / 15.6, 2048 to 4096 21.1 / 21.2; 2000 rows, 2000 to
+  // 2000 23.9 / 22.1; 512 rows, 4096 to 11008 50.7 / 51.3; 1929 rows, 10288 to 4184 208 / 125; 200
+  // rows, 256 to 12000 11.1 / 11.6.  The estimate takes the faster side of all these.
   const int64_t tiles256 = (N + 255) / 256 * ((M + 255) / 256), tiles128 = (N + 127) / 128 * ((M + 127) / 128);
-  const bool fill = 4 * tiles256 >= 3 * plan->pair_clusters || tiles128 > plan->sm_count;
-  const int cg = plan->pair_clusters > 0 && M >= 128 && fill ? 2 : 1;
+  int cg = 1;
+  if (plan->pair_clusters > 0 && M >= 128) {
+    const double per_tile = 0.33 * (double)((K + TC_BK - 1) / TC_BK);
+    const double single = 4.5 + std::max(1.0, (double)tiles128 / plan->sm_count) * (per_tile + 0.9);
+    const double pairs = 9.0 + (double)((tiles256 + plan->pair_clusters - 1) / plan->pair_clusters) * (per_tile + 1.7);
+    cg = pairs < single ? 2 : 1;
+  }
   const int64_t tiles = cg == 2 ? tiles256 : tiles128;
   if (tiles > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
   if (K > 0) {

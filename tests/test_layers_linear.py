@@ -71,6 +71,18 @@ def test_linear(M, K, N, box, splits, layout, dtype, act):
     assert ((c["bn"], c["split_k"]) if c["bk"] == 64 else (0, 0)) == (box, splits) and plan.device_status() == 0
 
 
+# Single CTAs and pairs of the tile kernel: rows of one and of several tiles, ragged last ones.
+@pytest.mark.parametrize("M,K,N,cta_group", [(65, 130, 300, 1), (1000, 1000, 2048, 1), (520, 72, 12000, 1), (250, 4100, 19001, 2),
+                                             (700, 2100, 6000, 2), (2040, 1990, 2100, 2), (3001, 640, 5000, 2)])
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32")])
+def test_single_ctas_and_pairs(M, K, N, cta_group, layout, dtype, out):
+    x, w = _layer(M, K, N, dtype, layout)
+    plan = G.Plan(G.DTYPE_CODES[dtype], G.GEMM_F32)
+    _check(x, w, "gelu", _rand((N,), "bf16", 3), _rand((M, N), out, 4), out, dtype, plan=plan)
+    assert plan.last_config()["cta_group"] == cta_group and plan.device_status() == 0
+
+
 @pytest.mark.parametrize("act", ACTS, ids=str)
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("M,K,N", [(5, 96, 200), (260, 128, 10001)])

@@ -262,6 +262,32 @@ def test_layers_together_in_a_graph_and_on_another_stream(M):
     assert plan.device_status() == 0
 
 
+def test_a_layer_past_four_gigabytes():
+    """Offsets past 32 bits in every operand that is as large as the result: 70000 x 40000 entries of
+    bf16; the first, middle and last rows."""
+    M, K, N = 70000, 64, 40000
+    x, w = _layer(M, K, N, "bf16")
+    res = torch.randn((M, N), device="cuda", generator=torch.Generator("cuda").manual_seed(5)).bfloat16()
+    y, pre = G.linear(x, w, activation="gelu", residual=res, save_pre=True)
+    rows = [0, 1, M // 2, M - 2, M - 1]
+    ref, z, ey, ez = linear_ref(x[rows], w, None, "gelu", res[rows])
+    within(y[rows], ref, U["bf16"] * (ref.abs() + ey) + ey, "y")
+    within(pre[rows], z, U["bf16"] * (z.abs() + ez) + ez, "pre")
+    del y
+    dx, _, db = G.linear_grad(res, x, w, activation="gelu", pre=pre, weight_grad=False)
+    _, d = act_ref(pre[rows].double(), "gelu")
+    dz = res[rows].double() * d
+    step = U["bf16"] * dz.abs() + res[rows].double().abs() * act_grad_error(pre[rows].double(), "gelu")
+    ref, wd = dz @ w.double().t(), w.double().abs().t()
+    e = (N + 4) * EPS * (dz.abs() @ wd) + 1.01 * (step @ wd)
+    within(dx[rows], ref, U["bf16"] * (ref.abs() + e) + e, "dx")
+    cols = [0, 20000, N - 1]
+    _, d = act_ref(pre[:, cols].double(), "gelu")
+    dz = res[:, cols].double() * d
+    e = (M + 4) * 2.0 ** -24 * dz.abs().sum(0) + (res[:, cols].double().abs() * act_grad_error(pre[:, cols].double(), "gelu")).sum(0)
+    within(db[cols], dz.sum(0), e, "db")
+
+
 def test_a_forced_kernel_is_for_other_calls():
     """set_kernel is gemm_run's: the layers choose for themselves and leave it as it was."""
     x, w = _layer(100, 264, 200, "f16")

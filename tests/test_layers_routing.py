@@ -206,6 +206,27 @@ def test_gradient_against_differences(renormalize):
             assert abs((value(up) - value(down)) / (2 * h) - float(d[t, e])) < 1e-5
 
 
+def test_logits_past_four_gigabytes():
+    """2.2 million tokens by 1000 experts in fp16: offsets past 32 bits; the last tokens' choices,
+    weights and gradients, and the counts of all."""
+    T, E, top, n = 2_200_000, 1000, 2, 50
+    z = torch.empty((T, E), device="cuda", dtype=torch.float16)
+    for i in range(0, T, 200_000):
+        z[i:i + 200_000] = torch.randn((200_000, E), device="cuda", generator=torch.Generator("cuda").manual_seed(i)).half()
+    r = G.route(z, top)
+    w, experts, *_, spread = route_ref(z[-n:], top)
+    assert torch.equal(r.experts[-n:].long().cpu(), experts)
+    within(r.weights[-n:].cpu(), w, 2 * (8 + 2 * spread) * EPS * w, "weights")
+    assert torch.equal(r.counts.long(), torch.bincount(r.experts.flatten().long(), minlength=E))
+    assert int(r.offsets[-1]) == T * top and int(r.routed) == T
+    place = torch.argsort(r.experts.flatten().long(), stable=True)
+    assert torch.equal(r.slots.flatten()[place].long(), torch.arange(T * top, device="cuda"))
+    dw = torch.randn((T, top), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    d = G.route_grad(z, r, dweights=dw)[-n:].double().cpu()
+    ref, mag, spread = route_grad_ref(z[-n:], top, dw[-n:], 0.0)
+    within(d, ref, U["f16"] * ref.abs() + (24 + E / 32 + 4 * spread) * EPS * (1 + U["f16"]) * mag + 2.0 ** -24)
+
+
 def test_gradient_over_the_logits():
     z = _logits(333, 24, "bf16", 8)
     r = G.route(z, 3)

@@ -97,16 +97,22 @@ __device__ __forceinline__ float activate_one(float x) {
   }
 }
 
+// x within +-16, beyond which the derivatives of both GELUs are 1 or 0 (and where x^2 would
+// overflow far out); keeps NaN.
+__device__ __forceinline__ float clamp16(float x) {
+  float c;
+  asm("max.NaN.f32 %0, %1, 0fC1800000;" : "=f"(c) : "f"(x));
+  asm("min.NaN.f32 %0, %1, 0f41800000;" : "=f"(c) : "f"(c));
+  return c;
+}
+
 // Their derivatives.
 template <int ACT>
 __device__ __forceinline__ float activate_grad_one(float x) {
   if constexpr (ACT == ACT_RELU) {
     return x > 0.0f ? 1.0f : x <= 0.0f ? 0.0f : x;
   } else if constexpr (ACT == ACT_GELU_TANH) {
-    // Beyond +-16 it is 1 or 0; x^2 would overflow far out.
-    float c;
-    asm("max.NaN.f32 %0, %1, 0fC1800000;" : "=f"(c) : "f"(x));
-    asm("min.NaN.f32 %0, %1, 0f41800000;" : "=f"(c) : "f"(c));
+    const float c = clamp16(x);
     const float s = sigmoid_fast(TANH_A * c * fmaf(0.044715f * c, c, 1.0f));
     const float n = sigmoid_fast(-TANH_A * c * fmaf(0.044715f * c, c, 1.0f));   // 1 - s, without cancellation
     return fmaf(c * s * n, TANH_A * fmaf(0.134145f * c, c, 1.0f), s);
@@ -147,8 +153,9 @@ __device__ __forceinline__ void activate_grad(const float (&z)[N], float (&g)[N]
     if constexpr (ACT == ACT_GELU) {
       float p, q;
       uint64_t e;
-      normal_pair(z[i], z[i + 1], p, q, e);
-      const uint64_t d = fma_pair(mul_pair(pair_of(z[i], z[i + 1]), both(0.3989422804f)), e, pair_of(p, q));
+      const float a = clamp16(z[i]), b = clamp16(z[i + 1]);
+      normal_pair(a, b, p, q, e);
+      const uint64_t d = fma_pair(mul_pair(pair_of(a, b), both(0.3989422804f)), e, pair_of(p, q));
       split_pair(mul_pair(d, pair_of(g[i], g[i + 1])), g[i], g[i + 1]);
     } else {
       g[i] *= activate_grad_one<ACT>(z[i]);

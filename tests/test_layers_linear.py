@@ -159,6 +159,17 @@ def test_large_arguments(act):
         assert db.isfinite().all()
 
 
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_derivatives_at_infinity(act):
+    """A z that has overflowed to infinity has the slope 1 or 0; NaN stays NaN."""
+    pre = torch.zeros((3, 8), device="cuda").half()
+    pre[:, 1], pre[:, 2], pre[1, 5] = math.inf, -math.inf, math.nan
+    _, _, db = G.linear_grad(torch.ones_like(pre), torch.ones((3, 8), device="cuda").half(),
+                             torch.ones((8, 8), device="cuda").half(), activation=act, pre=pre)
+    at0 = 0.0 if act == "relu" else 0.5
+    assert db[1] == 3 and db[2] == 0 and db[5].isnan() and abs(float(db[0]) - 3 * at0) < 1e-5
+
+
 GRADS = [(1, 64, 16), (5, 200, 130), (64, 1024, 1000), (300, 512, 1368), (777, 130, 264), (129, 1000, 2999), (2000, 264, 200),
          (1030, 1100, 2050)]
 

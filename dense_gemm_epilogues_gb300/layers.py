@@ -409,7 +409,7 @@ class TensorList:
             n = t.numel()
             self.table[i] = gemm_tensor_t(t.data_ptr(), o.data_ptr(), n, _code(t.dtype), _code(o.dtype))
             if n:
-                spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(), i, self.out is None))
+                spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(), i, o is t))
                 if o is not t:
                     spans.append((o.data_ptr(), o.data_ptr() + n * o.element_size(), i, True))
         spans.sort()

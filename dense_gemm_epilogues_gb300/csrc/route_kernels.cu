@@ -20,6 +20,8 @@
 // Bound by latency and by the choice's instructions (400 per token and warp): the data are a few
 // megabytes.  16384 tokens, top 6 of 64: 15.3 us, of which the choice takes 9; its gradient 6.1 us;
 // 16 tokens, top 2 of 8: 3.8 us.
+#include <atomic>
+
 #include "layer.h"
 
 namespace gemmlib {
@@ -423,13 +425,8 @@ cudaError_t with_values(const RouteParams& p, F&& f) {
   return with_values<GEMM_BF16>(p.experts, f);
 }
 
-template <typename... P>
-cudaError_t launch_smem(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t stream,
-                        const RouteParams& p) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+cudaError_t launch_routing(void (*kernel)(const RouteParams), int grid, int threads, size_t smem, cudaStream_t stream,
+                           const RouteParams& p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
@@ -441,6 +438,31 @@ cudaError_t launch_smem(void (*kernel)(P...), int grid, int threads, size_t smem
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// Bytes of shared memory of route_choose_kernel.
+constexpr size_t choose_smem(int warps, size_t experts) { return (2 * (size_t)warps * experts + 3 * experts + 1) * sizeof(int); }
+
+// The limit of shared memory is the function's on its device, not the launch's: threads that route
+// over other numbers of experts at the same time share it, so it is set to the most that the
+// instantiation can need and never to less.
+template <int V, int DT>
+cudaError_t launch_choose(const RouteParams& p, cudaStream_t stream) {
+  constexpr int WARPS = warps_of(V);
+  constexpr size_t MOST = choose_smem(WARPS, 32 * V);
+  static_assert(MOST <= 232448, "shared memory budget");
+  if constexpr (MOST > 48 * 1024) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<bool> configured[64] = {};
+    if (dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+      e = cudaFuncSetAttribute(route_choose_kernel<V, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MOST);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) configured[dev].store(true, std::memory_order_release);
+    }
+  }
+  return launch_routing(route_choose_kernel<V, DT>, p.blocks, 32 * WARPS, choose_smem(WARPS, (size_t)p.experts), stream, p);
 }
 
 }  // namespace
@@ -456,19 +478,16 @@ int route_blocks(int64_t tokens, int64_t experts, int sm_count) {
 }
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
-  const size_t E = (size_t)p.experts;
-  const cudaError_t e = with_values(p, [&](auto v, auto dt) {
-    constexpr int V = decltype(v)::value, WARPS = warps_of(V);
-    return launch_smem(route_choose_kernel<V, decltype(dt)::value>, p.blocks, 32 * WARPS, (2 * WARPS * E + 3 * E + 1) * 4, stream, p);
-  });
+  const cudaError_t e = with_values(
+      p, [&](auto v, auto dt) { return launch_choose<decltype(v)::value, decltype(dt)::value>(p, stream); });
   if (e != cudaSuccess || p.blocks == 1) return e;
-  return launch_smem(route_place_kernel, p.blocks + 1, PLACE_THREADS, place_smem(p.experts), stream, p);
+  return launch_routing(route_place_kernel, p.blocks + 1, PLACE_THREADS, place_smem(p.experts), stream, p);
 }
 
 cudaError_t launch_route_grad(const RouteParams& p, int sm_count, cudaStream_t stream) {
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(4 * (int64_t)sm_count, (p.tokens + 15) / 16));
   return with_values(p, [&](auto v, auto dt) {
-    return launch_smem(route_grad_kernel<decltype(v)::value, decltype(dt)::value>, grid, 512, 0, stream, p);
+    return launch_routing(route_grad_kernel<decltype(v)::value, decltype(dt)::value>, grid, 512, 0, stream, p);
   });
 }
 

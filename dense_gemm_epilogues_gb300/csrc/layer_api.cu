@@ -394,7 +394,7 @@ gemm_status_t gemm_dispatch(gemm_plan_t plan, int64_t tokens, int64_t top, int64
   const gemm_status_t s = exchange_of(plan, tokens, top, rows, width, slots, &p);
   if (s != GEMM_OK) return s;
   if (rows == 0 || width == 0) return GEMM_OK;
-  if (!D || ldd < width || (tokens > 0 && (!X || ldx < width))) return GEMM_ERR_INVALID_ARG;
+  if (!D || ldd < width || (tokens > 0 && (!X || ldx < width || D == X))) return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
   const int es = dtype_bytes(plan->ab);
@@ -417,7 +417,8 @@ gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top, int64_
   const gemm_status_t s = exchange_of(plan, tokens, top, rows, width, slots, &p);
   if (s != GEMM_OK) return s;
   if (tokens == 0 || width == 0) return GEMM_OK;
-  if (!D || ldd < width || (rows > 0 && (!Y || ldy < width)) || (residual && ldr < width)) return GEMM_ERR_INVALID_ARG;
+  if (!D || ldd < width || (rows > 0 && (!Y || ldy < width || D == Y)) || (residual && ldr < width))
+    return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
   const int es = dtype_bytes(plan->ab);
@@ -446,7 +447,8 @@ gemm_status_t gemm_combine_grad(gemm_plan_t plan, int64_t tokens, int64_t top, i
   const gemm_status_t s = exchange_of(plan, tokens, top, rows, width, slots, &p);
   if (s != GEMM_OK) return s;
   if (tokens > 0 && (!dweights || (width > 0 && (!dout || ldo < width)))) return GEMM_ERR_INVALID_ARG;
-  if (rows > 0 && width > 0 && (!Y || ldy < width || !dY || lddy < width || dY == Y)) return GEMM_ERR_INVALID_ARG;
+  if (rows > 0 && width > 0 && (!Y || ldy < width || !dY || lddy < width || dY == Y || (tokens > 0 && dY == dout)))
+    return GEMM_ERR_INVALID_ARG;
   if (tokens == 0 && (rows == 0 || width == 0)) return GEMM_OK;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;

@@ -738,7 +738,8 @@ gemm_status_t gemm_route_grad(gemm_plan_t plan, int64_t tokens, int64_t experts,
  *   used        device: rows in use (offsets + experts of a routing); rows from there on are
  *               written as zeros by dispatch and combine_grad.  NULL: all are in use; a row
  *               that no slot names is then left as it is.
- * D must not overlap the inputs, but combine's D may be its residual.
+ * D and dY must not overlap the inputs (the same address is GEMM_ERR_INVALID_ARG), but
+ * combine's D may be its residual.
  * ------------------------------------------------------------------------- */
 gemm_status_t gemm_dispatch(gemm_plan_t plan, int64_t tokens, int64_t top, int64_t rows, int64_t width, const void* X,
                             int64_t ldx, const int32_t* slots, const int32_t* used, void* D, int64_t ldd,

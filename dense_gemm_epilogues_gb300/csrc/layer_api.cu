@@ -221,7 +221,9 @@ gemm_status_t gemm_run_linear(gemm_plan_t plan, gemm_layout_t lb, int64_t M, int
   if (M == 0 || N == 0) return nothing(plan);
   if (!D || ldd < N) return GEMM_ERR_INVALID_ARG;
   if (epi && ((epi->residual && epi->ld_residual < N) || (epi->pre && epi->ld_pre < N))) return GEMM_ERR_INVALID_ARG;
-  if (K > 0 && (!A || !B || lda < K || ldb < (lb == GEMM_OP_N ? K : N))) return GEMM_ERR_INVALID_ARG;
+  if (K > 0 && (!A || !B || lda < K || ldb < (lb == GEMM_OP_N ? K : N) || D == A || D == B)) return GEMM_ERR_INVALID_ARG;
+  if (epi && epi->pre && (epi->pre == D || epi->pre == epi->residual || (K > 0 && (epi->pre == A || epi->pre == B))))
+    return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
@@ -272,6 +274,9 @@ gemm_status_t gemm_run_linear_grad(gemm_plan_t plan, gemm_layout_t lb, int64_t M
   if (dB && (lddb < wld || (M > 0 && K > 0 && (!A || lda < K)))) return GEMM_ERR_INVALID_ARG;
   const bool want_a = dA && M > 0 && K > 0, want_b = dB && N > 0 && K > 0, want_bias = dbias && N > 0;
   if (!want_a && !want_b && !want_bias) return nothing(plan);
+  auto is_input = [&](const void* p) { return p == dY || p == A || p == B || (act != GEMM_LINEAR_NONE && p == pre); };
+  if (M > 0 && N > 0 && ((want_a && is_input(dA)) || (want_b && is_input(dB)) || (want_bias && is_input(dbias))))
+    return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);

@@ -42,3 +42,44 @@ def test_rows_of_nothing():
     r = G.route(torch.zeros((4, 8), device="cuda"), 1)
     e = torch.empty((4, 0), device="cuda")
     assert G.dispatch(e, r, out=e) is e and G.combine(e, r, out=e) is e and G.combine_grad(e, e, r, out=e)[0] is e
+
+
+@pytest.mark.parametrize("M", [8, 600])
+def test_layers_in_place(M):
+    gen = torch.Generator("cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(s, device="cuda", generator=gen).bfloat16()   # noqa: E731
+    x, w, res = rand(M, 128), rand(128, 128), rand(M, 128)
+    kept = [t.clone() for t in (x, w, res)]
+    _refused(lambda: G.linear(x, w, out=x))
+    _refused(lambda: G.linear(x, w, residual=res, out=x))
+    _refused(lambda: G.linear(rand(128, 128), w, out=w))
+    plan, lib = G.Plan(G.GEMM_BF16, G.GEMM_F32), G.load_library()
+    D = torch.empty_like(res)
+    for pre in (x, w, res, D):
+        e = G.gemm_linear_t(None, G.GEMM_F32, G.GEMM_LINEAR_GELU, res.data_ptr(), 128, pre.data_ptr(), 128, G.GEMM_BF16)
+        assert lib.gemm_run_linear(plan.handle, G.GEMM_OP_T, M, 128, 128, x.data_ptr(), 128, w.data_ptr(), 128,
+                                   D.data_ptr(), 128, e, None) == G.GEMM_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((x, w, res), kept))
+    want = G.linear(x, w, activation="gelu", residual=res)
+    assert torch.equal(G.linear(x, w, activation="gelu", residual=res, out=res), want)
+
+
+@pytest.mark.parametrize("act", [G.GEMM_LINEAR_NONE, G.GEMM_LINEAR_SILU])
+def test_gradients_in_place(act):
+    gen = torch.Generator("cuda").manual_seed(1)
+    dy, pre, x, w, dx, dw = (torch.randn((128, 128), device="cuda", generator=gen).bfloat16() for _ in range(6))
+    db = torch.empty(128, device="cuda")
+    plan, lib = G.Plan(G.GEMM_BF16, G.GEMM_F32), G.load_library()
+
+    def status(dx=dx, dw=dw, db=db):
+        return lib.gemm_run_linear_grad(plan.handle, G.GEMM_OP_T, 128, 128, 128, dy.data_ptr(), 128, pre.data_ptr(), 128, act,
+                                        x.data_ptr(), 128, w.data_ptr(), 128, dx.data_ptr(), 128, dw.data_ptr(), 128,
+                                        G.GEMM_BF16, db.data_ptr(), torch.cuda.current_stream().cuda_stream)
+
+    for t in (dy, x, w) + ((pre,) if act else ()):
+        for name in ("dx", "dw", "db"):
+            assert status(**{name: t}) == G.GEMM_ERR_INVALID_ARG
+    assert status() == G.GEMM_OK
+    if not act:   # (not read without an activation: its memory may be used)
+        assert status(dx=pre) == G.GEMM_OK and torch.equal(pre, dx)

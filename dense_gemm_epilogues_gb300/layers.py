@@ -392,7 +392,8 @@ class TensorList:
     """Tensors whose global norm is taken and that are scaled together, laid out once: the
     gradients that a program keeps from step to step (a tensor that has other memory by the time
     of a call is refused).  out: where the scaled values go, tensors of the same shapes and
-    strides and any of the types (None: in place)."""
+    strides and any of the types, or None for one that only counts (out=None: all in place).
+    What is written may not share memory with any other entry."""
 
     def __init__(self, tensors, out=None):
         self.tensors, self.out = list(tensors), list(out) if out is not None else None
@@ -404,13 +405,14 @@ class TensorList:
         for i, (t, o) in enumerate(zip(self.tensors, to)):
             if not _fills(t):
                 raise ValueError("tensors must fill their memory (no gaps between their entries)")
-            if o is not t and (o.shape != t.shape or o.stride() != t.stride()):
+            if o is not None and o is not t and (o.shape != t.shape or o.stride() != t.stride()):
                 raise ValueError("out must have the tensors' shapes and strides")
-            n = t.numel()
-            self.table[i] = gemm_tensor_t(t.data_ptr(), o.data_ptr(), n, _code(t.dtype), _code(o.dtype))
+            n, code = t.numel(), _code(t.dtype)
+            self.table[i] = gemm_tensor_t(t.data_ptr(), o.data_ptr() if o is not None else None, n, code,
+                                          _code(o.dtype) if o is not None else code)
             if n:
                 spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(), i, o is t))
-                if o is not t:
+                if o is not None and o is not t:
                     spans.append((o.data_ptr(), o.data_ptr() + n * o.element_size(), i, True))
         spans.sort()
         end, written_end = 0, 0   # of all spans so far, and of those that are written
@@ -420,8 +422,15 @@ class TensorList:
             end = max(end, hi)
             written_end = max(written_end, hi) if written else written_end
         self.device = _device(*self.tensors, *(self.out or ())) if self.tensors else None
-        self._all = self.tensors + (self.out or [])
+        self._all = self.tensors + [o for o in self.out or () if o is not None]
         self._at = list(map(torch.Tensor.data_ptr, self._all))
+        self._read = None
+
+    def read_table(self):
+        """The table without places to write to, laid out once too."""
+        if self._read is None:
+            self._read = type(self.table)(*(gemm_tensor_t(e.src, None, e.count, e.src_type, e.src_type) for e in self.table))
+        return self._read
 
     def check(self):
         if list(map(torch.Tensor.data_ptr, self._all)) != self._at:
@@ -432,7 +441,8 @@ def _norm_of(tensors, max_norm: float, eps: float, scales: bool, plan, stream):
     if isinstance(tensors, TensorList):
         tensors.check()
     else:
-        tensors = TensorList(tensors)
+        tensors = list(tensors)
+        tensors = TensorList(tensors, None if scales else [None] * len(tensors))
     if not max_norm >= 0 or not 0 <= eps < math.inf:
         raise ValueError("max_norm and eps must not be negative, and eps finite")
     device = tensors.device
@@ -446,11 +456,8 @@ def _norm_of(tensors, max_norm: float, eps: float, scales: bool, plan, stream):
         plan = _plan_for(None, GEMM_F32, GEMM_F32, device, stream)
     elif plan.device != device:
         raise ValueError("the plan is on another device")
-    table, n = tensors.table, len(tensors.tensors)
-    if not scales:
-        table = (gemm_tensor_t * max(1, n))(*[gemm_tensor_t(e.src, None, e.count, e.src_type, e.src_type)
-                                              for e in table[:n]])
-    status = _LIB.gemm_clip_norm(plan.handle, n, table, max_norm, eps, norm.data_ptr(), stream)
+    table = tensors.table if scales else tensors.read_table()
+    status = _LIB.gemm_clip_norm(plan.handle, len(tensors.tensors), table, max_norm, eps, norm.data_ptr(), stream)
     if status:
         raise GemmError(status, "gemm_clip_norm")
     return norm
@@ -468,5 +475,6 @@ def clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, plan: Optiona
 
 
 def grad_norm(tensors, *, plan: Optional[Plan] = None, stream=None):
-    """The global norm of a list of tensors or a TensorList, a float32 scalar on the device."""
+    """The global norm of a list of tensors or a TensorList, a float32 scalar on the device.  The
+    tensors are only read: a list may name the same memory twice, and counts it as often."""
     return _norm_of(tensors, math.inf, 0.0, False, plan, stream)

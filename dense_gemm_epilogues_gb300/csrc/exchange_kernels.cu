@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(THREADS) combine_grad_kernel(const __grid_cons
 enum { DISPATCH, COMBINE, COMBINE_GRAD };
 
 template <int WHAT, int DT, bool WIDE>
-cudaError_t launch_as(ExchangeParams p, int sm_count, cudaStream_t stream) {
+cudaError_t launch_as(ExchangeParams p, int sm_count, cudaStream_t stream, int* ctas) {
   // Warps of a token: as many as leave each lane two turns of its loads (four pieces of dispatch,
   // eight of combine_grad), so that a row's bytes are asked for closer together; more,
   // down to one piece per lane, while the chip has less than 16 warps per SM.  At most eight.
@@ -299,6 +299,7 @@ cudaError_t launch_as(ExchangeParams p, int sm_count, cudaStream_t stream) {
     ++p.parts_shift;
   const int64_t work = ((p.tokens << p.parts_shift) + WARPS - 1) / WARPS;
   const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(work, 16 * (int64_t)sm_count)));
+  *ctas = (int)grid.x;
   if constexpr (WHAT == DISPATCH) return launch_dependent(dispatch_kernel<DT, WIDE>, grid, THREADS, stream, p);
   else if constexpr (WHAT == COMBINE) return p.top <= 2 ? launch_dependent(combine_kernel<DT, WIDE, 2>, grid, THREADS, stream, p)
                                       : p.top <= 4 ? launch_dependent(combine_kernel<DT, WIDE, 4>, grid, THREADS, stream, p)
@@ -307,24 +308,27 @@ cudaError_t launch_as(ExchangeParams p, int sm_count, cudaStream_t stream) {
 }
 
 template <int WHAT>
-cudaError_t launch_any(const ExchangeParams& p, int sm_count, cudaStream_t stream) {
+cudaError_t launch_any(const ExchangeParams& p, int sm_count, cudaStream_t stream, int* grid) {
   if (p.dtype == GEMM_F32)
-    return p.vec ? launch_as<WHAT, GEMM_F32, true>(p, sm_count, stream) : launch_as<WHAT, GEMM_F32, false>(p, sm_count, stream);
+    return p.vec ? launch_as<WHAT, GEMM_F32, true>(p, sm_count, stream, grid)
+                 : launch_as<WHAT, GEMM_F32, false>(p, sm_count, stream, grid);
   if (p.dtype == GEMM_F16)
-    return p.vec ? launch_as<WHAT, GEMM_F16, true>(p, sm_count, stream) : launch_as<WHAT, GEMM_F16, false>(p, sm_count, stream);
-  return p.vec ? launch_as<WHAT, GEMM_BF16, true>(p, sm_count, stream) : launch_as<WHAT, GEMM_BF16, false>(p, sm_count, stream);
+    return p.vec ? launch_as<WHAT, GEMM_F16, true>(p, sm_count, stream, grid)
+                 : launch_as<WHAT, GEMM_F16, false>(p, sm_count, stream, grid);
+  return p.vec ? launch_as<WHAT, GEMM_BF16, true>(p, sm_count, stream, grid)
+               : launch_as<WHAT, GEMM_BF16, false>(p, sm_count, stream, grid);
 }
 
 }  // namespace
 
-cudaError_t launch_dispatch(const ExchangeParams& p, int sm_count, cudaStream_t stream) {
-  return launch_any<DISPATCH>(p, sm_count, stream);
+cudaError_t launch_dispatch(const ExchangeParams& p, int sm_count, cudaStream_t stream, int* grid) {
+  return launch_any<DISPATCH>(p, sm_count, stream, grid);
 }
-cudaError_t launch_combine(const ExchangeParams& p, int sm_count, cudaStream_t stream) {
-  return launch_any<COMBINE>(p, sm_count, stream);
+cudaError_t launch_combine(const ExchangeParams& p, int sm_count, cudaStream_t stream, int* grid) {
+  return launch_any<COMBINE>(p, sm_count, stream, grid);
 }
-cudaError_t launch_combine_grad(const ExchangeParams& p, int sm_count, cudaStream_t stream) {
-  return launch_any<COMBINE_GRAD>(p, sm_count, stream);
+cudaError_t launch_combine_grad(const ExchangeParams& p, int sm_count, cudaStream_t stream, int* grid) {
+  return launch_any<COMBINE_GRAD>(p, sm_count, stream, grid);
 }
 
 }  // namespace gemmlib

@@ -70,7 +70,7 @@ __host__ __device__ inline int route_pitch(int experts) { return (experts + 4) /
 int route_blocks(int64_t tokens, int64_t experts, int sm_count);   // RouteParams::blocks
 int route_warps(int64_t experts);                                  // RouteParams::warps
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);
-cudaError_t launch_route_grad(const RouteParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_route_grad(const RouteParams& p, int sm_count, cudaStream_t stream, int* grid);   // grid: CTAs launched
 
 // ---- rows between tokens and experts (exchange_kernels.cu) ----
 struct ExchangeParams {
@@ -87,9 +87,10 @@ struct ExchangeParams {
   int32_t parts_shift;       // log2 of the warps that share a token (set by the launch)
   int32_t* err;
 };
-cudaError_t launch_dispatch(const ExchangeParams& p, int sm_count, cudaStream_t stream);
-cudaError_t launch_combine(const ExchangeParams& p, int sm_count, cudaStream_t stream);
-cudaError_t launch_combine_grad(const ExchangeParams& p, int sm_count, cudaStream_t stream);
+// grid: CTAs launched.
+cudaError_t launch_dispatch(const ExchangeParams& p, int sm_count, cudaStream_t stream, int* grid);
+cudaError_t launch_combine(const ExchangeParams& p, int sm_count, cudaStream_t stream, int* grid);
+cudaError_t launch_combine_grad(const ExchangeParams& p, int sm_count, cudaStream_t stream, int* grid);
 
 // ---- global norm and clipping (clip_kernels.cu) ----
 // A part of the list of tensors, as one launch takes it (by value: a captured launch keeps

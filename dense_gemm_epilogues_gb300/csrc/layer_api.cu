@@ -15,6 +15,19 @@ bool is_type(int t) { return t == GEMM_F32 || t == GEMM_F16 || t == GEMM_BF16; }
 // Rows that can be read and written 16 bytes at a time.
 bool wide_rows(const void* p, int64_t ld, int es) { return aligned16(p) && (ld * es) % 16 == 0; }
 
+// What gemm_plan_last_config reports of a call without a product, and its log line.
+gemm_status_t launched(gemm_plan* plan, cudaError_t e, const char* entry, int64_t M, int64_t N, int64_t K, int64_t batch,
+                       int grid) {
+  if (e != cudaSuccess) return GEMM_ERR_CUDA;
+  gemm_config_t c{};
+  c.kernel = GEMM_KERNEL_SIMT;
+  c.cta_group = c.cluster = c.split_k = 1;
+  c.grid = grid;
+  plan->last = c;
+  log_config(entry, M, N, K, batch, c);
+  return GEMM_OK;
+}
+
 gemm_status_t check_routing(const gemm_plan* plan, int64_t tokens, int64_t experts, const void* logits, int64_t ld,
                             const gemm_routing_t* r) {
   if (!is_type(plan->ab)) return GEMM_ERR_UNSUPPORTED;
@@ -325,6 +338,8 @@ gemm_status_t gemm_run_linear_grad(gemm_plan_t plan, gemm_layout_t lb, int64_t M
   if (s == GEMM_OK && xb > 0) s = repitch(&x, M, K, 1, nullptr, ws + zb, stream);
   if (s == GEMM_OK && wb > 0) s = repitch(&w, wrows, wcols, 1, nullptr, ws + zb + xb, stream);
   if (s != GEMM_OK) return s;
+  if (!want_a && !want_b)   // (the products report themselves)
+    return launched(plan, cudaSuccess, "linear_grad", M, N, K, 1, (int)strips * std::max(1, blocks));
   if (want_a) {   // dA = dz W': W' is N x K, N contiguous where W's K is
     s = linear_product(plan, M, K, N, dy, w, !w_mn, plain_epilogue(dA, ldda, plan->ab), LinearEpilogue{}, "linear_grad",
                        stream);
@@ -366,7 +381,7 @@ gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, cons
     p.hist = static_cast<int32_t*>(plan->ws.p);
     p.mass = reinterpret_cast<float*>(static_cast<char*>(plan->ws.p) + hist);
   }
-  return launch_route(p, stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  return launched(plan, launch_route(p, stream), "route", tokens, experts, p.top, 1, p.blocks);
 }
 
 gemm_status_t gemm_route_grad(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ld,
@@ -376,7 +391,7 @@ gemm_status_t gemm_route_grad(gemm_plan_t plan, int64_t tokens, int64_t experts,
   NvtxRange range("gemm_route_grad");
   gemm_status_t s = check_routing(plan, tokens, experts, logits, ld, routing);
   if (s != GEMM_OK) return s;
-  if (tokens == 0) return GEMM_OK;
+  if (tokens == 0) return nothing(plan);
   if (!dlogits || ldd < experts) return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
@@ -386,8 +401,9 @@ gemm_status_t gemm_route_grad(gemm_plan_t plan, int64_t tokens, int64_t experts,
   p.dloss_scale = (float)dloss_scale;
   p.dlogits = dlogits;
   p.ldd = ldd;
-  return launch_route_grad(p, plan->sm_count, reinterpret_cast<cudaStream_t>(stream_)) == cudaSuccess ? GEMM_OK
-                                                                                                     : GEMM_ERR_CUDA;
+  int grid = 0;
+  const cudaError_t e = launch_route_grad(p, plan->sm_count, reinterpret_cast<cudaStream_t>(stream_), &grid);
+  return launched(plan, e, "route_grad", tokens, experts, p.top, 1, grid);
 }
 
 gemm_status_t gemm_dispatch(gemm_plan_t plan, int64_t tokens, int64_t top, int64_t rows, int64_t width, const void* X,
@@ -398,7 +414,7 @@ gemm_status_t gemm_dispatch(gemm_plan_t plan, int64_t tokens, int64_t top, int64
   ExchangeParams p;
   const gemm_status_t s = exchange_of(plan, tokens, top, rows, width, slots, &p);
   if (s != GEMM_OK) return s;
-  if (rows == 0 || width == 0) return GEMM_OK;
+  if (rows == 0 || width == 0) return nothing(plan);
   if (!D || ldd < width || (tokens > 0 && (!X || ldx < width || D == X))) return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
@@ -409,8 +425,9 @@ gemm_status_t gemm_dispatch(gemm_plan_t plan, int64_t tokens, int64_t top, int64
   p.out = D;
   p.ldo = ldd;
   p.vec = (width * es) % 16 == 0 && wide_rows(X, ldx, es) && wide_rows(D, ldd, es) ? 1 : 0;
-  return launch_dispatch(p, plan->sm_count, reinterpret_cast<cudaStream_t>(stream_)) == cudaSuccess ? GEMM_OK
-                                                                                                   : GEMM_ERR_CUDA;
+  int grid = 0;
+  const cudaError_t e = launch_dispatch(p, plan->sm_count, reinterpret_cast<cudaStream_t>(stream_), &grid);
+  return launched(plan, e, "dispatch", tokens, width, top, 1, grid);
 }
 
 gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top, int64_t rows, int64_t width, const void* Y,
@@ -421,7 +438,7 @@ gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top, int64_
   ExchangeParams p;
   const gemm_status_t s = exchange_of(plan, tokens, top, rows, width, slots, &p);
   if (s != GEMM_OK) return s;
-  if (tokens == 0 || width == 0) return GEMM_OK;
+  if (tokens == 0 || width == 0) return nothing(plan);
   if (!D || ldd < width || (rows > 0 && (!Y || ldy < width || D == Y)) || (residual && ldr < width))
     return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(plan->device);
@@ -438,8 +455,9 @@ gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top, int64_
                   (!residual || wide_rows(residual, ldr, es))
               ? 1
               : 0;
-  return launch_combine(p, plan->sm_count, reinterpret_cast<cudaStream_t>(stream_)) == cudaSuccess ? GEMM_OK
-                                                                                                  : GEMM_ERR_CUDA;
+  int grid = 0;
+  const cudaError_t e = launch_combine(p, plan->sm_count, reinterpret_cast<cudaStream_t>(stream_), &grid);
+  return launched(plan, e, "combine", tokens, width, top, 1, grid);
 }
 
 gemm_status_t gemm_combine_grad(gemm_plan_t plan, int64_t tokens, int64_t top, int64_t rows, int64_t width,
@@ -454,7 +472,7 @@ gemm_status_t gemm_combine_grad(gemm_plan_t plan, int64_t tokens, int64_t top, i
   if (tokens > 0 && (!dweights || (width > 0 && (!dout || ldo < width)))) return GEMM_ERR_INVALID_ARG;
   if (rows > 0 && width > 0 && (!Y || ldy < width || !dY || lddy < width || dY == Y || (tokens > 0 && dY == dout)))
     return GEMM_ERR_INVALID_ARG;
-  if (tokens == 0 && (rows == 0 || width == 0)) return GEMM_OK;
+  if (tokens == 0 && (rows == 0 || width == 0)) return nothing(plan);
   DeviceGuard g(plan->device);
   if (!g.ok) return GEMM_ERR_CUDA;
   const int es = dtype_bytes(plan->ab);
@@ -468,9 +486,9 @@ gemm_status_t gemm_combine_grad(gemm_plan_t plan, int64_t tokens, int64_t top, i
   p.ldo = lddy;
   p.dweights = dweights;
   p.vec = (width * es) % 16 == 0 && wide_rows(dout, ldo, es) && wide_rows(Y, ldy, es) && wide_rows(dY, lddy, es) ? 1 : 0;
-  return launch_combine_grad(p, plan->sm_count, reinterpret_cast<cudaStream_t>(stream_)) == cudaSuccess
-             ? GEMM_OK
-             : GEMM_ERR_CUDA;
+  int grid = 0;
+  const cudaError_t e = launch_combine_grad(p, plan->sm_count, reinterpret_cast<cudaStream_t>(stream_), &grid);
+  return launched(plan, e, "combine_grad", tokens, width, top, 1, grid);
 }
 
 gemm_status_t gemm_clip_norm(gemm_plan_t plan, int64_t count, const gemm_tensor_t* tensors, double max_norm, double eps,
@@ -528,7 +546,7 @@ gemm_status_t gemm_clip_norm(gemm_plan_t plan, int64_t count, const gemm_tensor_
         cudaSuccess)
       return GEMM_ERR_CUDA;
   }
-  return GEMM_OK;
+  return launched(plan, cudaSuccess, "clip_norm", total, 1, 1, count, p.num_partials);
 }
 
 }  // extern "C"

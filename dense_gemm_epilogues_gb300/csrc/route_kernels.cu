@@ -484,8 +484,9 @@ cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
   return launch_routing(route_place_kernel, p.blocks + 1, PLACE_THREADS, place_smem(p.experts), stream, p);
 }
 
-cudaError_t launch_route_grad(const RouteParams& p, int sm_count, cudaStream_t stream) {
+cudaError_t launch_route_grad(const RouteParams& p, int sm_count, cudaStream_t stream, int* ctas) {
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(4 * (int64_t)sm_count, (p.tokens + 15) / 16));
+  *ctas = grid;
   return with_values(p, [&](auto v, auto dt) {
     return launch_routing(route_grad_kernel<decltype(v)::value, decltype(dt)::value>, grid, 512, 0, stream, p);
   });

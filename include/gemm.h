@@ -618,6 +618,10 @@ gemm_status_t gemm_orthogonalize(gemm_plan_t plan, int64_t batch, int64_t M, int
  * language models need beside the products.  They use
  * the plan's device, error word and scratch as the others do and are asynchronous
  * on `stream`.  No atomics decide an order: equal inputs give equal bits.
+ * gemm_plan_last_config describes a layer's product as it does the expert layers'
+ * (gemm_run_linear with few tiles: bk 64, bn rows of a tile, split_k CTAs that share its
+ * K; gemm_run_linear_grad: its last product), and of a call without a product
+ * GEMM_KERNEL_SIMT with the CTAs of its first pass.
  * ======================================================================== */
 
 /* Activations of a fully connected layer.  GELU is x P(x) with the normal distribution P,

@@ -52,8 +52,31 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// A limit below a microsecond, the step of the timer and less than the hardware may suspend a
+// try for, gives a wait one look: these loads mostly land within a single try, which no limit
+// would ever end.
+constexpr uint64_t ONE_LOOK_NS = 1000;
+
+__device__ __forceinline__ bool mbar_look(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (ok != 0) return true;
+  atomicCAS(wc.err, 0, (int32_t)GEMM_ERR_TIMEOUT);
+  *wc.abort = 1;
+  __threadfence_block();
+  return false;
+}
+
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
-  const bool ok = mbar_wait(bar, parity, wc);
+  const bool ok = wc.timeout_ns >= ONE_LOOK_NS ? mbar_wait(bar, parity, wc) : mbar_look(bar, parity, wc);
   return __all_sync(0xffffffffu, ok) != 0;
 }
 

@@ -693,16 +693,15 @@ __global__ void __launch_bounds__(SegThreads<MODE>::COUNT, 1) seg_kernel(const _
     int stage = 0, issued = 0;   // stages filled so far
     uint32_t phase = 0;
     bool ok = true;
-    // WGRAD: a group's tensor maps are acquired and fetched a tile ahead of their use.
+    // WGRAD: a group's tensor maps are acquired a tile ahead of their use.  They lie in global
+    // memory, so they are not fetched ahead: prefetch.tensormap is for maps in constant or
+    // parameter memory.
     int map_of = -1;
     auto acquire_maps = [&](const Tile& a) {
       if (a.k == 0 || a.e == map_of) return;
       map_of = a.e;
       if (one) {
-        for (int i = 0; i < 2; ++i) {
-          tensormap_acquire(p.group_maps + 2 * a.e + i);
-          tma_prefetch_desc(p.group_maps + 2 * a.e + i);
-        }
+        for (int i = 0; i < 2; ++i) tensormap_acquire(p.group_maps + 2 * a.e + i);
       }
       __syncwarp();
     };
@@ -1151,9 +1150,10 @@ __global__ void __launch_bounds__(32) wgrad_maps_kernel(const __grid_constant__ 
     const uint64_t addr = which ? p.b_base + (uint64_t)lo * p.b_pitch : p.a_base + (uint64_t)lo * p.a_pitch;
     asm volatile("tensormap.replace.tile.global_address.global.b1024.b64 [%0], %1;" ::"l"(out), "l"(addr) : "memory");
     asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(out), "r"(hi - lo) : "memory");
-    asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
-    __threadfence();
   }
+  // Every lane releases what it has written.
+  asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+  __threadfence();
 }
 
 template <int CG, bool A_MN, bool B_MN, int MODE>

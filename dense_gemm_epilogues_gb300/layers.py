@@ -337,7 +337,9 @@ def combine(y, routing: Routing, *, residual=None, out=None, plan: Optional[Plan
     """The experts' rows back to their tokens (gemm_combine):
     out[t] = residual[t] + sum_j weights[t, j] * y[slots[t, j]], [tokens, width] of y's type.
 
-    y: [rows, width] sorted rows; residual: [tokens, width] of y's type (it may be `out`)."""
+    y: [rows, width] sorted rows; residual: [tokens, width] of y's type (it may be `out`).  Sums
+    are fp32; for a result or a residual of fp32 beside 16-bit experts y goes in as fp32 (y.float(),
+    or the product's out_dtype)."""
     return _combine(y, routing, routing.weights, residual, out, plan, stream)
 
 

@@ -67,6 +67,16 @@ def serve_q4(x, offsets, packed, b1, group, plan):
     return G.q4_matmul(h, q2, s2, group, zeros=z2, offsets=offsets, plan=plan)
 
 
+def added(y, r, plan):
+    """The experts' 16-bit rows back to their tokens, added up and kept in fp32."""
+    return G.combine(y.float(), r, plan=plan)
+
+
+def row_gradients(dout, y, r, plan):
+    """Gradient of `added`'s rows for its fp32 output's, rounded once to their type."""
+    return G.combine_grad(dout, y.float(), r, plan=plan)[0].to(y.dtype)
+
+
 def main(experts=8, d=256, h=512, tokens=1024, steps=60, rate=0.02, group=64, seed=0, verbose=True):
     gen = torch.Generator("cuda").manual_seed(seed)
     router = torch.randn((d, experts), generator=gen, device="cuda") * d ** -0.5
@@ -76,11 +86,11 @@ def main(experts=8, d=256, h=512, tokens=1024, steps=60, rate=0.02, group=64, se
         x = torch.randn((tokens, d), generator=gen, device="cuda").bfloat16()
         r = G.route(x.float() @ router, TOP, plan=student.plan32)
         rows = G.dispatch(x, r, plan=student.plan)
-        target = G.combine(teacher.forward(rows, r.offsets)[0], r, plan=teacher.plan)
+        target = added(teacher.forward(rows, r.offsets)[0], r, teacher.plan32)
         y, hidden = student.forward(rows, r.offsets)
-        error = G.combine(y, r, plan=student.plan).float() - target
+        error = added(y, r, student.plan32) - target
         losses.append(float(error.square().mean()))
-        dy, _ = G.combine_grad((error * (2.0 / error.numel())).bfloat16(), y, r, plan=student.plan)
+        dy = row_gradients(error * (2.0 / error.numel()), y, r, student.plan32)
         student.update(student.backward(rows, hidden, dy, r.offsets), rate * (1 - step / steps))
         if verbose and step % 10 == 0:
             print(f"step {step:3d}  loss {losses[-1]:.4f}  balance {float(r.loss):.3f}")
@@ -91,8 +101,8 @@ def main(experts=8, d=256, h=512, tokens=1024, steps=60, rate=0.02, group=64, se
         x = torch.randn((1, d), generator=gen, device="cuda").bfloat16()
         r = G.route(x.float() @ router, TOP, plan=student.plan32)
         rows = G.dispatch(x, r, plan=student.plan)
-        full = G.combine(student.forward(rows, r.offsets)[0], r, plan=student.plan).float()
-        low = G.combine(serve_q4(rows, r.offsets, packed, student.b1, group, student.plan), r, plan=student.plan).float()
+        full = added(student.forward(rows, r.offsets)[0], r, student.plan32)
+        low = added(serve_q4(rows, r.offsets, packed, student.b1, group, student.plan), r, student.plan32)
         worst = max(worst, float((low - full).norm() / full.norm()))
     if verbose:
         print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f}; 4-bit weights change an output by {100 * worst:.1f} % at most")

@@ -4,8 +4,9 @@
 //     combine_grad  out[slot(t, j)] = w(t, j) x[t],  dweights(t, j) = <x[t], y[slot(t, j)]>
 // (dispatch's own gradient is combine without weights and residual.)  All three go by
 // tokens: a token's row is read or written once and its `top` sorted rows lie anywhere, each
-// a long run of bytes; so every byte moves once, no atomics decide an order, and the sums
-// over a token's rows and over a row's entries have one order.
+// a long run of bytes; so memory moves every byte once (combine_grad reads a token's row again
+// from the caches for every four choices beyond the first four), no atomics decide an order, and
+// the sums over a token's rows and over a row's entries have one order.
 //
 // Bound by memory.  A warp takes a token -- of few tokens with long rows, a part of one, up to
 // eight warps of a CTA together -- with its slots and weights in its lanes, and goes along the

@@ -1,5 +1,6 @@
-// layer.h -- launch interface of the kernels around the products: routing, the exchange
-// of rows between tokens and experts, clipping by a global norm (internal).
+// layer.h -- launch interface of the kernels around the products: fully connected layers of few
+// tiles and the elementwise pass of their gradient, routing, the exchange of rows between tokens
+// and experts, clipping by a global norm (internal).
 #pragma once
 
 #include "expert.h"

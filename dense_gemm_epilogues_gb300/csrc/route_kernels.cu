@@ -17,6 +17,10 @@
 // launch places: every CTA adds the counts of the CTAs before it (B x E integers, from L2) to
 // its tokens' numbers, and one more CTA adds up the loss.  Nothing waits for another CTA and no atomics decide an order,
 // so a routing is the same bits every time.  A batch that one CTA takes whole is one launch.
+// Exponentials and quotients are the hardware's (2 steps of fp32, and |x| 2^-24 of an argument):
+// every lane takes several per token, and beside fp32 sums over the experts they change little
+// (weights and loss against 64 bits 3.4e-8 and 6.0e-8 of their norm in two cases, 3.3e-8 and 5.3e-8
+// with accurate ones).
 // Bound by latency and by the choice's instructions (400 per token and warp): the data are a few
 // megabytes.  16384 tokens, top 6 of 64: 15.3 us, of which the choice takes 9; its gradient 6.1 us;
 // 16 tokens, top 2 of 8: 3.8 us.

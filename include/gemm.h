@@ -394,7 +394,8 @@ gemm_status_t gemm_plan_device_status(gemm_plan_t plan, gemm_stream_t stream, in
 /* Set the bound of every in-kernel wait, in nanoseconds (default 4e9).  A wait
  * that runs past it records GEMM_ERR_TIMEOUT in the error word and its CTA
  * winds down (waiting, again bounded, for its own copies in flight and
- * releasing its tensor memory) instead of spinning for ever. */
+ * releasing its tensor memory) instead of spinning for ever.  The hardware may
+ * suspend a try for longer than a short bound. */
 gemm_status_t gemm_plan_set_timeout(gemm_plan_t plan, uint64_t timeout_ns);
 
 /* Human-readable name of a status code (static storage; never NULL). */
@@ -672,8 +673,8 @@ gemm_status_t gemm_run_linear(gemm_plan_t plan, gemm_layout_t layoutB, int64_t M
  *   dA          row-major M x K of the plan's ab_dtype, or NULL: not wanted (B is not read).
  *   dB          K x N in layoutB (B's own), of db_dtype F32, F16 or BF16, or NULL (A is not read).
  *   dbias       N fp32 entries, or NULL.
- * dZ is rounded to the operands' type for the two products, as the tensor cores take it, and
- * summed unrounded, in fp32, for dbias.  It takes M x N entries of the plan's scratch (none
+ * dZ is rounded to the operands' type for the two products, as the tensor cores take it (half a
+ * step of every term), and summed unrounded, in fp32, for dbias.  It takes M x N entries of the plan's scratch (none
  * without an activation).  M == 0 gives zeros.  The outputs must not overlap the inputs (the
  * same address is GEMM_ERR_INVALID_ARG).
  * ------------------------------------------------------------------------- */
@@ -710,7 +711,7 @@ typedef struct {
  *     which is 1 for an even routing; the sum runs over the tokens that have any expert.
  *   mask        tokens bytes, 0: the token gets no expert and counts nowhere; NULL: all do.
  *   experts     1 .. 1024, tokens * top < 2^31 (else GEMM_ERR_UNSUPPORTED).
- * Softmax and sums are fp32.
+ * Softmax and sums are fp32, exponentials and quotients by two fp32 steps each.
  * ------------------------------------------------------------------------- */
 gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ld,
                          const uint8_t* mask, const gemm_routing_t* routing, gemm_stream_t stream);

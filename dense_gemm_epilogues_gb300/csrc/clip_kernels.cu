@@ -88,14 +88,8 @@ struct Unit {
   __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-      if constexpr (DT == GEMM_F32) {
-        x[2 * h] = __uint_as_float(w[2 * h]), x[2 * h + 1] = __uint_as_float(w[2 * h + 1]);
-      } else if constexpr (DT == GEMM_F16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-        x[2 * h] = f.x, x[2 * h + 1] = f.y;
-      } else {
-        x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
-      }
+      if constexpr (DT == GEMM_F32) x[2 * h] = __uint_as_float(w[2 * h]), x[2 * h + 1] = __uint_as_float(w[2 * h + 1]);
+      else unpack2<DT>(w[h], x[2 * h], x[2 * h + 1]);
     }
   }
 };
@@ -111,10 +105,7 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int64_t n, bool vec, 
       st_row_32b(static_cast<float*>(p) + i, w);
     } else {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        if constexpr (DT == GEMM_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
-        else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
-      }
+      for (int h = 0; h < 4; ++h) w[h] = pack2<DT>(x[2 * h], x[2 * h + 1]);
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   } else {

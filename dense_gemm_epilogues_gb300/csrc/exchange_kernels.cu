@@ -48,16 +48,12 @@ struct Piece {
     for (int h = 0; h < (WIDE ? 4 : 1); ++h) w[h] = 0u;
   }
   __device__ __forceinline__ void get(float (&x)[N]) const {
+    if constexpr (!WIDE || DT == GEMM_F32) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      if constexpr (!WIDE || DT == GEMM_F32) {
-        x[k] = __uint_as_float(w[k]);
-      } else if constexpr (DT == GEMM_F16) {
-        const __half2 h = *reinterpret_cast<const __half2*>(&w[k / 2]);
-        x[k] = k % 2 ? __high2float(h) : __low2float(h);
-      } else {
-        x[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
-      }
+      for (int k = 0; k < N; ++k) x[k] = __uint_as_float(w[k]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < N / 2; ++h) unpack2<DT>(w[h], x[2 * h], x[2 * h + 1]);
     }
   }
   __device__ __forceinline__ void set(const float (&x)[N]) {
@@ -66,10 +62,7 @@ struct Piece {
       for (int k = 0; k < N; ++k) w[k] = __float_as_uint(x[k]);
     } else {
 #pragma unroll
-      for (int h = 0; h < N / 2; ++h) {
-        if constexpr (DT == GEMM_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
-        else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
-      }
+      for (int h = 0; h < N / 2; ++h) w[h] = pack2<DT>(x[2 * h], x[2 * h + 1]);
     }
   }
 };

@@ -37,26 +37,6 @@ constexpr int A_BYTES = 128 * TC_BK * 2;           // 16 KiB: 128 columns of wei
 constexpr uint32_t MN_BOX_BYTES = 64 * TC_BK * 2;  // MN-major box: 64 columns, 64 deep
 constexpr int MAX_STAGES = 8;
 
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t user_timeout_ns) {
-  const uint64_t timeout_ns = user_timeout_ns > 1000000000ull ? user_timeout_ns : 1000000000ull;
-  if (mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer_ns() - t0 > timeout_ns) return;
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "elect.sync _|p, 0xffffffff;\n"
-      "selp.u32 %0, 1, 0, p;\n"
-      "}\n"
-      : "=r"(one));
-  return one != 0;
-}
-
 // A limit below a microsecond, the step of the timer and less than the hardware may suspend a
 // try for, gives a wait one look: these loads mostly land within a single try, which no limit
 // would ever end.
@@ -102,14 +82,7 @@ __device__ __forceinline__ void load4(const void* p, int64_t i, int n, bool vec,
       const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
       const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (DT == GEMM_F16) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-          x[2 * h] = f.x, x[2 * h + 1] = f.y;
-        } else {
-          x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
-        }
-      }
+      for (int h = 0; h < 2; ++h) unpack2<DT>(w[h], x[2 * h], x[2 * h + 1]);
     }
   } else {
 #pragma unroll
@@ -124,10 +97,7 @@ __device__ __forceinline__ void store4(void* p, int64_t i, int n, bool vec, cons
     } else {
       uint32_t w[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (DT == GEMM_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
-        else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(x[2 * h + 1]), "f"(x[2 * h]));
-      }
+      for (int h = 0; h < 2; ++h) w[h] = pack2<DT>(x[2 * h], x[2 * h + 1]);
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(w[0], w[1]);
     }
   } else {
@@ -357,14 +327,7 @@ template <int DT>
 __device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    if constexpr (DT == GEMM_F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-      x[2 * h] = f.x, x[2 * h + 1] = f.y;
-    } else {
-      x[2 * h] = __uint_as_float(w[h] << 16), x[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
-    }
-  }
+  for (int h = 0; h < 4; ++h) unpack2<DT>(w[h], x[2 * h], x[2 * h + 1]);
 }
 
 // Grid: (256-column strips, row blocks).  A lane copies its pieces of four rows ahead into
@@ -410,10 +373,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 4) act_grad_kernel(const __grid_
         copy(r + GRAD_STAGES * GRAD_WARPS, stage);
         activate_grad<ACT>(z, g);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {   // (dz's rows are padded to whole pieces; what lies past N is 0)
-          if constexpr (DT == GEMM_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(g[2 * h + 1]), "f"(g[2 * h]));
-          else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(g[2 * h + 1]), "f"(g[2 * h]));
-        }
+        for (int h = 0; h < 4; ++h)   // (dz's rows are padded to whole pieces; what lies past N is 0)
+          w[h] = pack2<DT>(g[2 * h], g[2 * h + 1]);
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dz) + r * p.ldz + c) = make_uint4(w[0], w[1], w[2], w[3]);
       } else {
         copy(r + GRAD_STAGES * GRAD_WARPS, stage);

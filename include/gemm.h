@@ -658,8 +658,9 @@ typedef struct {
  *   epi         NULL: none of it, D of the plan's ab_dtype.
  * Any sizes, alignments and pitches; operands that TMA cannot address cost a copy into the
  * plan's scratch.  K == 0 gives act(bias) + residual.  D may be the residual, but must not
- * overlap A, B or pre, nor pre the inputs (the same address is GEMM_ERR_INVALID_ARG).  Where few rows give few tiles (a decoding step), up to eight CTAs
- * of a cluster share a tile's K (gemm_config_t.split_k); the sum has one order all the same.
+ * overlap A, B or pre, nor pre the inputs (the same address is GEMM_ERR_INVALID_ARG).
+ * Where few rows give few tiles (a decoding step), up to eight CTAs of a cluster share a
+ * tile's K (gemm_config_t.split_k); the sum has one order all the same.
  * ------------------------------------------------------------------------- */
 gemm_status_t gemm_run_linear(gemm_plan_t plan, gemm_layout_t layoutB, int64_t M, int64_t N, int64_t K, const void* A,
                               int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd, const gemm_linear_t* epi,
@@ -673,10 +674,10 @@ gemm_status_t gemm_run_linear(gemm_plan_t plan, gemm_layout_t layoutB, int64_t M
  *   dA          row-major M x K of the plan's ab_dtype, or NULL: not wanted (B is not read).
  *   dB          K x N in layoutB (B's own), of db_dtype F32, F16 or BF16, or NULL (A is not read).
  *   dbias       N fp32 entries, or NULL.
- * dZ is rounded to the operands' type for the two products, as the tensor cores take it (half a
- * step of every term), and summed unrounded, in fp32, for dbias.  It takes M x N entries of the plan's scratch (none
- * without an activation).  M == 0 gives zeros.  The outputs must not overlap the inputs (the
- * same address is GEMM_ERR_INVALID_ARG).
+ * dZ is rounded to the operands' type for the two products, as the tensor cores take it
+ * (half a step of every term), and summed unrounded, in fp32, for dbias.  It takes M x N
+ * entries of the plan's scratch (none without an activation).  M == 0 gives zeros.  The
+ * outputs must not overlap the inputs (the same address is GEMM_ERR_INVALID_ARG).
  * ------------------------------------------------------------------------- */
 gemm_status_t gemm_run_linear_grad(gemm_plan_t plan, gemm_layout_t layoutB, int64_t M, int64_t N, int64_t K,
                                    const void* dY, int64_t lddy, const void* pre, int64_t ldp, gemm_linear_act_t act,
